@@ -515,3 +515,172 @@ def dist_sampler_indices_from(n_items: int, n_replicas: int, rank: int, seed: in
 
 
 __all__ += ["dist_sampler_indices_from"]
+
+
+# ---------------------------------------------------------------- operators of a distillation step
+
+DISTILL_MAX_TOP = 1024
+_i32, _i64, _f32 = _c.c_int32, _c.c_int64, _c.c_float
+_lib.rmsnorm_forward.argtypes = [_P, _i64, _P, _i64, _i32, _P, _i64, _i32, _f32, _P, _i64, _P, _i64, _i32, _P, _P]
+_lib.rmsnorm_forward.restype = _c.c_int
+_lib.rmsnorm_forward_q8.argtypes = [_P, _i64, _P, _i64, _i32, _P, _i64, _i32, _f32, _P, _i64, _P, _i64, _P, _P, _P]
+_lib.rmsnorm_forward_q8.restype = _c.c_int
+_lib.rmsnorm_backward_workspace_bytes.argtypes = [_i64, _i32]
+_lib.rmsnorm_backward_workspace_bytes.restype = _c.c_size_t
+_lib.rmsnorm_backward.argtypes = [_P, _i64, _i32, _P, _i64, _i32, _P, _P, _P, _i64, _i64, _i32, _P, _i64, _P, _P,
+                                  _c.c_size_t, _P]
+_lib.rmsnorm_backward.restype = _c.c_int
+_lib.q8_matmul_workspace_bytes.argtypes = [_i64, _i64, _i32]
+_lib.q8_matmul_workspace_bytes.restype = _c.c_size_t
+_lib.q8_matmul.argtypes = [_P, _i64, _P, _P, _i64, _P, _i64, _i64, _i32, _P, _i64, _i32, _P, _c.c_size_t, _P]
+_lib.q8_matmul.restype = _c.c_int
+_DISTILL_ARGS = [_P, _i64, _i32, _P, _i64, _i32, _P, _i64, _i32, _i64, _i32, _i32, _f32]
+_lib.distill_topk_forward.argtypes = _DISTILL_ARGS + [_P, _P, _P]
+_lib.distill_topk_forward.restype = _c.c_int
+_lib.distill_topk_backward.argtypes = _DISTILL_ARGS + [_P, _P, _P, _i64, _P]
+_lib.distill_topk_backward.restype = _c.c_int
+_lib.distill_topk_forward_backward.argtypes = _DISTILL_ARGS + [_P, _P, _P, _P, _i64, _P]
+_lib.distill_topk_forward_backward.restype = _c.c_int
+
+
+def _mat(t, name: str, shape=None, dtype=None):
+    """(address, leading dimension) of a 2-D row-major tensor; None -> (NULL, 0)."""
+    if t is None:
+        return None, 0
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name}: need a 2-D tensor with unit column stride")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, need {tuple(shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, need {dtype}")
+    return t.data_ptr(), t.stride(0)
+
+
+def _vec(t, name: str, n: int):
+    """Address of a contiguous float32 vector of n elements; None -> NULL."""
+    if t is None:
+        return None
+    import torch
+    if t.dtype != torch.float32:
+        raise TypeError(f"{name}: dtype {t.dtype}, need torch.float32")
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name}: need {n} contiguous elements")
+    return t.data_ptr()
+
+
+def _bytes(ws) -> int:
+    return 0 if ws is None else ws.numel() * ws.element_size()
+
+
+def rmsnorm_forward(x, gamma, y, eps: float = 1e-6, residual=None, h_out=None, rstd_out=None, stream=None) -> None:
+    """y = h * rstd * gamma with h = x + residual, rstd = 1/sqrt(mean(h^2) + eps) per row of [rows, D] matrices
+    (fp32 or bf16, row strides as they are); h_out receives the sum, rstd_out (float32 [rows]) the statistics."""
+    rows, D = x.shape
+    px, ldx = _mat(x, "x")
+    pr, ldr = _mat(residual, "residual", x.shape, x.dtype)
+    ph, ldh = _mat(h_out, "h_out", x.shape, x.dtype)
+    py, ldy = _mat(y, "y", x.shape)
+    _check(_lib.rmsnorm_forward(px, ldx, pr, ldr, _dtype_code(x), _vec(gamma, "gamma", D), rows, D, eps, ph, ldh,
+                                py, ldy, _dtype_code(y), _vec(rstd_out, "rstd_out", rows), _stream_ptr(stream)),
+           "rmsnorm_forward")
+
+
+def rmsnorm_forward_q8(x, gamma, q, scale, eps: float = 1e-6, residual=None, h_out=None, rstd_out=None,
+                       stream=None) -> None:
+    """rmsnorm_forward with its output in 8 bits: q (int8 [rows, D]) times scale (float32 [rows]) stands for y."""
+    import torch
+    rows, D = x.shape
+    px, ldx = _mat(x, "x")
+    pr, ldr = _mat(residual, "residual", x.shape, x.dtype)
+    ph, ldh = _mat(h_out, "h_out", x.shape, x.dtype)
+    pq, ldq = _mat(q, "q", x.shape, torch.int8)
+    _check(_lib.rmsnorm_forward_q8(px, ldx, pr, ldr, _dtype_code(x), _vec(gamma, "gamma", D), rows, D, eps, ph, ldh,
+                                   pq, ldq, _vec(scale, "scale", rows), _vec(rstd_out, "rstd_out", rows),
+                                   _stream_ptr(stream)),
+           "rmsnorm_forward_q8")
+
+
+def rmsnorm_backward_workspace_bytes(rows: int, D: int) -> int:
+    return int(_lib.rmsnorm_backward_workspace_bytes(rows, D))
+
+
+def rmsnorm_backward(dy, h, rstd, gamma, dx, dgamma=None, workspace=None, dh=None, stream=None) -> None:
+    """Gradient of rmsnorm_forward: dx (of x and of residual alike; dh is what reaches h by other ways) and dgamma
+    (float32 [D]; needs a workspace of rmsnorm_backward_workspace_bytes(rows, D) bytes)."""
+    rows, D = h.shape
+    ph, ldh = _mat(h, "h")
+    py, ldy = _mat(dy, "dy", h.shape)
+    pd, ldd = _mat(dh, "dh", h.shape, h.dtype)
+    po, ldo = _mat(dx, "dx", h.shape, h.dtype)
+    _check(_lib.rmsnorm_backward(py, ldy, _dtype_code(dy), ph, ldh, _dtype_code(h), _vec(rstd, "rstd", rows),
+                                 _vec(gamma, "gamma", D), pd, ldd, rows, D, po, ldo, _vec(dgamma, "dgamma", D),
+                                 _ptr(workspace), _bytes(workspace), _stream_ptr(stream)),
+           "rmsnorm_backward")
+
+
+def q8_matmul_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int(_lib.q8_matmul_workspace_bytes(M, N, K))
+
+
+def q8_matmul(a, a_scale, w, w_scale, out, workspace, stream=None) -> None:
+    """out[m, n] = (sum_k a[m, k] * w[n, k]) * a_scale[m] * w_scale[n]: int8 tokens a [M, K] and channels w [N, K],
+    float32 scales, out [M, N] fp32 or bf16; workspace of q8_matmul_workspace_bytes(M, N, K) bytes."""
+    import torch
+    M, K = a.shape
+    pa, lda = _mat(a, "a", None, torch.int8)
+    pw, ldw = _mat(w, "w", None, torch.int8)
+    if w.shape[1] != K:
+        raise ValueError(f"w: shape {tuple(w.shape)}, need [N, {K}]")
+    N = w.shape[0]
+    po, ldo = _mat(out, "out", (M, N))
+    _check(_lib.q8_matmul(pa, lda, _vec(a_scale, "a_scale", M), pw, ldw, _vec(w_scale, "w_scale", N), M, N, K, po, ldo,
+                          _dtype_code(out), _ptr(workspace), _bytes(workspace), _stream_ptr(stream)),
+           "q8_matmul")
+
+
+def _distill_args(logits, index, teacher, temperature):
+    import torch
+    T, V = logits.shape
+    pz, ldz = _mat(logits, "logits")
+    pi, ldi = _mat(index, "index")
+    if index.dtype not in (torch.int32, torch.int64):
+        raise TypeError(f"index: dtype {index.dtype}, need torch.int32 or torch.int64")
+    k = index.shape[1]
+    if index.shape[0] != T:
+        raise ValueError(f"index: shape {tuple(index.shape)}, need [{T}, k]")
+    pt, ldt = _mat(teacher, "teacher", index.shape)
+    return T, (pz, ldz, _dtype_code(logits), pi, ldi, 8 * index.element_size(), pt, ldt, _dtype_code(teacher), T, V, k,
+               temperature)
+
+
+def distill_topk_forward(logits, index, teacher, loss, lse=None, temperature: float = 1.0, stream=None) -> None:
+    """loss[t] = temperature^2 * KL(p || q): p the softmax of the teacher's entries teacher [T, k] at index [T, k]
+    (an index outside the vocabulary is no entry), q that of logits [T, V], both at the temperature; loss and lse
+    are float32 [T]."""
+    T, args = _distill_args(logits, index, teacher, temperature)
+    _check(_lib.distill_topk_forward(*args, _vec(loss, "loss", T), _vec(lse, "lse", T), _stream_ptr(stream)),
+           "distill_topk_forward")
+
+
+def distill_topk_backward(logits, index, teacher, lse, dloss, dlogits, temperature: float = 1.0, stream=None) -> None:
+    """Gradient of distill_topk_forward's loss (dloss float32 [T], or None for 1) into dlogits (may be logits)."""
+    T, args = _distill_args(logits, index, teacher, temperature)
+    pd, ldd = _mat(dlogits, "dlogits", logits.shape, logits.dtype)
+    _check(_lib.distill_topk_backward(*args, _vec(lse, "lse", T), _vec(dloss, "dloss", T), pd, ldd,
+                                      _stream_ptr(stream)),
+           "distill_topk_backward")
+
+
+def distill_topk_forward_backward(logits, index, teacher, dloss, loss, lse, dlogits, temperature: float = 1.0,
+                                  stream=None) -> None:
+    """Loss and gradient in one pass, for a training step that knows dloss beforehand."""
+    T, args = _distill_args(logits, index, teacher, temperature)
+    pd, ldd = _mat(dlogits, "dlogits", logits.shape, logits.dtype)
+    _check(_lib.distill_topk_forward_backward(*args, _vec(dloss, "dloss", T), _vec(loss, "loss", T),
+                                              _vec(lse, "lse", T), pd, ldd, _stream_ptr(stream)),
+           "distill_topk_forward_backward")
+
+
+__all__ += ["rmsnorm_forward", "rmsnorm_forward_q8", "rmsnorm_backward_workspace_bytes", "rmsnorm_backward",
+            "q8_matmul_workspace_bytes", "q8_matmul", "distill_topk_forward", "distill_topk_backward",
+            "distill_topk_forward_backward", "DISTILL_MAX_TOP"]

@@ -1,0 +1,109 @@
+// Shared by the row operators (RMS norm, 8-bit product, distillation loss):
+// rows of a strided matrix read and written as fp32, CTA reductions, and the
+// host's checks of matrices against one another.
+#pragma once
+
+#include <cstdint>
+
+#include "common.cuh"
+#include "host_common.h"
+
+namespace ddp {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+template <bool BF16>
+__device__ __forceinline__ void store_elem(void* base, int64_t e, float v) {
+    if constexpr (BF16) reinterpret_cast<__nv_bfloat16*>(base)[e] = __float2bfloat16_rn(v);
+    else reinterpret_cast<float*>(base)[e] = v;
+}
+
+// First byte of row `row` of a matrix with `ld` elements between rows.
+template <bool BF16>
+__device__ __forceinline__ const char* row_ptr(const void* base, int64_t row, int64_t ld) {
+    return static_cast<const char*>(base) + row * ld * (BF16 ? 2 : 4);
+}
+template <bool BF16>
+__device__ __forceinline__ char* row_ptr(void* base, int64_t row, int64_t ld) {
+    return static_cast<char*>(base) + row * ld * (BF16 ? 2 : 4);
+}
+
+// Sum / maximum over the CTA, in every thread; MaxOp leaves NaN out (its
+// callers carry NaN through a sum), MaxNanOp carries it.  `sh` holds one float per
+// warp and is free again when the call returns.
+struct SumOp {
+    __device__ __forceinline__ static float id() { return 0.0f; }
+    __device__ __forceinline__ static float f(float a, float b) { return a + b; }
+};
+struct MaxOp {
+    __device__ __forceinline__ static float id() { return -INFINITY; }
+    __device__ __forceinline__ static float f(float a, float b) { return fmaxf(a, b); }
+};
+
+__device__ __forceinline__ float max_nan(float a, float b) {   // NaN if either is
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+struct MaxNanOp {
+    __device__ __forceinline__ static float id() { return -INFINITY; }
+    __device__ __forceinline__ static float f(float a, float b) { return max_nan(a, b); }
+};
+
+template <class Op>
+__device__ __forceinline__ float warp_all(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = Op::f(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+
+template <class Op>
+__device__ __forceinline__ float block_all(float v, float* sh) {
+    v = warp_all<Op>(v);
+    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
+    __syncthreads();
+    const int nw = (blockDim.x + 31) >> 5;
+    float r = (threadIdx.x & 31) < nw ? sh[threadIdx.x & 31] : Op::id();
+    r = warp_all<Op>(r);
+    __syncthreads();
+    return r;
+}
+
+// ---- host: a matrix argument of a call --------------------------------
+
+struct Mat {
+    const void* p;
+    int64_t rows, cols, ld;   // ld in elements
+    int esz;                  // bytes per element
+};
+
+inline bool mat_valid(const Mat& m) {
+    return m.rows >= 0 && m.cols >= 0 && (m.rows <= 1 || m.ld >= m.cols) && m.ld >= 0 && m.ld <= INT64_MAX / 64 &&
+           (m.rows == 0 || m.ld == 0 || m.rows <= INT64_MAX / 64 / m.ld) && m.cols <= INT64_MAX / 64;
+}
+
+inline bool mat_aligned(const Mat& m) { return (reinterpret_cast<uintptr_t>(m.p) & (m.esz - 1)) == 0; }
+
+inline size_t mat_span(const Mat& m) {
+    return m.rows <= 0 || m.cols <= 0 ? 0 : static_cast<size_t>(((m.rows - 1) * m.ld + m.cols) * m.esz);
+}
+
+// Whether two matrices share a byte.  Two column slices of one buffer
+// (the same pitch, disjoint columns) do not; matrices of different pitch
+// whose spans meet are taken to.
+inline bool mats_overlap(const Mat& a, const Mat& b) {
+    if (a.p == nullptr || b.p == nullptr || !overlaps(a.p, mat_span(a), b.p, mat_span(b))) return false;
+    const int64_t pitch = a.ld * a.esz;
+    if (pitch != b.ld * b.esz || pitch == 0 || a.rows <= 1 || b.rows <= 1) return true;
+    const int64_t wa = a.cols * a.esz, wb = b.cols * b.esz;
+    const intptr_t d = reinterpret_cast<intptr_t>(b.p) - reinterpret_cast<intptr_t>(a.p);
+    const int64_t off = ((d % pitch) + pitch) % pitch;   // b's columns start here in a's pitch
+    return off < wa || off + wb > pitch;
+}
+
+inline bool mats_same(const Mat& a, const Mat& b) {
+    return a.p == b.p && a.esz == b.esz && (a.ld == b.ld || a.rows <= 1);
+}
+
+}  // namespace ddp

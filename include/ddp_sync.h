@@ -35,7 +35,8 @@
  *     untouched.  A failed kernel launch returns DDP_ERR_CUDA and the CUDA
  *     error code is available from ddp_last_cuda_error() on the same thread.
  *   - Alignment: every device pointer must be 16-byte aligned
- *     (DDP_ERR_ALIGNMENT otherwise); bucket offsets from ddp_plan_buckets are
+ *     (DDP_ERR_ALIGNMENT otherwise; the operators of a distillation step ask
+ *     for less, see there); bucket offsets from ddp_plan_buckets are
  *     256-byte aligned, so pointers into planned buffers always qualify.
  *   - Replica count: 1 <= n_replicas <= DDP_MAX_REPLICAS.
  *   - Empty requests: with numel == 0 (or an empty sampler list) nothing is
@@ -583,6 +584,143 @@ int dist_sampler_indices_from(int64_t n_items, int32_t n_replicas, int32_t rank,
                               uint64_t seed, uint64_t epoch, int32_t shuffle, int32_t drop_last,
                               int64_t start, int64_t* out, int64_t out_capacity, int64_t* num_samples_out,
                               int32_t* walk_status, void* stream);
+
+/*
+ * ---- Operators of a distillation step ----
+ * What stands around the gradient average when the replicas distil a student
+ * from a teacher that runs in 8 bits: the teacher's RMS norm with its output
+ * in 8 bits and the 8-bit product that reads it; the student's RMS norm,
+ * forward and backward; the loss on the teacher's top logits and its gradient
+ * (the pages name no such operators).
+ *
+ * Matrices are row-major with a leading dimension: element (i, j) lies at
+ * base + i*ld + j, ld >= the row's length (not checked for one row).  Column
+ * slices of a larger matrix are ordinary arguments.  Pointers need the
+ * alignment of their element only; rows on 16-byte boundaries run fastest.
+ * Results do not depend on timing (fixed summation orders, no atomics on
+ * sums).  These entry points use fused multiply-adds.
+ */
+
+/*
+ * rmsnorm_forward — h = x + residual; rstd = 1/sqrt(mean(h^2) + eps);
+ * y = h*rstd*gamma, per row.
+ *   x, residual   device [rows, D], in_dtype; residual may be NULL (h = x)
+ *   gamma         device float[D] or NULL (1)
+ *   eps           >= 0
+ *   h_out         device [rows, D], in_dtype, or NULL: the sum, rounded to
+ *                 in_dtype (statistics and y use it unrounded); may be x or
+ *                 residual itself (same pointer and ld)
+ *   y             device [rows, D], out_dtype; may be x or residual itself
+ *                 when the dtypes match, not h_out
+ *   rstd_out      device float[rows] or NULL (the backward pass reads it)
+ * Sums are fp32.  rows == 0 enqueues nothing.
+ */
+int rmsnorm_forward(const void* x, int64_t ldx, const void* residual, int64_t ldr, int32_t in_dtype,
+                    const float* gamma, int64_t rows, int32_t D, float eps, void* h_out, int64_t ldh,
+                    void* y, int64_t ldy, int32_t out_dtype, float* rstd_out, void* stream);
+
+/*
+ * rmsnorm_forward_q8 — rmsnorm_forward with y as 8-bit integers:
+ *   scale[row] = max|y| / 127,  q = y / scale to the nearest integer (ties to
+ *   even), in [-127, 127].  A row of zeros has scale 0 and zeros; a row that
+ *   is not finite has a scale that is not finite, and zeros.
+ *   q       device int8[rows, D], overlapping nothing else of the call
+ *   scale   device float[rows]
+ */
+int rmsnorm_forward_q8(const void* x, int64_t ldx, const void* residual, int64_t ldr, int32_t in_dtype,
+                       const float* gamma, int64_t rows, int32_t D, float eps, void* h_out, int64_t ldh,
+                       int8_t* q, int64_t ldq, float* scale, float* rstd_out, void* stream);
+
+/* Workspace of rmsnorm_backward (0 for invalid sizes). */
+size_t rmsnorm_backward_workspace_bytes(int64_t rows, int32_t D);
+
+/*
+ * rmsnorm_backward — the gradient of rmsnorm_forward.  With n = h*rstd and
+ * c = mean(dy*gamma*n):
+ *     dx = rstd*(dy*gamma - n*c) + dh      (x and residual have this gradient)
+ *     dgamma = sum over the rows of dy*n
+ *   dy           device [rows, D], dy_dtype: the gradient of y
+ *   h, rstd      what the forward pass wrote (h in h_dtype)
+ *   dh           device [rows, D], h_dtype, or NULL: the gradient that
+ *                reaches h by other ways (the residual stream)
+ *   dx           device [rows, D], h_dtype; may be dy, h or dh itself when
+ *                the dtypes match
+ *   dgamma       device float[D] or NULL (not wanted); written, not added to
+ *   workspace    device buffer of rmsnorm_backward_workspace_bytes(rows, D),
+ *                16-byte aligned, contents ignored on entry (NULL without
+ *                dgamma); overlapping calls need different ones
+ * rows == 0 writes a dgamma of zeros.
+ */
+int rmsnorm_backward(const void* dy, int64_t lddy, int32_t dy_dtype, const void* h, int64_t ldh, int32_t h_dtype,
+                     const float* rstd, const float* gamma, const void* dh, int64_t lddh, int64_t rows, int32_t D,
+                     void* dx, int64_t lddx, float* dgamma, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace of q8_matmul (0 for invalid sizes). */
+size_t q8_matmul_workspace_bytes(int64_t M, int64_t N, int32_t K);
+
+/*
+ * q8_matmul — product of 8-bit integers with a scale for each token and each
+ * channel:  out[m, n] = (sum_k a[m, k]*w[n, k]) * a_scale[m] * w_scale[n]
+ *   a            device int8[M, K] (tokens), a_scale device float[M]
+ *   w            device int8[N, K] (channels), w_scale device float[N]
+ *   out          device [M, N], out_dtype; overlapping nothing of the call
+ *   workspace    device buffer of q8_matmul_workspace_bytes(M, N, K), 16-byte
+ *                aligned, contents ignored on entry; overlapping calls need
+ *                different ones
+ * K <= 131071, M and N < 2^31 (DDP_ERR_UNSUPPORTED beyond).  K == 0 gives
+ * zeros (0*a_scale*w_scale).
+ */
+int q8_matmul(const int8_t* a, int64_t lda, const float* a_scale, const int8_t* w, int64_t ldw,
+              const float* w_scale, int64_t M, int64_t N, int32_t K, void* out, int64_t ldo, int32_t out_dtype,
+              void* workspace, size_t workspace_bytes, void* stream);
+
+#define DDP_DISTILL_MAX_TOP 1024
+
+/*
+ * distill_topk_forward — loss of a student against a teacher's top logits.
+ * Per token, with student logits z[0..V) and the teacher's k entries
+ * (index, logit), at temperature t:
+ *     p = softmax(teacher/t) over the entries whose index lies in [0, V)
+ *     q = softmax(z/t) over the vocabulary, lse = ln(sum exp(z/t))
+ *     loss = t^2 * sum_j p_j (ln p_j - ln q[index_j])
+ *   logits          device [T, V], dtype
+ *   index           device [T, k], int32 or int64 (index_bits 32 or 64);
+ *                   an index outside [0, V) is no entry (pad lists with -1);
+ *                   an index may occur more than once
+ *   teacher         device [T, k], teacher_dtype
+ *   k               0 .. DDP_DISTILL_MAX_TOP (DDP_ERR_UNSUPPORTED beyond)
+ *   temperature     > 0
+ *   loss            device float[T]
+ *   lse             device float[T] or NULL (the backward pass reads it)
+ * A token without entries, or whose entries are all -infinity, has loss 0.
+ * Entries and logits of -infinity have probability 0.
+ */
+int distill_topk_forward(const void* logits, int64_t ldz, int32_t dtype, const void* index, int64_t ldi,
+                         int32_t index_bits, const void* teacher, int64_t ldt, int32_t teacher_dtype, int64_t T,
+                         int32_t V, int32_t k, float temperature, float* loss, float* lse, void* stream);
+
+/*
+ * distill_topk_backward — the gradient of the logits:
+ *     dlogits[v] = dloss*t*(q_v - sum_{j: index_j = v} p_j)
+ *   lse       what the forward pass wrote
+ *   dloss     device float[T] or NULL (1): the gradient of each token's loss;
+ *             a token of dloss 0 (or without entries) has gradient 0,
+ *             whatever its logits hold
+ *   dlogits   device [T, V], dtype; may be logits itself
+ */
+int distill_topk_backward(const void* logits, int64_t ldz, int32_t dtype, const void* index, int64_t ldi,
+                          int32_t index_bits, const void* teacher, int64_t ldt, int32_t teacher_dtype, int64_t T,
+                          int32_t V, int32_t k, float temperature, const float* lse, const float* dloss,
+                          void* dlogits, int64_t lddz, void* stream);
+
+/*
+ * distill_topk_forward_backward — both at once, for a training step that
+ * knows dloss beforehand (a mean over tokens: 1/tokens).
+ */
+int distill_topk_forward_backward(const void* logits, int64_t ldz, int32_t dtype, const void* index, int64_t ldi,
+                                  int32_t index_bits, const void* teacher, int64_t ldt, int32_t teacher_dtype,
+                                  int64_t T, int32_t V, int32_t k, float temperature, const float* dloss,
+                                  float* loss, float* lse, void* dlogits, int64_t lddz, void* stream);
 
 /* Human-readable name of a ddp_status value (static string). */
 const char* ddp_status_string(int status);
