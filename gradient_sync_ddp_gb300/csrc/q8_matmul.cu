@@ -1,57 +1,574 @@
 // Product of 8-bit integers with a scale for each token and each channel:
 //   out[m, n] = (Σ_k a[m, k]·w[n, k]) · a_scale[m] · w_scale[n]
 //
-// The sum is an exact 32-bit integer (K <= 131071 keeps |Σ| < 2^31).
+// Up to kFewTokens tokens: the channels are streamed once and multiplied with
+// dp4a into exact 32-bit integers (few_kernel); bound by HBM.
+//
+// More tokens: GB300's tensor cores run 8-bit integers far below their 16-bit
+// rate, and an 8-bit integer is exact in fp16, as is a product of two in
+// fp32, so the product runs as an fp16 tcgen05 contraction with fp32
+// accumulators (exact while partial sums stay below 2^24, always for
+// K <= 1024; beyond that each 16-wide step of K rounds once).  Computed as
+// its transpose, D[n, m]: channels are the 128-row operand, tokens the wide one.
+//   widen_kernel   tokens to fp16 in the workspace (channels whose rows TMA
+//                  cannot address are repacked there too, still in 8 bits)
+//   tile_kernel    persistent, one CTA per SM, roles by warp:
+//     two producers  TMA: tokens [NT][64] fp16 (128-byte swizzle), channels
+//                    [128][64] int8 (64-byte swizzle), each into its own ring
+//     converters     two warpgroups, a channel row per thread: 64 bytes from
+//                    shared memory, widened in registers, stored to TMEM;
+//                    channels thus cost 8 bits of L2 and shared memory
+//     one issuer     tcgen05.mma, A from TMEM, B from shared memory,
+//                    accumulators [128][NT] fp32 in TMEM, two of them
+//     epilogue       one warpgroup: TMEM -> scales -> out, under the next
+//                    tile's contraction
+// Every wait is bounded; a tile whose wait ran out is written as NaN.
 #include <cstdint>
+
+#include <cuda.h>
+#include <cuda_fp16.h>
 
 #include "rows.cuh"
 
 namespace ddp {
 namespace {
 
-constexpr int kMaxK = 131071;
+constexpr int kMaxK = 131071;     // |Σ| < 2^31
+constexpr int kFewTokens = 8;
+constexpr int kTileN = 128;       // channels per tile: the MMA's rows
+constexpr int kMaxNT = 192;       // tokens per tile: 2 accumulators of 192 columns + 4 channel stages of 32 = 512
+constexpr int kBlockK = 64;
+constexpr int kWStageBytes = kTileN * kBlockK;
+constexpr int kAStages = 4;       // channel stages in TMEM, 32 columns each
+constexpr int kAColumn0 = 2 * kMaxNT;
+constexpr int kMaxStages = 16;
+constexpr int kRingBytes = 200 * 1024;
+constexpr int kTileThreads = 512;
+constexpr uint64_t kWaitNs = 1000000000ull;
 
-struct Q8Params {
+__device__ __forceinline__ uint32_t smem_u32(const void* p) {
+    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ uint64_t global_ns() {
+    uint64_t t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    return t;
+}
+
+// ---- few tokens ---------------------------------------------------------
+
+struct FewParams {
     const int8_t* a;
     const int8_t* w;
     const float* sa;
     const float* sw;
     void* out;
-    int64_t lda, ldw, ldo, M, N;
-    int32_t K;
+    int64_t lda, ldw, ldo, N;
+    int32_t K, M;
+    int32_t w_align, a_align;   // 16, 4 or 1: what the rows' addresses are multiples of
 };
 
-// 32 x 32 outputs per CTA, 32 bytes of K at a time in shared memory, four
-// products per dp4a.
-template <bool BF16>
-__global__ void __launch_bounds__(256) q8_tile_kernel(const __grid_constant__ Q8Params p) {
-    __shared__ int sa[32][9], sw[32][9];
-    pdl_enter();
-    const int64_t m0 = static_cast<int64_t>(blockIdx.y) * 32, n0 = static_cast<int64_t>(blockIdx.x) * 32;
-    const int t = threadIdx.x, row = t >> 3, q = t & 7;
-    int acc[4] = {0, 0, 0, 0};
-    for (int k0 = 0; k0 < p.K; k0 += 32) {
-        uint32_t va = 0, vw = 0;
-        for (int j = 0; j < 4; ++j) {
-            const int k = k0 + 4 * q + j;
-            if (k >= p.K) break;
-            if (m0 + row < p.M) va |= static_cast<uint32_t>(static_cast<uint8_t>(p.a[(m0 + row) * p.lda + k])) << (8 * j);
-            if (n0 + row < p.N) vw |= static_cast<uint32_t>(static_cast<uint8_t>(p.w[(n0 + row) * p.ldw + k])) << (8 * j);
-        }
-        sa[row][q] = static_cast<int>(va);
-        sw[row][q] = static_cast<int>(vw);
-        __syncthreads();
-        for (int j = 0; j < 8; ++j)
-            for (int i = 0; i < 4; ++i) acc[i] = __dp4a(sa[(t >> 5) * 4 + i][j], sw[t & 31][j], acc[i]);
-        __syncthreads();
+// 16 bytes at p of which the first `valid` exist, the others read as 0.
+__device__ __forceinline__ int4 load16(const int8_t* p, int valid, int align) {
+    if (valid >= 16 && align == 16) {
+        const uint4 v = ld16<true>(p);
+        return make_int4(static_cast<int>(v.x), static_cast<int>(v.y), static_cast<int>(v.z), static_cast<int>(v.w));
     }
-    const int64_t n = n0 + (t & 31);
-    for (int i = 0; i < 4; ++i) {
-        const int64_t m = m0 + (t >> 5) * 4 + i;
-        if (m < p.M && n < p.N)
-            store_elem<BF16>(p.out, m * p.ldo + n, static_cast<float>(acc[i]) * p.sa[m] * p.sw[n]);
+    int r[4] = {0, 0, 0, 0};
+    if (valid >= 16 && align == 4) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r[i] = __ldg(reinterpret_cast<const int*>(p) + i);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (i < valid) r[i >> 2] |= static_cast<int>(static_cast<uint32_t>(static_cast<uint8_t>(p[i])) << (8 * (i & 3)));
+    }
+    return make_int4(r[0], r[1], r[2], r[3]);
+}
+
+constexpr int kFewThreads = 256;
+constexpr int kFewChunk = 4096;   // bytes of K of every token in shared memory at a time
+
+// LPR lanes per channel row, R rows per lane group at a time.
+template <int M, int LPR, int R, bool BF16>
+__global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant__ FewParams p) {
+    extern __shared__ int4 tok[];   // [M][chunk / 16]
+    pdl_enter();
+    constexpr int GROUPS = kFewThreads / LPR;
+    const int g = threadIdx.x / LPR, l = threadIdx.x % LPR;
+    const int chunk_vec = min(kFewChunk, (p.K + 15) / 16 * 16) / 16;
+    const bool one_chunk = p.K <= kFewChunk;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * GROUPS * R;
+    for (int64_t n0 = static_cast<int64_t>(blockIdx.x) * GROUPS * R; n0 < p.N; n0 += step) {
+        int acc[R][M] = {};
+        for (int k0 = 0; k0 < p.K; k0 += kFewChunk) {
+            const int kn = min(kFewChunk, p.K - k0), nv = (kn + 15) / 16;
+            if (!one_chunk || n0 == static_cast<int64_t>(blockIdx.x) * GROUPS * R) {
+                __syncthreads();
+                for (int i = threadIdx.x; i < M * nv; i += kFewThreads) {
+                    const int m = i / nv, v = i - m * nv;
+                    tok[m * chunk_vec + v] = load16(p.a + m * p.lda + k0 + 16 * v, kn - 16 * v, p.a_align);
+                }
+                __syncthreads();
+            }
+            for (int v = l; v < nv; v += LPR) {
+                int4 w[R];
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const int64_t n = n0 + g + static_cast<int64_t>(r) * GROUPS;
+                    w[r] = n < p.N ? load16(p.w + n * p.ldw + k0 + 16 * v, kn - 16 * v, p.w_align) : make_int4(0, 0, 0, 0);
+                }
+#pragma unroll
+                for (int m = 0; m < M; ++m) {
+                    const int4 t = tok[m * chunk_vec + v];
+#pragma unroll
+                    for (int r = 0; r < R; ++r) {
+                        acc[r][m] = __dp4a(w[r].x, t.x, acc[r][m]);
+                        acc[r][m] = __dp4a(w[r].y, t.y, acc[r][m]);
+                        acc[r][m] = __dp4a(w[r].z, t.z, acc[r][m]);
+                        acc[r][m] = __dp4a(w[r].w, t.w, acc[r][m]);
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int64_t n = n0 + g + static_cast<int64_t>(r) * GROUPS;
+#pragma unroll
+            for (int m = 0; m < M; ++m) {
+                int s = acc[r][m];
+#pragma unroll
+                for (int o = LPR / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+                if (l == m % LPR && n < p.N)
+                    store_elem<BF16>(p.out, m * p.ldo + n, static_cast<float>(s) * p.sa[m] * p.sw[n]);
+            }
+        }
     }
 }
+
+// ---- tokens to fp16, unaligned channels to a 16-byte pitch ---------------
+
+struct WidenParams {
+    const int8_t* a;
+    __half* x;         // [M][xp]
+    const int8_t* w;
+    int8_t* wr;        // [N][wp] or NULL
+    int64_t lda, ldw, M, N, xp, wp;
+    int32_t K, a_align;
+};
+
+__device__ __forceinline__ void widen4(uint32_t v, uint32_t& lo, uint32_t& hi) {
+    // byte b + 128 behind the exponent of 1024 is fp16 1152 + b; 1152 is exact, so the difference is b
+    const uint32_t u = v ^ 0x80808080u;
+    const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
+    uint32_t l = __byte_perm(u, 0x64646464u, 0x4140), h = __byte_perm(u, 0x64646464u, 0x4342);
+    const __half2 x = __hsub2(*reinterpret_cast<__half2*>(&l), off), y = __hsub2(*reinterpret_cast<__half2*>(&h), off);
+    lo = *reinterpret_cast<const uint32_t*>(&x);
+    hi = *reinterpret_cast<const uint32_t*>(&y);
+}
+
+__global__ void __launch_bounds__(kThreads) widen_kernel(const __grid_constant__ WidenParams p) {
+    pdl_enter();
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * kThreads;
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+    const int64_t av = (p.xp + 15) / 16;
+    for (int64_t i = first; i < p.M * av; i += stride) {
+        const int64_t m = i / av, v = i - m * av;
+        const int4 t = load16(p.a + m * p.lda + 16 * v, static_cast<int>(p.K - 16 * v), p.a_align);
+        uint4 q[2];
+        widen4(t.x, q[0].x, q[0].y);
+        widen4(t.y, q[0].z, q[0].w);
+        widen4(t.z, q[1].x, q[1].y);
+        widen4(t.w, q[1].z, q[1].w);
+        uint4* d = reinterpret_cast<uint4*>(p.x + m * p.xp + 16 * v);
+        d[0] = q[0];
+        if (16 * v + 8 < p.xp) d[1] = q[1];
+    }
+    if (p.wr == nullptr) return;
+    const int64_t wv = p.wp / 16;
+    for (int64_t i = first; i < p.N * wv; i += stride) {
+        const int64_t n = i / wv, v = i - n * wv;
+        *reinterpret_cast<int4*>(p.wr + n * p.wp + 16 * v) = load16(p.w + n * p.ldw + 16 * v, static_cast<int>(p.K - 16 * v), 1);
+    }
+}
+
+// ---- tensor core tiles ---------------------------------------------------
+
+struct TileParams {
+    CUtensorMap tx, tw;
+    const float* sa;
+    const float* sw;
+    void* out;
+    int64_t ldo;
+    int32_t M, N, kblocks, nt, m_tiles, n_tiles, stages;
+};
+
+struct TileShared {
+    uint64_t x_full[kMaxStages], x_empty[kMaxStages], w_full[kMaxStages], w_empty[kMaxStages];
+    uint64_t a_full[kAStages], a_empty[kAStages], d_full[2], d_empty[2], idle;
+    uint32_t tmem;
+    volatile int failed;
+};
+
+__device__ __forceinline__ void bar_init(uint64_t* b, int count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(b)), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint64_t* b) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(b)) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint64_t* b, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(b)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool bar_poll(uint64_t* b, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 100000;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(b)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// Wait for the phase of `parity`; false once a wait of this CTA has run out.
+__device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, TileShared& s) {
+    if (bar_poll(b, parity)) return true;
+    const uint64_t t0 = global_ns();
+    while (!bar_poll(b, parity)) {
+        if (s.failed) return false;
+        if (global_ns() - t0 > kWaitNs) {
+            s.failed = 1;
+            return false;
+        }
+    }
+    return true;
+}
+
+// The same for work of this CTA that is still in flight when it ends, whether or not a wait has run out before.
+__device__ __forceinline__ void bar_drain(uint64_t* b, uint32_t parity, TileShared& s) {
+    const uint64_t t0 = global_ns();
+    while (!bar_poll(b, parity)) {
+        if (global_ns() - t0 > kWaitNs) {
+            s.failed = 1;
+            return;
+        }
+    }
+}
+
+__device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            smem_u32(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// Shared-memory operand, K-major rows of 128 bytes in the 128-byte swizzle: 8-row groups 1024 bytes apart.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr) {
+    return static_cast<uint64_t>((addr >> 4) & 0x3fff) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
+        : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+                 : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, float (&v)[16]) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr)
+        : "memory");
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// Position of a ring: index and phase parity.
+struct Ring {
+    int i = 0;
+    uint32_t ph = 0;
+    __device__ __forceinline__ void next(int n) {
+        if (++i == n) {
+            i = 0;
+            ph ^= 1;
+        }
+    }
+};
+
+template <bool BF16>
+__global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_constant__ TileParams p) {
+    extern __shared__ unsigned char raw[];
+    __shared__ TileShared s;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t pad = (1024u - (smem_u32(raw) & 1023u)) & 1023u;
+    unsigned char* xs = raw + pad;                                   // [stages][nt][128]
+    unsigned char* wsm = xs + p.stages * p.nt * 128;                 // [stages][128][64]
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < p.stages; ++i) {
+            bar_init(&s.x_full[i], 1);
+            bar_init(&s.x_empty[i], 1);
+            bar_init(&s.w_full[i], 1);
+            bar_init(&s.w_empty[i], 4);
+        }
+        for (int i = 0; i < kAStages; ++i) {
+            bar_init(&s.a_full[i], 4);
+            bar_init(&s.a_empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            bar_init(&s.d_full[i], 1);
+            bar_init(&s.d_empty[i], 4);
+        }
+        bar_init(&s.idle, 1);
+        s.failed = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s.tmem)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = s.tmem;
+    pdl_enter();
+    const int tiles = p.m_tiles * p.n_tiles;
+
+    if (warp == 0 && lane == 0) {                       // token producer
+        Ring r;
+        int issued = 0;
+        bool ok = true;
+        for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+            const int m0 = (t % p.m_tiles) * p.nt;
+            for (int kb = 0; kb < p.kblocks; ++kb) {
+                if (!(ok = bar_wait(&s.x_empty[r.i], r.ph ^ 1, s))) break;
+                bar_expect(&s.x_full[r.i], p.nt * 128);
+                tma_load(xs + r.i * p.nt * 128, &p.tx, kb * kBlockK, m0, &s.x_full[r.i]);
+                r.next(p.stages);
+                ++issued;
+            }
+        }
+        // every copy has landed before the CTA gives its shared memory back
+        for (int j = 0; j < p.stages && j < issued; ++j) {
+            if (r.i == 0) r.ph ^= 1;
+            r.i = r.i == 0 ? p.stages - 1 : r.i - 1;
+            bar_drain(&s.x_full[r.i], r.ph, s);
+        }
+    } else if (warp == 2 && lane == 0) {                // channel producer
+        Ring r;
+        int issued = 0;
+        bool ok = true;
+        for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+            const int n0 = (t / p.m_tiles) * kTileN;
+            for (int kb = 0; kb < p.kblocks; ++kb) {
+                if (!(ok = bar_wait(&s.w_empty[r.i], r.ph ^ 1, s))) break;
+                bar_expect(&s.w_full[r.i], kWStageBytes);
+                tma_load(wsm + r.i * kWStageBytes, &p.tw, kb * kBlockK, n0, &s.w_full[r.i]);
+                r.next(p.stages);
+                ++issued;
+            }
+        }
+        for (int j = 0; j < p.stages && j < issued; ++j) {
+            if (r.i == 0) r.ph ^= 1;
+            r.i = r.i == 0 ? p.stages - 1 : r.i - 1;
+            bar_drain(&s.w_full[r.i], r.ph, s);
+        }
+    } else if (warp == 1 && lane == 0) {                // issuer
+        Ring x, a, d;
+        const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(p.nt / 8) << 17) | ((kTileN / 16u) << 24);
+        bool ok = true;
+        for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+            if (!(ok = bar_wait(&s.d_empty[d.i], d.ph ^ 1, s))) break;
+            fence_after();
+            const uint32_t acc = tmem + d.i * kMaxNT;
+            for (int kb = 0; kb < p.kblocks; ++kb) {
+                if (!(ok = bar_wait(&s.x_full[x.i], x.ph, s)) || !(ok = bar_wait(&s.a_full[a.i], a.ph, s))) break;
+                fence_after();
+                const uint64_t desc = smem_desc(smem_u32(xs + x.i * p.nt * 128));
+                const uint32_t at = tmem + kAColumn0 + a.i * 32;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) mma_ts(acc, at + 8 * k, desc + 2 * k, idesc, kb > 0 || k > 0);
+                mma_commit(&s.x_empty[x.i]);
+                mma_commit(&s.a_empty[a.i]);
+                x.next(p.stages);
+                a.next(kAStages);
+            }
+            if (ok) mma_commit(&s.d_full[d.i]);
+            d.next(2);
+        }
+        mma_commit(&s.idle);
+        bar_drain(&s.idle, 0, s);
+    } else if (warp >= 4 && warp < 8) {                 // epilogue
+        Ring d;
+        const int q = warp & 3;
+        for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+            const int m0 = (t % p.m_tiles) * p.nt;
+            const int64_t n = static_cast<int64_t>(t / p.m_tiles) * kTileN + q * 32 + lane;
+            const bool ok = bar_wait(&s.d_full[d.i], d.ph, s) && !s.failed;
+            fence_after();
+            const float swn = n < p.N ? p.sw[n] : 0.0f;
+            const uint32_t acc = tmem + d.i * kMaxNT + (static_cast<uint32_t>(q * 32) << 16);
+            for (int c = 0; c < p.nt; c += 16) {
+                float v[16];
+                __syncwarp();
+                tmem_ld16(acc + c, v);
+                if (c + 16 >= p.nt) {
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(&s.d_empty[d.i]);
+                }
+                if (n < p.N) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const int m = m0 + c + j;
+                        if (m < p.M)
+                            store_elem<BF16>(p.out, m * p.ldo + n, ok ? v[j] * __ldg(p.sa + m) * swn : __int_as_float(0x7fffffff));
+                    }
+                }
+            }
+            d.next(2);
+        }
+    } else if (warp >= 8) {                             // converters: warpgroup g takes every other k block
+        const int g = (warp - 8) >> 2, q = warp & 3, row = q * 32 + lane;
+        Ring w, a;
+        const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
+        int turn = 0;
+        bool ok = true;
+        for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+            for (int kb = 0; kb < p.kblocks; ++kb, turn ^= 1) {
+                if (turn == g) {
+                    if (!(ok = __all_sync(0xffffffffu, bar_wait(&s.w_full[w.i], w.ph, s)))) break;
+                    const unsigned char* src = wsm + w.i * kWStageBytes + row * kBlockK;
+                    uint32_t r[32];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const int4 v = *reinterpret_cast<const int4*>(src + ((c ^ ((row >> 1) & 3)) << 4));
+                        widen4(v.x, r[8 * c], r[8 * c + 1]);
+                        widen4(v.y, r[8 * c + 2], r[8 * c + 3]);
+                        widen4(v.z, r[8 * c + 4], r[8 * c + 5]);
+                        widen4(v.w, r[8 * c + 6], r[8 * c + 7]);
+                    }
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(&s.w_empty[w.i]);
+                    if (!(ok = __all_sync(0xffffffffu, bar_wait(&s.a_empty[a.i], a.ph ^ 1, s)))) break;
+                    fence_after();
+                    tmem_st32(tmem + kAColumn0 + a.i * 32 + lane_base, r);
+                    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(&s.a_full[a.i]);
+                }
+                w.next(p.stages);
+                a.next(kAStages);
+            }
+        }
+    }
+    __syncwarp();
+    fence_before();
+    __syncthreads();
+    fence_after();
+    if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+// ---- host ----------------------------------------------------------------
+
+int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+    static EncodeFn fn = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &r) != cudaSuccess ||
+            r != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<EncodeFn>(f);
+    }();
+    return fn;
+}
+
+int encode(CUtensorMap* map, CUtensorMapDataType type, const void* base, int64_t cols, int64_t rows,
+           int64_t pitch_bytes, int box_cols, int box_rows, CUtensorMapSwizzle swizzle) {
+    EncodeFn fn = encode_fn();
+    if (fn == nullptr) return DDP_ERR_UNSUPPORTED;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch_bytes)};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows)}, one[2] = {1, 1};
+    const CUresult r = fn(map, type, 2, const_cast<void*>(base), dims, strides, box, one,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? DDP_OK : cuda_fail(cudaErrorInvalidValue);
+}
+
+// Launch with dynamic shared memory, programmatic stream serialisation allowed (the kernels begin with pdl_enter()).
+template <typename Params>
+int launch_smem(void (*kernel)(Params), unsigned grid, int block, size_t smem, cudaStream_t s, const Params& params) {
+    cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return cuda_fail(e);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(static_cast<unsigned>(block));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if ((e = cudaLaunchKernelEx(&cfg, kernel, params)) != cudaSuccess) return cuda_fail(e);
+    return check_launch();
+}
+
+template <int LPR, int R, bool BF16>
+void (*few_by_tokens(int M))(FewParams) {
+    switch (M) {
+        case 1: return few_kernel<1, LPR, R, BF16>;
+        case 2: return few_kernel<2, LPR, R, BF16>;
+        case 3: return few_kernel<3, LPR, R, BF16>;
+        case 4: return few_kernel<4, LPR, R, BF16>;
+        case 5: return few_kernel<5, LPR, R, BF16>;
+        case 6: return few_kernel<6, LPR, R, BF16>;
+        case 7: return few_kernel<7, LPR, R, BF16>;
+        default: return few_kernel<8, LPR, R, BF16>;
+    }
+}
+
+int row_align(const void* p, int64_t ld, int64_t rows) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p) | (rows > 1 ? static_cast<uintptr_t>(ld) : 0);
+    return a % 16 == 0 ? 16 : a % 4 == 0 ? 4 : 1;
+}
+
+// Channels whose rows are not on 16-byte boundaries are repacked for TMA; the
+// workspace keeps room for that, so that it depends on the sizes alone.
+int64_t token_pitch(int32_t K) { return round_up(K, 8); }
+int64_t channel_pitch(int32_t K) { return round_up(K, 16); }
+size_t token_bytes(int64_t M, int32_t K) { return static_cast<size_t>(round_up(M * token_pitch(K) * 2, 256)); }
 
 }  // namespace
 }  // namespace ddp
@@ -59,7 +576,9 @@ __global__ void __launch_bounds__(256) q8_tile_kernel(const __grid_constant__ Q8
 using namespace ddp;
 
 extern "C" size_t q8_matmul_workspace_bytes(int64_t M, int64_t N, int32_t K) {
-    return M < 0 || N < 0 || K < 0 || K > kMaxK ? 0 : 16;
+    if (M < 0 || N < 0 || K < 0 || K > kMaxK || M > INT32_MAX || N > INT32_MAX) return 0;
+    if (M <= kFewTokens || N == 0 || K == 0) return 16;
+    return token_bytes(M, K) + static_cast<size_t>(N * channel_pitch(K));
 }
 
 extern "C" int q8_matmul(const int8_t* a, int64_t lda, const float* a_scale, const int8_t* w, int64_t ldw,
@@ -70,7 +589,7 @@ extern "C" int q8_matmul(const int8_t* a, int64_t lda, const float* a_scale, con
     const Mat ma{a, M, K, lda, 1}, mw{w, N, K, ldw, 1}, mo{out, M, N, ldo, out_dtype == DDP_BF16 ? 2 : 4},
         msa{a_scale, 1, M, M, 4}, msw{w_scale, 1, N, N, 4};
     if (!mat_valid(ma) || !mat_valid(mw) || !mat_valid(mo)) return DDP_ERR_INVALID_ARG;
-    if (M > 0 && N > 0 && (out == nullptr || a_scale == nullptr || w_scale == nullptr ||
+    if (M > 0 && N > 0 && (out == nullptr || a_scale == nullptr || w_scale == nullptr || workspace == nullptr ||
                            (K > 0 && (a == nullptr || w == nullptr))))
         return DDP_ERR_INVALID_ARG;
     const size_t need = q8_matmul_workspace_bytes(M, N, K);
@@ -81,12 +600,67 @@ extern "C" int q8_matmul(const int8_t* a, int64_t lda, const float* a_scale, con
         if (mats_overlap(mo, *i) || mats_overlap(ws, *i)) return DDP_ERR_INVALID_ARG;
     if (mats_overlap(mo, ws)) return DDP_ERR_INVALID_ARG;
     if (M == 0 || N == 0) return DDP_OK;
-    if (workspace == nullptr) return DDP_ERR_INVALID_ARG;
     if (!aligned16(workspace)) return DDP_ERR_ALIGNMENT;
     if (workspace_bytes < need) return DDP_ERR_CAPACITY;
-    const Q8Params p{a, w, a_scale, w_scale, out, lda, ldw, ldo, M, N, K};
-    if ((M + 31) / 32 > 65535) return DDP_ERR_UNSUPPORTED;
-    void (*kernel)(Q8Params) = out_dtype == DDP_BF16 ? q8_tile_kernel<true> : q8_tile_kernel<false>;
-    return launch_pdl(kernel, dim3(static_cast<unsigned>((N + 31) / 32), static_cast<unsigned>((M + 31) / 32)), 256,
-                      static_cast<cudaStream_t>(stream), p);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool bf16 = out_dtype == DDP_BF16;
+    DeviceInfo d;
+    int st = current_device_info(&d);
+    if (st != DDP_OK) return st;
+
+    if (M <= kFewTokens || K == 0) {
+        // K == 0 takes the same path in slices of kFewTokens tokens: nothing is summed
+        for (int64_t m = 0; m < M; m += kFewTokens) {
+            const int32_t rows = static_cast<int32_t>(M - m < kFewTokens ? M - m : kFewTokens);
+            const FewParams p{a ? a + m * lda : nullptr, w, a_scale + m, w_scale,
+                              static_cast<char*>(out) + m * ldo * (bf16 ? 2 : 4), lda, ldw, ldo, N, K, rows,
+                              row_align(w, ldw, N), row_align(a ? a + m * lda : nullptr, lda, rows)};
+            constexpr int LPR = 16, R = 2;
+            const int64_t rows_per_cta = kFewThreads / LPR * R;
+            const int64_t need_ctas = (N + rows_per_cta - 1) / rows_per_cta, cap = 8ll * d.sm_count;
+            const int64_t kc = K < kFewChunk ? round_up(K, 16) : kFewChunk;
+            st = launch_smem(bf16 ? few_by_tokens<LPR, R, true>(rows) : few_by_tokens<LPR, R, false>(rows),
+                             static_cast<unsigned>(need_ctas < cap ? need_ctas : cap), kFewThreads,
+                             static_cast<size_t>(rows * kc), s, p);
+            if (st != DDP_OK) return st;
+        }
+        return DDP_OK;
+    }
+
+    __half* x = static_cast<__half*>(workspace);
+    int8_t* wr = static_cast<int8_t*>(workspace) + token_bytes(M, K);
+    const bool repack = row_align(w, ldw, N) != 16 || (N > 1 && ldw >= (1ll << 40)) || (N == 1 && (ldw % 16 != 0 || ldw < K));
+    const int64_t xp = token_pitch(K), wp = channel_pitch(K);
+    const WidenParams wp_{a, x, w, repack ? wr : nullptr, lda, ldw, M, N, xp, wp, K, row_align(a, lda, M)};
+    int64_t vecs = M * ((xp + 15) / 16);
+    if (repack && N * (wp / 16) > vecs) vecs = N * (wp / 16);
+    const int64_t wide = (vecs + kThreads - 1) / kThreads, cap = 16ll * d.sm_count;
+    st = launch_pdl(widen_kernel, dim3(static_cast<unsigned>(wide < cap ? wide : cap)), kThreads, s, wp_);
+    if (st != DDP_OK) return st;
+
+    TileParams p{};
+    p.m_tiles = static_cast<int32_t>((M + kMaxNT - 1) / kMaxNT);
+    p.nt = static_cast<int32_t>(round_up((M + p.m_tiles - 1) / p.m_tiles, 16));
+    p.m_tiles = static_cast<int32_t>((M + p.nt - 1) / p.nt);
+    p.n_tiles = static_cast<int32_t>((N + kTileN - 1) / kTileN);
+    if (static_cast<int64_t>(p.m_tiles) * p.n_tiles > INT32_MAX / 2) return DDP_ERR_UNSUPPORTED;
+    p.kblocks = (K + kBlockK - 1) / kBlockK;
+    const int stage = p.nt * 128 + kWStageBytes;
+    p.stages = kRingBytes / stage < kMaxStages ? kRingBytes / stage : kMaxStages;
+    p.M = static_cast<int32_t>(M);
+    p.N = static_cast<int32_t>(N);
+    p.sa = a_scale;
+    p.sw = w_scale;
+    p.out = out;
+    p.ldo = ldo;
+    if ((st = encode(&p.tx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, x, K, M, xp * 2, kBlockK, p.nt,
+                     CU_TENSOR_MAP_SWIZZLE_128B)) != DDP_OK)
+        return st;
+    if ((st = encode(&p.tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, repack ? wr : w, K, N, repack ? wp : ldw, kBlockK, kTileN,
+                     CU_TENSOR_MAP_SWIZZLE_64B)) != DDP_OK)
+        return st;
+    const int tiles = p.m_tiles * p.n_tiles;
+    return launch_smem(bf16 ? tile_kernel<true> : tile_kernel<false>,
+                       static_cast<unsigned>(tiles < d.sm_count ? tiles : d.sm_count), kTileThreads,
+                       static_cast<size_t>(p.stages) * stage + 1024, s, p);
 }
