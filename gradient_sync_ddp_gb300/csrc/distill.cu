@@ -9,6 +9,15 @@
 // (τ² · d(z/τ)/dz = τ).  A token without entries (none in the vocabulary, or
 // all of them -infinity) has loss and gradient 0, and the gradient of one
 // whose dloss is 0 is 0, whatever its logits hold.
+//
+// One launch.  A CTA takes a token (a cluster of CTAs, when tokens are too few
+// to fill the GPU, each a slice of the vocabulary): one pass over z keeps a
+// running maximum and a sum of exponentials per thread; the CTA (cluster)
+// joins them; a second pass writes dz = dloss·τ·q, reading z again while it is
+// still in L2; last, the at most k entries of dz that hold a p are rewritten.
+// HBM sees z once and dz once.  Rows need not start on 16-byte boundaries
+// (an odd vocabulary): a row is its 16-byte vectors and up to 2·(VEC − 1)
+// elements at its ends.
 #include <cstdint>
 
 #include "rows.cuh"
@@ -16,8 +25,13 @@
 namespace ddp {
 namespace {
 
-constexpr int kDistillThreads = 512;
+constexpr int kDistillThreads = 256;
 constexpr int kMaxTop = DDP_DISTILL_MAX_TOP;
+constexpr int kTopPerThread = kMaxTop / kDistillThreads;
+constexpr int kMaxCluster = 8;
+constexpr int kHash = 2 * kMaxTop;
+constexpr int kScanTop = 32;          // up to this many entries repeats are found by scanning all pairs
+constexpr float kFar = 1.0e37f;       // beyond this, z·c may overflow: exponents from (z − max)·c instead
 
 struct DistillParams {
     const void* z;
@@ -31,103 +45,337 @@ struct DistillParams {
     int64_t ldz, ldi, ldt, lddz, T;
     int32_t V, k;
     float tau, c;          // c = log2(e) / τ
+    int32_t t_bf16, i_64, cluster;
 };
 
-// A CTA per token.  All exponentials are powers of two of z·c − M with
-// M = c·max z, so that loss and gradient see differences of logits only.
-template <bool BF16, bool TBF16, bool I64, bool FWD, bool BWD>
-__global__ void __launch_bounds__(kDistillThreads) distill_loop_kernel(const __grid_constant__ DistillParams a) {
-    __shared__ float sh[32];
-    __shared__ int s_idx[kMaxTop];
-    __shared__ float s_p[kMaxTop], s_z[kMaxTop];
-    pdl_enter();
-    for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
-        const void* z = row_ptr<BF16>(a.z, row, a.ldz);
-        // the teacher's entries: p_j, and ln p_j kept as a power of two in registers
-        float tm = -INFINITY;
-        int n_valid = 0;
-        for (int j = threadIdx.x; j < a.k; j += kDistillThreads) {
-            const int64_t e = row * a.ldi + j;
-            const int64_t i = I64 ? static_cast<const int64_t*>(a.index)[e]
-                                  : static_cast<int64_t>(static_cast<const int32_t*>(a.index)[e]);
-            const bool ok = i >= 0 && i < a.V;
-            const float t = load_elem<TBF16>(row_ptr<TBF16>(a.teacher, row, a.ldt), j) * a.c;
-            s_idx[j] = ok ? static_cast<int>(i) : -1;
-            s_p[j] = ok ? t : -INFINITY;
-            s_z[j] = ok ? load_elem<BF16>(z, i) : 0.0f;
-            if (ok) {
-                tm = max_nan(tm, t);
-                n_valid += t == -INFINITY ? 0 : 1;
-            }
-        }
-        const bool some = __syncthreads_or(n_valid) != 0;
-        tm = block_all<MaxNanOp>(tm, sh);
-        float ts = 0.0f;
-        for (int j = threadIdx.x; j < a.k; j += kDistillThreads) ts += some && s_idx[j] >= 0 ? exp2f(s_p[j] - tm) : 0.0f;
-        ts = block_all<SumOp>(ts, sh);
-        const float g = (a.dloss ? a.dloss[row] : 1.0f) * a.tau;
-        const bool zero = !some || g == 0.0f;
+// 2^x; results under 2^-126 are 0.
+__device__ __forceinline__ float pow2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
 
-        float M = 0.0f, ls = 0.0f;   // q_v = 2^(z·c − M − ls)
-        if constexpr (FWD) {
-            float m = -INFINITY;
-            for (int v = threadIdx.x; v < a.V; v += kDistillThreads) m = fmaxf(m, load_elem<BF16>(z, v));
-            m = block_all<MaxOp>(m, sh);
-            M = m == -INFINITY ? 0.0f : m * a.c;
-            float s = 0.0f;
-            for (int v = threadIdx.x; v < a.V; v += kDistillThreads) s += exp2f(fmaf(load_elem<BF16>(z, v), a.c, -M));
-            s = block_all<SumOp>(s, sh);
-            ls = log2f(s);
-            float l = 0.0f;
-            for (int j = threadIdx.x; j < a.k; j += kDistillThreads) {
-                if (!some || s_idx[j] < 0) continue;
-                const float p = exp2f(s_p[j] - tm) / ts;
-                if (p == 0.0f) continue;
-                l += p * ((s_p[j] - tm) - log2f(ts) - (fmaf(s_z[j], a.c, -M) - ls));
-            }
-            l = block_all<SumOp>(l, sh);
-            if (threadIdx.x == 0) {
-                a.loss[row] = some ? l * kLn2 * a.tau * a.tau : 0.0f;
-                if (a.lse) a.lse[row] = (M + ls) * kLn2;
-            }
-        } else {
-            M = a.lse_in[row] * kLog2e;
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float cluster_read(const float* p, uint32_t rank) {
+    uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(p)), r;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(r) : "memory");
+    return v;
+}
+
+// Two values over the CTA at once, in every thread; `sh` as in block_all.
+template <class OpA, class OpB>
+__device__ __forceinline__ void block_all2(float& a, float& b, float2* sh) {
+    a = warp_all<OpA>(a);
+    b = warp_all<OpB>(b);
+    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = make_float2(a, b);
+    __syncthreads();
+    const bool in = (threadIdx.x & 31) < kDistillThreads / 32;
+    const float2 v = in ? sh[threadIdx.x & 31] : make_float2(OpA::id(), OpB::id());
+    a = warp_all<OpA>(v.x);
+    b = warp_all<OpB>(v.y);
+    __syncthreads();
+}
+
+// Running maximum m of z and Σ 2^(z·c − mc), mc = m·c kept within ±kFar.
+struct Running {
+    float m = -INFINITY, mc = 0.0f, s = 0.0f;
+    __device__ __forceinline__ void raise(float to, float c) {
+        if (to > m) {
+            m = to;
+            const float n = fminf(fmaxf(to * c, -kFar), kFar);
+            s = s == 0.0f ? 0.0f : s * pow2(mc - n);
+            mc = n;
         }
-        if constexpr (BWD) {
-            void* dz = row_ptr<BF16>(a.dz, row, a.lddz);
-            __syncthreads();
-            for (int v = threadIdx.x; v < a.V; v += kDistillThreads)
-                store_elem<BF16>(dz, v, zero ? 0.0f : g * exp2f(fmaf(load_elem<BF16>(z, v), a.c, -M) - ls));
-            __syncthreads();
-            for (int j = threadIdx.x; j < a.k && !zero; j += kDistillThreads) {
-                const int i = s_idx[j];
-                if (i < 0) continue;
-                bool first = true;
-                float p = 0.0f;
-                for (int u = 0; u < a.k; ++u) {
-                    if (s_idx[u] != i) continue;
-                    if (u < j) first = false;
-                    p += exp2f(s_p[u] - tm) / ts;
-                }
-                if (first) store_elem<BF16>(dz, i, g * (exp2f(fmaf(s_z[j], a.c, -M) - ls) - p));
-            }
-        }
-        __syncthreads();
     }
+};
+
+// The slice [v0, v1) of a row, v1 > v0: `lead` elements before its first
+// 16-byte boundary, `nvec` whole vectors, `tail` elements after them.
+struct Slice {
+    const char* base;   // of the row
+    int v0, lead, nvec, tail;
+};
+template <bool BF16>
+__device__ __forceinline__ Slice make_slice(const char* row, int v0, int v1) {
+    constexpr int ES = BF16 ? 2 : 4, VEC = 16 / ES;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(row) + static_cast<uintptr_t>(v0) * ES;
+    Slice s;
+    s.base = row;
+    s.v0 = v0;
+    s.lead = min(static_cast<int>(((16 - (a & 15)) & 15) / ES), v1 - v0);
+    s.nvec = (v1 - v0 - s.lead) / VEC;
+    s.tail = v1 - v0 - s.lead - s.nvec * VEC;
+    return s;
+}
+// Index of the slice's e-th element outside its vectors (e < lead + tail).
+template <bool BF16>
+__device__ __forceinline__ int edge(const Slice& s, int e) {
+    return s.v0 + (e < s.lead ? e : e + s.nvec * (BF16 ? 8 : 4));
+}
+
+// dz = g·2^(exponent) over a slice, the exponent as FAR says.
+template <bool BF16, bool FAR>
+__device__ __forceinline__ void write_grad(const Slice& s, char* dz, float c, float M, float m, float ls, float g) {
+    constexpr int ES = BF16 ? 2 : 4, VEC = 16 / ES, U = 4;
+    const float off = FAR ? ls : M + ls;
+    auto f = [&](float z) { return g * pow2(FAR ? fmaf(z - m, c, -off) : fmaf(z, c, -off)); };
+    const char* zv = s.base + static_cast<int64_t>(s.v0 + s.lead) * ES;
+    char* dv = dz + static_cast<int64_t>(s.v0 + s.lead) * ES;
+    const bool whole = (reinterpret_cast<uintptr_t>(dv) & 15) == 0;
+    for (int i0 = threadIdx.x; i0 < s.nvec; i0 += kDistillThreads * U) {
+        uint4 v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = i0 + u * kDistillThreads;
+            if (i < s.nvec) v[u] = ld16<false>(zv + static_cast<int64_t>(i) * 16);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = i0 + u * kDistillThreads;
+            if (i >= s.nvec) break;
+            float o[VEC];
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) o[e] = f(vec_elem<BF16>(v[u], e));
+            if (whole) {
+                uint4 w;
+                if constexpr (BF16) w = make_uint4(pack2(o[0], o[1]), pack2(o[2], o[3]), pack2(o[4], o[5]), pack2(o[6], o[7]));
+                else w = f4_bits(o[0], o[1], o[2], o[3]);
+                st16(dv + static_cast<int64_t>(i) * 16, w);
+            } else {
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) store_elem<BF16>(dv, static_cast<int64_t>(i) * VEC + e, o[e]);
+            }
+        }
+    }
+    if (threadIdx.x < s.lead + s.tail) {
+        const int v = edge<BF16>(s, threadIdx.x);
+        store_elem<BF16>(dz, v, f(load_elem<BF16>(s.base, v)));
+    }
+}
+
+template <bool BF16>
+__device__ __forceinline__ void write_zero(const Slice& s, char* dz) {
+    constexpr int ES = BF16 ? 2 : 4, VEC = 16 / ES;
+    char* dv = dz + static_cast<int64_t>(s.v0 + s.lead) * ES;
+    const bool whole = (reinterpret_cast<uintptr_t>(dv) & 15) == 0;
+    for (int i = threadIdx.x; i < s.nvec; i += kDistillThreads) {
+        if (whole) {
+            st16(dv + static_cast<int64_t>(i) * 16, make_uint4(0, 0, 0, 0));
+        } else {
+            for (int e = 0; e < VEC; ++e) store_elem<BF16>(dv, static_cast<int64_t>(i) * VEC + e, 0.0f);
+        }
+    }
+    if (threadIdx.x < s.lead + s.tail) store_elem<BF16>(dz, edge<BF16>(s, threadIdx.x), 0.0f);
+}
+
+template <bool BF16, bool FWD, bool BWD>
+__global__ void __launch_bounds__(kDistillThreads) distill_kernel(const __grid_constant__ DistillParams a) {
+    constexpr int ES = BF16 ? 2 : 4, VEC = 16 / ES, U = 4;
+    __shared__ float2 sh[kDistillThreads / 32];
+    __shared__ float s_part[2];                      // this CTA's (m, s), read by its cluster
+    __shared__ int s_idx[kMaxTop];
+    __shared__ float s_p[kMaxTop];
+    __shared__ int s_hash[BWD ? kHash : 1];
+    pdl_enter();
+    const int tid = threadIdx.x;
+    const int64_t row = blockIdx.x / a.cluster;
+    const int rank = blockIdx.x % a.cluster;
+    const char* z = row_ptr<BF16>(a.z, row, a.ldz);
+    // slices of whole 256-byte lines of the row's own grid
+    const int per = ((a.V + a.cluster - 1) / a.cluster + 127) / 128 * 128;
+    const int v0 = min(a.V, rank * per), v1 = min(a.V, v0 + per);
+    const Slice s = make_slice<BF16>(z, v0, v1);
+
+    // the teacher's entries, in registers until the pass over z is done
+    int idx[kTopPerThread];
+    float t[kTopPerThread], zi[kTopPerThread];
+#pragma unroll
+    for (int u = 0; u < kTopPerThread; ++u) {
+        const int j = tid + u * kDistillThreads;
+        idx[u] = -1;
+        t[u] = -INFINITY;
+        zi[u] = 0.0f;
+        if (j >= a.k) continue;
+        const int64_t e = row * a.ldi + j;
+        const int64_t i = a.i_64 ? static_cast<const int64_t*>(a.index)[e]
+                                 : static_cast<int64_t>(static_cast<const int32_t*>(a.index)[e]);
+        if (i < 0 || i >= a.V) continue;
+        idx[u] = static_cast<int>(i);
+        t[u] = a.t_bf16 ? load_elem<true>(row_ptr<true>(a.teacher, row, a.ldt), j)
+                        : load_elem<false>(row_ptr<false>(a.teacher, row, a.ldt), j);
+        // only what this CTA writes or sums: another's slice may hold gradients already
+        if ((FWD && rank == 0) || (i >= v0 && i < v1)) zi[u] = load_elem<BF16>(z, i);
+    }
+
+    Running run;
+    if constexpr (FWD) {
+        const char* zv = z + static_cast<int64_t>(s.v0 + s.lead) * ES;
+        for (int i0 = tid; i0 < s.nvec; i0 += kDistillThreads * U) {
+            uint4 v[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int i = i0 + u * kDistillThreads;
+                if (i < s.nvec) v[u] = ld16_keep(zv + static_cast<int64_t>(i) * 16);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (i0 + u * kDistillThreads >= s.nvec) break;
+                float x[VEC], top = -INFINITY;
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    x[e] = vec_elem<BF16>(v[u], e);
+                    top = fmaxf(top, x[e]);
+                }
+                run.raise(top, a.c);
+                float part = 0.0f;
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) part += pow2(fmaf(x[e], a.c, -run.mc));
+                run.s += part;
+            }
+        }
+        if (tid < s.lead + s.tail) {
+            const float x = load_elem<BF16>(z, edge<BF16>(s, tid));
+            run.raise(x, a.c);
+            run.s += pow2(fmaf(x, a.c, -run.mc));
+        }
+    }
+
+    // maxima of the logits and of the entries, then their sums
+    float m = run.m, tm = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < kTopPerThread; ++u) tm = max_nan(tm, t[u]);
+    block_all2<MaxOp, MaxNanOp>(m, tm, sh);
+    const bool some = !(tm == -INFINITY);
+    float ts = 0.0f;
+#pragma unroll
+    for (int u = 0; u < kTopPerThread; ++u) ts += some && idx[u] >= 0 ? pow2((t[u] - tm) * a.c) : 0.0f;
+    float M = fminf(fmaxf(m * a.c, -kFar), kFar);
+    float sum = run.s == 0.0f ? 0.0f : run.s * pow2(run.mc - M);
+    block_all2<SumOp, SumOp>(sum, ts, sh);
+    if constexpr (FWD) {
+        if (a.cluster > 1) {
+            if (tid == 0) {
+                s_part[0] = m;
+                s_part[1] = sum;
+            }
+            cluster_sync();
+            float pm[kMaxCluster], ps[kMaxCluster];
+            m = -INFINITY;
+#pragma unroll
+            for (int r = 0; r < kMaxCluster; ++r) {
+                pm[r] = r < a.cluster ? cluster_read(&s_part[0], r) : -INFINITY;
+                ps[r] = r < a.cluster ? cluster_read(&s_part[1], r) : 0.0f;
+                m = fmaxf(m, pm[r]);
+            }
+            M = fminf(fmaxf(m * a.c, -kFar), kFar);
+            sum = 0.0f;
+#pragma unroll
+            for (int r = 0; r < kMaxCluster; ++r)
+                sum += ps[r] == 0.0f ? 0.0f : ps[r] * pow2(fminf(fmaxf(pm[r] * a.c, -kFar), kFar) - M);
+        }
+    } else {
+        M = a.lse_in[row] * kLog2e;
+        m = a.lse_in[row] * a.tau;
+    }
+    // Logits whose product with c may overflow (a row that a mask of the type's lowest value leaves whole): differences first.
+    const bool far = !(fabsf(m) * fmaxf(a.c, 1.0f) < kFar) && fabsf(m) < INFINITY;
+    if constexpr (FWD) {
+        if (far) {                                   // rare, and every CTA of the token sums the whole row itself
+            float all = 0.0f, none = 0.0f;
+            for (int v = tid; v < a.V; v += kDistillThreads) all += pow2((load_elem<BF16>(z, v) - m) * a.c);
+            block_all2<SumOp, SumOp>(all, none, sh);
+            sum = all;
+        }
+    }
+    const float ls = FWD ? log2f(sum) : 0.0f;        // q_v = 2^(z·c − M − ls)
+    auto q2 = [&](float x) { return (far ? (x - m) * a.c : fmaf(x, a.c, -M)) - ls; };
+    if constexpr (FWD) {
+        if (rank == 0) {
+            const float lts = log2f(ts);
+            float l = 0.0f, none = 0.0f;
+#pragma unroll
+            for (int u = 0; u < kTopPerThread; ++u) {
+                const float lp = (t[u] - tm) * a.c, p = some && idx[u] >= 0 ? pow2(lp) / ts : 0.0f;
+                if (p != 0.0f) l += p * (lp - lts - q2(zi[u]));
+            }
+            block_all2<SumOp, SumOp>(l, none, sh);
+            if (tid == 0) {
+                a.loss[row] = some ? l * kLn2 * a.tau * a.tau : 0.0f;
+                if (a.lse) a.lse[row] = far ? m / a.tau + ls * kLn2 : (M + ls) * kLn2;
+            }
+        }
+    }
+    if constexpr (BWD) {
+        const float g = (a.dloss ? a.dloss[row] : 1.0f) * a.tau;
+        char* dz = row_ptr<BF16>(a.dz, row, a.lddz);
+        // every read of z beyond this thread's own elements lies before any write: far above re-reads the whole row
+        if (FWD && far && a.cluster > 1) cluster_sync();
+        __syncthreads();
+        if (!some || g == 0.0f) {
+            write_zero<BF16>(s, dz);
+        } else {
+            if (far) write_grad<BF16, true>(s, dz, a.c, M, m, ls, g);
+            else write_grad<BF16, false>(s, dz, a.c, M, m, ls, g);
+            // the entries: p into shared memory, repeated indices found there
+            const bool hash = a.k > kScanTop;
+            if (hash)
+                for (int i = tid; i < kHash; i += kDistillThreads) s_hash[i] = -1;
+#pragma unroll
+            for (int u = 0; u < kTopPerThread; ++u) {
+                const int j = tid + u * kDistillThreads;
+                if (j >= a.k) continue;
+                s_idx[j] = idx[u];
+                s_p[j] = idx[u] >= 0 ? pow2((t[u] - tm) * a.c) / ts : 0.0f;
+            }
+            __syncthreads();
+            bool twice = !hash;
+            if (hash) {
+#pragma unroll
+                for (int u = 0; u < kTopPerThread; ++u) {
+                    if (idx[u] < 0) continue;
+                    for (uint32_t h = (static_cast<uint32_t>(idx[u]) * 2654435761u) >> 21;; h = (h + 1) & (kHash - 1)) {
+                        const int old = atomicCAS(&s_hash[h], -1, idx[u]);
+                        twice |= old == idx[u];
+                        if (old == -1 || old == idx[u]) break;
+                    }
+                }
+                twice = __syncthreads_or(twice);
+            }
+#pragma unroll
+            for (int u = 0; u < kTopPerThread; ++u) {
+                const int j = tid + u * kDistillThreads, i = idx[u];
+                if (i < v0 || i >= v1) continue;     // absent ones are negative
+                float p = twice ? 0.0f : s_p[j];
+                bool first = true;
+                if (twice) {
+                    for (int w = 0; w < a.k; ++w) {
+                        if (s_idx[w] != i) continue;
+                        if (w < j) first = false;
+                        p += s_p[w];
+                    }
+                }
+                if (first) store_elem<BF16>(dz, i, g * (pow2(q2(zi[u])) - p));
+            }
+        }
+    }
+    if (FWD && a.cluster > 1) cluster_sync();        // no CTA ends while another reads its part
 }
 
 bool dtype_ok(int32_t t) { return t == DDP_F32 || t == DDP_BF16; }
 int dsize(int32_t t) { return t == DDP_BF16 ? 2 : 4; }
 
-template <bool BF16, bool TBF16, bool I64>
-void (*pick_dir(bool fwd, bool bwd))(DistillParams) {
-    return fwd ? (bwd ? distill_loop_kernel<BF16, TBF16, I64, true, true> : distill_loop_kernel<BF16, TBF16, I64, true, false>)
-               : distill_loop_kernel<BF16, TBF16, I64, false, true>;
-}
 template <bool BF16>
-void (*pick(bool tb, bool i64, bool fwd, bool bwd))(DistillParams) {
-    return tb ? (i64 ? pick_dir<BF16, true, true>(fwd, bwd) : pick_dir<BF16, true, false>(fwd, bwd))
-              : (i64 ? pick_dir<BF16, false, true>(fwd, bwd) : pick_dir<BF16, false, false>(fwd, bwd));
+void (*pick(bool fwd, bool bwd))(DistillParams) {
+    return fwd ? (bwd ? distill_kernel<BF16, true, true> : distill_kernel<BF16, true, false>) : distill_kernel<BF16, false, true>;
 }
 
 int distill(const void* z, int64_t ldz, int32_t dtype, const void* index, int64_t ldi, int32_t index_bits,
@@ -158,12 +406,30 @@ int distill(const void* z, int64_t ldz, int32_t dtype, const void* index, int64_
         mats_overlap(mle, md))
         return DDP_ERR_INVALID_ARG;
     if (T == 0) return DDP_OK;
-    const DistillParams p{z, index, teacher, lse_in, dloss, loss, lse, dz, ldz, ldi, ldt, lddz, T, V, k, tau, c};
-    void (*kernel)(DistillParams) = dtype == DDP_BF16 ? pick<true>(t_dtype == DDP_BF16, index_bits == 64, fwd, bwd)
-                                                      : pick<false>(t_dtype == DDP_BF16, index_bits == 64, fwd, bwd);
-    const int64_t cap = 1 << 16;
-    return launch_pdl(kernel, dim3(static_cast<unsigned>(T < cap ? T : cap)), kDistillThreads,
-                      static_cast<cudaStream_t>(stream), p);
+    DeviceInfo d;
+    int st = current_device_info(&d);
+    if (st != DDP_OK) return st;
+    // one CTA per token fills the GPU from about two CTAs per SM; fewer tokens are split into slices of at least
+    // 2048 logits each
+    int cluster = 1;
+    while (cluster < kMaxCluster && T * cluster < 2ll * d.sm_count && V / (2 * cluster) >= 2048) cluster *= 2;
+    if (T * cluster > INT32_MAX) return DDP_ERR_UNSUPPORTED;
+    const DistillParams p{z, index, teacher, lse_in, dloss, loss, lse, dz, ldz, ldi, ldt, lddz, T, V, k, tau, c,
+                          t_dtype == DDP_BF16, index_bits == 64, cluster};
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(T * cluster));
+    cfg.blockDim = dim3(kDistillThreads);
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, dtype == DDP_BF16 ? pick<true>(fwd, bwd) : pick<false>(fwd, bwd), p);
+    return e == cudaSuccess ? check_launch() : cuda_fail(e);
 }
 
 }  // namespace

@@ -126,6 +126,24 @@ def test_ragged_lists(g, T, V, k, dt):
             assert not got[2][masked].any()
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("T,V", [(2, 300), (2, 40000), (700, 300)])
+def test_row_masked_whole(g, T, V, dt):
+    """Every logit at the type's lowest value: q is uniform, however large the common value."""
+    z, index, t, up = make(T, V, 3, dt)
+    z[1] = torch.finfo(DT[dt]).min
+    loss, lse, dz = torch.empty(T, device="cuda"), torch.empty(T, device="cuda"), torch.empty_like(z)
+    for tau in (0.5, 1.0, 2.0):
+        g.distill_topk_forward_backward(z, index, t, up, loss, lse, dz, temperature=tau)
+        only = torch.empty_like(loss)
+        g.distill_topk_forward(z, index, t, only, temperature=tau)
+        sync()
+        flat = torch.zeros_like(z[1:2])
+        check(flat, index[1:2], t[1:2], up[1:2], tau, loss[1:2], None, dz[1:2])
+        assert torch.equal(only, loss)
+        check(z, index, t, up, tau, loss, lse, dz, rows=slice(0, 1))
+
+
 def test_zero_weight_and_special_logits(g):
     z, index, t, up = make(5, 700, 8, "f32")
     up[0] = 0.0
