@@ -525,26 +525,6 @@ int encode(CUtensorMap* map, CUtensorMapDataType type, const void* base, int64_t
     return r == CUDA_SUCCESS ? DDP_OK : cuda_fail(cudaErrorInvalidValue);
 }
 
-// Launch with dynamic shared memory, programmatic stream serialisation allowed (the kernels begin with pdl_enter()).
-template <typename Params>
-int launch_smem(void (*kernel)(Params), unsigned grid, int block, size_t smem, cudaStream_t s, const Params& params) {
-    cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return cuda_fail(e);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(static_cast<unsigned>(block));
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if ((e = cudaLaunchKernelEx(&cfg, kernel, params)) != cudaSuccess) return cuda_fail(e);
-    return check_launch();
-}
-
 template <int LPR, int R, bool BF16>
 void (*few_by_tokens(int M))(FewParams) {
     switch (M) {

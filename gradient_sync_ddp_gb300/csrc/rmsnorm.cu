@@ -8,6 +8,17 @@
 //
 // Sums and statistics are fp32; h is rounded to its type only where it is
 // stored, the statistics and y use the unrounded sum.
+//
+// Bound by HBM: forward reads x and residual and writes h and y once,
+// backward reads dy, h and dh and writes dx once.  A row stays in registers
+// between the reduction and the output: a warp per row (narrow rows) or a CTA
+// per row, 16-byte vectors.  Where rows do not start on 16-byte boundaries (an
+// odd width) but all matrices of the call lie alike, the vectors are those of
+// the aligned grid and up to 2·(VEC − 1) elements at the row's ends go one per
+// thread.  Matrices that lie differently, and rows wider than the registers
+// hold, take the element loop (two passes over the row).
+// dγ: every thread owns the same columns of all its rows, a CTA's part goes to
+// the workspace and a second kernel adds the parts in their order.
 #include <cstdint>
 
 #include "rows.cuh"
@@ -74,6 +85,193 @@ __global__ void __launch_bounds__(kNormThreads) norm_loop_kernel(const __grid_co
     }
 }
 
+// What one thread holds of a row: vectors threadIdx-strided, one element at the row's ends.
+struct RowShape {
+    int lead, nvec, edges;
+};
+template <bool BF16, bool EDGE>
+__device__ __forceinline__ RowShape row_shape(const char* p, int D) {
+    constexpr int ES = BF16 ? 2 : 4, VEC = 16 / ES;
+    RowShape s{0, D / VEC, 0};
+    if constexpr (EDGE) {
+        s.lead = min(static_cast<int>((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / ES, D);
+        s.nvec = (D - s.lead) / VEC;
+        s.edges = D - s.nvec * VEC;
+    }
+    return s;
+}
+template <int VEC>
+__device__ __forceinline__ int edge_elem(const RowShape& s, int e) {
+    return e < s.lead ? e : e + s.nvec * VEC;
+}
+
+// N consecutive values of a matrix, N·size a power of two up to 32 bytes and p aligned to it (or to 16).
+template <bool BF16, int N>
+__device__ __forceinline__ void load_n(const char* p, float (&o)[N]) {
+    if constexpr (!BF16) {
+#pragma unroll
+        for (int q = 0; q < N / 4; ++q) {
+            const uint4 v = ld16<false>(p + 16 * q);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[4 * q + e] = vec_elem<false>(v, e);
+        }
+    } else if constexpr (N == 8) {
+        const uint4 v = ld16<false>(p);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = vec_elem<true>(v, e);
+    } else {
+        uint2 v;
+        asm volatile("ld.global.cs.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p) : "memory");
+        o[0] = bf16_lo(v.x);
+        o[1] = bf16_hi(v.x);
+        o[2] = bf16_lo(v.y);
+        o[3] = bf16_hi(v.y);
+    }
+}
+template <bool BF16, int N>
+__device__ __forceinline__ void store_n(char* p, const float (&o)[N]) {
+    if constexpr (!BF16) {
+#pragma unroll
+        for (int q = 0; q < N / 4; ++q) *reinterpret_cast<float4*>(p + 16 * q) = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+    } else if constexpr (N == 8) {
+        *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7]));
+    } else {
+        *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+    }
+}
+// γ of VEC columns from d on (1 without γ); vectors where its columns lie on 16 bytes.
+template <bool EDGE, int VEC>
+__device__ __forceinline__ void load_gamma(const float* gamma, int d, float (&o)[VEC]) {
+    if (gamma == nullptr) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) o[e] = 1.0f;
+    } else if constexpr (EDGE) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) o[e] = __ldg(gamma + d + e);
+    } else {
+#pragma unroll
+        for (int q = 0; q < VEC / 4; ++q) {
+            const float4 v = __ldg(reinterpret_cast<const float4*>(gamma + d) + q);
+            o[4 * q] = v.x;
+            o[4 * q + 1] = v.y;
+            o[4 * q + 2] = v.z;
+            o[4 * q + 3] = v.w;
+        }
+    }
+}
+
+constexpr int kWarpRows = 8;      // rows per CTA of the warp-per-row kernels
+constexpr int max_group(bool bf16, int vpt) { return vpt * (bf16 ? 8 : 4) > 16 ? 512 : 1024; }
+
+// Forward: VPT vectors per thread.  WARP: a warp per row, kWarpRows per CTA; else a CTA per row.
+template <bool BF16, int OUT, int VPT, bool EDGE, bool WARP>
+__global__ void __launch_bounds__(WARP ? 32 * kWarpRows : max_group(BF16, VPT))
+    norm_kernel(const __grid_constant__ NormParams a) {
+    constexpr int ES = BF16 ? 2 : 4, VEC = 16 / ES, YS = OUT == kOutQ8 ? 1 : OUT == kOutBf16 ? 2 : 4;
+    __shared__ float sh[32];
+    pdl_enter();
+    const int G = WARP ? 32 : blockDim.x;
+    const int t = WARP ? threadIdx.x & 31 : threadIdx.x;
+    const int64_t row = WARP ? static_cast<int64_t>(blockIdx.x) * kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
+    if (row >= a.rows) return;       // whole warps
+    const char* x = row_ptr<BF16>(a.x, row, a.ldx);
+    const char* r = a.res ? row_ptr<BF16>(a.res, row, a.ldr) : nullptr;
+    const RowShape s = row_shape<BF16, EDGE>(x, a.D);
+    float h[VPT][VEC], he = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int v = t + i * G;
+        if (v < s.nvec) load_n<BF16, VEC>(x + (s.lead + v * VEC) * ES, h[i]);
+        else
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) h[i][e] = 0.0f;
+    }
+    if (r != nullptr) {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int v = t + i * G;
+            if (v >= s.nvec) break;
+            float rr[VEC];
+            load_n<BF16, VEC>(r + (s.lead + v * VEC) * ES, rr);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) h[i][e] += rr[e];
+        }
+    }
+    const bool has_edge = EDGE && t < s.edges;
+    const int de = EDGE ? edge_elem<VEC>(s, t) : 0;
+    if (has_edge) he = load_elem<BF16>(x, de) + (r ? load_elem<BF16>(r, de) : 0.0f);
+    float ss = he * he, mx = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) ss = fmaf(h[i][e], h[i][e], ss);
+    if (a.h != nullptr) {
+        char* ho = row_ptr<BF16>(a.h, row, a.ldh);
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int v = t + i * G;
+            if (v < s.nvec) store_n<BF16, VEC>(ho + (s.lead + v * VEC) * ES, h[i]);
+        }
+        if (has_edge) store_elem<BF16>(ho, de, he);
+    }
+    // h·γ
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int v = t + i * G;
+        if (v >= s.nvec) break;
+        float g[VEC];
+        load_gamma<EDGE, VEC>(a.gamma, s.lead + v * VEC, g);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            h[i][e] *= g[e];
+            if constexpr (OUT == kOutQ8) mx = max_nan(mx, fabsf(h[i][e]));
+        }
+    }
+    if (has_edge) {
+        he = a.gamma ? he * a.gamma[de] : he;
+        if constexpr (OUT == kOutQ8) mx = max_nan(mx, fabsf(he));
+    }
+    ss = WARP ? warp_all<SumOp>(ss) : block_all<SumOp>(ss, sh);
+    const float rstd = 1.0f / sqrtf(ss / a.D + a.eps);
+    if (t == 0 && a.rstd) a.rstd[row] = rstd;
+    if constexpr (OUT == kOutQ8) {
+        mx = WARP ? warp_all<MaxNanOp>(mx) : block_all<MaxNanOp>(mx, sh);
+        const float sc = mx * rstd / 127.0f;
+        const float inv = sc > 0.0f && sc < INFINITY ? rstd / sc : 0.0f;
+        if (t == 0) a.scale[row] = sc;
+        auto quant = [&](float v) {
+            const int q = __float2int_rn(fminf(fmaxf(v * inv, -127.0f), 127.0f));
+            return static_cast<uint32_t>(inv > 0.0f ? q : 0) & 0xffu;
+        };
+        char* y = static_cast<char*>(a.y) + row * a.ldy;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int v = t + i * G;
+            if (v >= s.nvec) break;
+            uint32_t w[VEC / 4];
+#pragma unroll
+            for (int q = 0; q < VEC / 4; ++q)
+                w[q] = quant(h[i][4 * q]) | quant(h[i][4 * q + 1]) << 8 | quant(h[i][4 * q + 2]) << 16 | quant(h[i][4 * q + 3]) << 24;
+            char* d = y + s.lead + v * VEC;
+            if constexpr (VEC == 8) *reinterpret_cast<uint2*>(d) = make_uint2(w[0], w[VEC / 4 - 1]);
+            else *reinterpret_cast<uint32_t*>(d) = w[0];
+        }
+        if (has_edge) y[de] = static_cast<char>(quant(he));
+    } else {
+        char* y = row_ptr<OUT == kOutBf16>(a.y, row, a.ldy);
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int v = t + i * G;
+            if (v >= s.nvec) break;
+            float o[VEC];
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) o[e] = h[i][e] * rstd;
+            store_n<OUT == kOutBf16, VEC>(y + (s.lead + v * VEC) * YS, o);
+        }
+        if (has_edge) store_elem<OUT == kOutBf16>(y, de, he * rstd);
+    }
+}
+
 struct NormGradParams {
     const void* dy;
     const void* h;
@@ -116,28 +314,143 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_loop_kernel(const __gr
     }
 }
 
+// Backward, rows of a CTA (warp) grid-stride; a thread's columns are the same
+// for every row, except with EDGE, where the aligned grid shifts from row to
+// row: there dγ's part is kept in shared memory, by column.
+template <bool BF16, bool DYBF16, int VPT, bool EDGE, bool WARP>
+__global__ void __launch_bounds__(WARP ? 32 * kWarpRows : max_group(BF16, VPT))
+    norm_grad_kernel(const __grid_constant__ NormGradParams a) {
+    constexpr int ES = BF16 ? 2 : 4, VEC = 16 / ES, YS = DYBF16 ? 2 : 4;
+    extern __shared__ float part_sh[];   // [WARP ? kWarpRows : 1][D] where a.partial
+    __shared__ float sh[32];
+    pdl_enter();
+    const int G = WARP ? 32 : blockDim.x;
+    const int t = WARP ? threadIdx.x & 31 : threadIdx.x;
+    const int w = WARP ? threadIdx.x >> 5 : 0;
+    const bool want = a.partial != nullptr;
+    float* mine = part_sh + w * a.D;
+    float acc[EDGE ? 1 : VPT][EDGE ? 1 : VEC] = {};
+    if (EDGE && want) {
+        for (int d = t; d < a.D; d += G) mine[d] = 0.0f;
+        if (WARP) __syncwarp();
+        else __syncthreads();
+    }
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * (WARP ? kWarpRows : 1);
+    for (int64_t row = static_cast<int64_t>(blockIdx.x) * (WARP ? kWarpRows : 1) + w; row < a.rows; row += stride) {
+        const char* dy = row_ptr<DYBF16>(a.dy, row, a.lddy);
+        const char* hp = row_ptr<BF16>(a.h, row, a.ldh);
+        const char* dh = a.dh ? row_ptr<BF16>(a.dh, row, a.lddh) : nullptr;
+        char* dx = row_ptr<BF16>(a.dx, row, a.lddx);
+        const RowShape s = row_shape<BF16, EDGE>(hp, a.D);
+        float g[VPT][VEC], n[VPT][VEC], ge = 0.0f, ne = 0.0f;
+        const float rstd = a.rstd[row];
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int v = t + i * G;
+            if (v < s.nvec) {
+                load_n<DYBF16, VEC>(dy + (s.lead + v * VEC) * YS, g[i]);
+                load_n<BF16, VEC>(hp + (s.lead + v * VEC) * ES, n[i]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) g[i][e] = n[i][e] = 0.0f;
+            }
+        }
+        const bool has_edge = EDGE && t < s.edges;
+        const int de = EDGE ? edge_elem<VEC>(s, t) : 0;
+        if (has_edge) {
+            ge = load_elem<DYBF16>(dy, de);
+            ne = load_elem<BF16>(hp, de) * rstd;
+        }
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int v = t + i * G;
+            if (v >= s.nvec) break;
+            const int d0 = s.lead + v * VEC;
+            float gm[VEC];
+            load_gamma<EDGE, VEC>(a.gamma, d0, gm);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                n[i][e] *= rstd;
+                if constexpr (EDGE) {
+                    if (want) mine[d0 + e] = fmaf(g[i][e], n[i][e], mine[d0 + e]);
+                } else {
+                    acc[i][e] = fmaf(g[i][e], n[i][e], acc[i][e]);
+                }
+                g[i][e] *= gm[e];
+                sum = fmaf(g[i][e], n[i][e], sum);
+            }
+        }
+        if (has_edge) {
+            if (want) mine[de] = fmaf(ge, ne, mine[de]);
+            if (a.gamma) ge *= a.gamma[de];
+            sum = fmaf(ge, ne, sum);
+        }
+        const float c = (WARP ? warp_all<SumOp>(sum) : block_all<SumOp>(sum, sh)) / a.D;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int v = t + i * G;
+            if (v >= s.nvec) break;
+            float o[VEC];
+            if (dh != nullptr) {
+                load_n<BF16, VEC>(dh + (s.lead + v * VEC) * ES, o);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) o[e] = fmaf(rstd, g[i][e] - n[i][e] * c, o[e]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) o[e] = rstd * (g[i][e] - n[i][e] * c);
+            }
+            store_n<BF16, VEC>(dx + (s.lead + v * VEC) * ES, o);
+        }
+        if (has_edge) store_elem<BF16>(dx, de, fmaf(rstd, ge - ne * c, dh ? load_elem<BF16>(dh, de) : 0.0f));
+        if (EDGE && WARP) __syncwarp();   // another lane takes over a column
+    }
+    if (!want) return;
+    float* out = a.partial + static_cast<int64_t>(blockIdx.x) * a.D;
+    if constexpr (!EDGE) {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int v = t + i * G;
+            if (v * VEC >= a.D) break;
+            float* d = (WARP ? mine : out) + v * VEC;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) d[e] = acc[i][e];
+        }
+        if (!WARP) return;
+    }
+    __syncthreads();
+    for (int d = threadIdx.x; d < a.D; d += blockDim.x) {
+        float v = part_sh[d];
+        if constexpr (WARP) {
+#pragma unroll
+            for (int i = 1; i < kWarpRows; ++i) v += part_sh[i * a.D + d];
+        }
+        out[d] = v;
+    }
+}
+
 struct GammaParams {
     const float* partial;
     float* dgamma;
     int32_t n, D;
 };
 
-// dγ[d] = Σ over the CTAs' parts, in their order: 32 columns per CTA, 8
-// threads per column over interleaved parts, then those 8 in order.
-__global__ void __launch_bounds__(kNormThreads) norm_gamma_kernel(const __grid_constant__ GammaParams a) {
-    __shared__ float sh[8][32];
+// dγ[d] = Σ over the CTAs' parts, in a fixed order: 32 columns per CTA, 32
+// threads per column over interleaved parts, then those 32 in order.
+__global__ void __launch_bounds__(1024) norm_gamma_kernel(const __grid_constant__ GammaParams a) {
+    __shared__ float sh[32][33];
     pdl_enter();
     const int c = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int d = blockIdx.x * 32 + c;
     float s = 0.0f;
-    if (d < a.D)
-        for (int i = w; i < a.n; i += 8) s += a.partial[static_cast<int64_t>(i) * a.D + d];
+    if (d < a.D) {
+#pragma unroll 8
+        for (int i = w; i < a.n; i += 32) s += a.partial[static_cast<int64_t>(i) * a.D + d];
+    }
     sh[w][c] = s;
     __syncthreads();
-    if (w == 0 && d < a.D) {
-        for (int i = 1; i < 8; ++i) s += sh[i][c];
-        a.dgamma[d] = s;
-    }
+    s = warp_all<SumOp>(sh[c][w]);     // warp w: column w's 32 sums
+    if (c == 0 && blockIdx.x * 32 + w < a.D) a.dgamma[blockIdx.x * 32 + w] = s;
 }
 
 constexpr int kGradCtas = 608;   // at most this many parts of dγ
@@ -146,6 +459,61 @@ int grad_parts(int64_t rows) { return static_cast<int>(rows < kGradCtas ? (rows 
 
 bool dtype_ok(int32_t t) { return t == DDP_F32 || t == DDP_BF16; }
 int dsize(int32_t t) { return t == DDP_BF16 ? 2 : 4; }
+
+// How the rows of a call's matrices lie on the grid of VEC elements (16 bytes of x's type).
+enum class Lay { kAligned, kAlike, kDifferent };
+Lay layout(const Mat* const* mats, int n, int D, int vec, const float* gamma) {
+    bool aligned = D % vec == 0 && aligned16(gamma), alike = true;
+    for (int i = 0; i < n; ++i) {
+        const Mat &m = *mats[i], &f = *mats[0];
+        if (m.p == nullptr) continue;
+        const uintptr_t e = reinterpret_cast<uintptr_t>(m.p) / m.esz, e0 = reinterpret_cast<uintptr_t>(f.p) / f.esz;
+        const bool one = m.rows <= 1;
+        alike &= e % vec == e0 % vec && (one || m.ld % vec == f.ld % vec);
+        aligned &= e % vec == 0 && (one || m.ld % vec == 0);
+    }
+    return aligned ? Lay::kAligned : alike ? Lay::kAlike : Lay::kDifferent;
+}
+
+// Vectors per thread and threads per row.  Many rows: a warp per row up to 128
+// vectors, then two vectors per thread; few rows (they do not fill the GPU):
+// as many threads as the row has vectors.  0 threads: the row does not fit.
+struct Group {
+    int vpt, threads;
+    bool warp;
+};
+Group pick_group(int64_t rows, int D, bool bf16, int sms) {
+    const int vec = bf16 ? 8 : 4, nv = (D + vec - 1) / vec;
+    if (nv <= 32) return {1, 32, true};
+    const bool few = rows < 2ll * sms;
+    if (!few && nv <= 128) return {nv <= 64 ? 2 : 4, 32, true};
+    for (int vpt = few ? 1 : 2; vpt <= 4; vpt *= 2) {
+        const int t = ((nv + vpt - 1) / vpt + 31) / 32 * 32;
+        if (t <= max_group(bf16, vpt)) return {vpt, t, false};
+    }
+    return {0, 0, false};
+}
+
+template <bool BF16, int OUT, bool EDGE>
+void (*fwd_kernel(const Group& g))(NormParams) {
+    if (g.warp) return g.vpt == 1 ? norm_kernel<BF16, OUT, 1, EDGE, true> : g.vpt == 2 ? norm_kernel<BF16, OUT, 2, EDGE, true> : norm_kernel<BF16, OUT, 4, EDGE, true>;
+    return g.vpt == 1 ? norm_kernel<BF16, OUT, 1, EDGE, false> : g.vpt == 2 ? norm_kernel<BF16, OUT, 2, EDGE, false> : norm_kernel<BF16, OUT, 4, EDGE, false>;
+}
+template <bool BF16, int OUT>
+void (*fwd_kernel(Lay lay, const Group& g))(NormParams) {
+    if (lay == Lay::kDifferent || g.threads == 0) return norm_loop_kernel<BF16, OUT>;
+    return lay == Lay::kAligned ? fwd_kernel<BF16, OUT, false>(g) : fwd_kernel<BF16, OUT, true>(g);
+}
+template <bool BF16, bool DYBF16, bool EDGE>
+void (*bwd_kernel(const Group& g))(NormGradParams) {
+    if (g.warp) return g.vpt == 1 ? norm_grad_kernel<BF16, DYBF16, 1, EDGE, true> : g.vpt == 2 ? norm_grad_kernel<BF16, DYBF16, 2, EDGE, true> : norm_grad_kernel<BF16, DYBF16, 4, EDGE, true>;
+    return g.vpt == 1 ? norm_grad_kernel<BF16, DYBF16, 1, EDGE, false> : g.vpt == 2 ? norm_grad_kernel<BF16, DYBF16, 2, EDGE, false> : norm_grad_kernel<BF16, DYBF16, 4, EDGE, false>;
+}
+template <bool BF16, bool DYBF16>
+void (*bwd_kernel(Lay lay, const Group& g))(NormGradParams) {
+    if (lay == Lay::kDifferent || g.threads == 0) return norm_grad_loop_kernel<BF16, DYBF16>;
+    return lay == Lay::kAligned ? bwd_kernel<BF16, DYBF16, false>(g) : bwd_kernel<BF16, DYBF16, true>(g);
+}
 
 int forward(const void* x, int64_t ldx, const void* residual, int64_t ldr, int32_t in_dtype, const float* gamma,
             int64_t rows, int32_t D, float eps, void* h_out, int64_t ldh, void* y, int64_t ldy, int out,
@@ -171,12 +539,20 @@ int forward(const void* x, int64_t ldx, const void* residual, int64_t ldr, int32
             if (mats_overlap(*o, *i)) return DDP_ERR_INVALID_ARG;
     if (rows == 0) return DDP_OK;
     const NormParams p{x, residual, gamma, h_out, y, scale, rstd_out, ldx, ldr, ldh, ldy, rows, D, eps};
+    DeviceInfo d;
+    const int st = current_device_info(&d);
+    if (st != DDP_OK) return st;
     const bool b = in_dtype == DDP_BF16;
-    void (*kernel)(NormParams) = out == kOutQ8    ? (b ? norm_loop_kernel<true, kOutQ8> : norm_loop_kernel<false, kOutQ8>)
-                                 : out == kOutBf16 ? (b ? norm_loop_kernel<true, kOutBf16> : norm_loop_kernel<false, kOutBf16>)
-                                                   : (b ? norm_loop_kernel<true, kOutF32> : norm_loop_kernel<false, kOutF32>);
-    const int64_t cap = 1 << 16;
-    return launch_pdl(kernel, dim3(static_cast<unsigned>(rows < cap ? rows : cap)), kNormThreads,
+    const Mat* const mats[4] = {&mx, &mr, &mh, &my};
+    const Lay lay = layout(mats, 4, D, b ? 8 : 4, gamma);
+    const Group g = pick_group(rows, D, b, d.sm_count);
+    void (*kernel)(NormParams) = out == kOutQ8    ? (b ? fwd_kernel<true, kOutQ8>(lay, g) : fwd_kernel<false, kOutQ8>(lay, g))
+                                 : out == kOutBf16 ? (b ? fwd_kernel<true, kOutBf16>(lay, g) : fwd_kernel<false, kOutBf16>(lay, g))
+                                                   : (b ? fwd_kernel<true, kOutF32>(lay, g) : fwd_kernel<false, kOutF32>(lay, g));
+    const bool loop = lay == Lay::kDifferent || g.threads == 0;
+    const int64_t ctas = loop ? (rows < (1 << 16) ? rows : 1 << 16) : g.warp ? (rows + kWarpRows - 1) / kWarpRows : rows;
+    if (ctas > INT32_MAX) return DDP_ERR_UNSUPPORTED;
+    return launch_pdl(kernel, dim3(static_cast<unsigned>(ctas)), loop ? kNormThreads : g.warp ? 32 * kWarpRows : g.threads,
                       static_cast<cudaStream_t>(stream), p);
 }
 
@@ -231,19 +607,32 @@ extern "C" int rmsnorm_backward(const void* dy, int64_t lddy, int32_t dy_dtype, 
             if (mats_overlap(*o, *i)) return DDP_ERR_INVALID_ARG;
     if (mats_overlap(mw, ws)) return DDP_ERR_INVALID_ARG;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const int parts = grad_parts(rows);
+    int parts = 0;
     if (rows > 0) {
         const NormGradParams p{dy, h, rstd, gamma, dh, dx, dgamma ? static_cast<float*>(workspace) : nullptr,
                                lddy, ldh, lddh, lddx, rows, D};
-        const bool b = h_dtype == DDP_BF16, c = dy_dtype == DDP_BF16;
-        void (*kernel)(NormGradParams) = b ? (c ? norm_grad_loop_kernel<true, true> : norm_grad_loop_kernel<true, false>)
-                                           : (c ? norm_grad_loop_kernel<false, true> : norm_grad_loop_kernel<false, false>);
-        const int st = launch_pdl(kernel, dim3(static_cast<unsigned>(parts)), kNormThreads, s, p);
+        DeviceInfo d;
+        int st = current_device_info(&d);
         if (st != DDP_OK) return st;
+        const bool b = h_dtype == DDP_BF16, c = dy_dtype == DDP_BF16;
+        const Mat* const mats[4] = {&mh, &my, &md, &mo};
+        const Lay lay = layout(mats, 4, D, b ? 8 : 4, gamma);
+        const Group g = pick_group(rows, D, b, d.sm_count);
+        const bool loop = lay == Lay::kDifferent || g.threads == 0;
+        void (*kernel)(NormGradParams) = b ? (c ? bwd_kernel<true, true>(lay, g) : bwd_kernel<true, false>(lay, g))
+                                           : (c ? bwd_kernel<false, true>(lay, g) : bwd_kernel<false, false>(lay, g));
+        const int threads = loop ? kNormThreads : g.warp ? 32 * kWarpRows : g.threads;
+        const int64_t ctas = !loop && g.warp ? (rows + kWarpRows - 1) / kWarpRows : rows;
+        const int per_sm = threads >= 1024 ? 1 : threads >= 512 ? 2 : threads > 256 ? 3 : 4;
+        const int64_t cap = static_cast<int64_t>(d.sm_count) * per_sm < kGradCtas ? d.sm_count * per_sm : kGradCtas;
+        parts = static_cast<int>(ctas < cap ? ctas : cap);
+        const size_t smem = loop || !dgamma || (lay == Lay::kAligned && !g.warp)
+                                ? 0 : static_cast<size_t>(g.warp ? kWarpRows : 1) * D * 4;
+        if ((st = launch_smem(kernel, static_cast<unsigned>(parts), threads, smem, s, p)) != DDP_OK) return st;
     }
     if (dgamma) {
-        const GammaParams q{static_cast<const float*>(workspace), dgamma, rows > 0 ? parts : 0, D};
-        return launch_pdl(norm_gamma_kernel, dim3(static_cast<unsigned>((D + 31) / 32)), kNormThreads, s, q);
+        const GammaParams q{static_cast<const float*>(workspace), dgamma, parts, D};
+        return launch_pdl(norm_gamma_kernel, dim3(static_cast<unsigned>((D + 31) / 32)), 1024, s, q);
     }
     return DDP_OK;
 }

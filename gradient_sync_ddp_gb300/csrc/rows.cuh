@@ -106,4 +106,27 @@ inline bool mats_same(const Mat& a, const Mat& b) {
     return a.p == b.p && a.esz == b.esz && (a.ld == b.ld || a.rows <= 1);
 }
 
+// Launch with dynamic shared memory and programmatic stream serialisation allowed (the kernels begin with
+// pdl_enter()); the opt-in beyond 48 KB is asked for only where it is needed.
+template <typename Params>
+int launch_smem(void (*kernel)(Params), unsigned grid, int block, size_t smem, cudaStream_t s, const Params& params) {
+    cudaError_t e;
+    if (smem > 48 * 1024 - 1024 &&
+        (e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  static_cast<int>(smem))) != cudaSuccess)
+        return cuda_fail(e);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(static_cast<unsigned>(block));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if ((e = cudaLaunchKernelEx(&cfg, kernel, params)) != cudaSuccess) return cuda_fail(e);
+    return check_launch();
+}
+
 }  // namespace ddp

@@ -175,10 +175,15 @@ def test_strides_offsets_and_in_place(g, D, dt):
     sync()
     check_forward(x0, r0, gamma, 1e-5, h, y, rstd)
     assert torch.all(out[:, :2] == 7) and torch.all(out[:, 2 + D:] == 7)
-    y0 = y.clone()
-    g.rmsnorm_forward(x, gamma, x, 1e-5, residual=r, h_out=r)              # both in place, in one buffer
+    # both in place, in one buffer: the bits of a call whose outputs lie like x and residual (other layouts may sum
+    # in another order)
+    other = torch.empty_like(buf)
+    y0, h0 = other[:, 3:3 + D], other[:, D + 7:2 * D + 7]
+    g.rmsnorm_forward(x, gamma, y0, 1e-5, residual=r, h_out=h0)
+    g.rmsnorm_forward(x, gamma, x, 1e-5, residual=r, h_out=r)
     sync()
-    assert torch.equal(x, y0) and torch.equal(r, h)
+    assert torch.equal(x, y0) and torch.equal(r, h0)
+    check_forward(x0, r0, gamma, 1e-5, r, x, None)
     rest = torch.ones(wide, dtype=torch.bool, device="cuda")
     rest[3:3 + D] = False
     rest[D + 7:2 * D + 7] = False
