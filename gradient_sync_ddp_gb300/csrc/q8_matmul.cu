@@ -12,16 +12,24 @@
 // its transpose, D[n, m]: channels are the 128-row operand, tokens the wide one.
 //   widen_kernel   tokens to fp16 in the workspace (channels whose rows TMA
 //                  cannot address are repacked there too, still in 8 bits)
-//   tile_kernel    persistent, one CTA per SM, roles by warp:
-//     two producers  TMA: tokens [NT][64] fp16 (128-byte swizzle), channels
-//                    [128][64] int8 (64-byte swizzle), each into its own ring
-//     converters     two warpgroups, a channel row per thread: 64 bytes from
-//                    shared memory, widened in registers, stored to TMEM;
-//                    channels thus cost 8 bits of L2 and shared memory
-//     one issuer     tcgen05.mma, A from TMEM, B from shared memory,
-//                    accumulators [128][NT] fp32 in TMEM, two of them
+//   tile_kernel    persistent, a pair of CTAs (two SMs) per tile of 256
+//                  channels x NT tokens, roles by warp in each CTA:
+//     two producers  TMA, 128 of K at a time: the CTA's half of the tokens
+//                    [NT/2][2 x 64] fp16 and its 128 channels [128][128] int8
+//                    (both in the 128-byte swizzle), each into its own ring
+//     converters     two warpgroups, a channel row per thread, each its half
+//                    of the 128: 64 bytes from shared memory, widened in
+//                    registers, stored to TMEM; channels thus cost 8 bits of
+//                    L2 and shared memory
+//     one issuer     (of the pair's first CTA) tcgen05.mma.cta_group::2, A
+//                    from TMEM, B from shared memory, accumulators fp32 in
+//                    TMEM, two of them
 //     epilogue       one warpgroup: TMEM -> scales -> out, under the next
 //                    tile's contraction
+// The pair halves what a tile's tokens cost: with one CTA per tile, L2 -> SM
+// traffic (65 bytes per clock and SM) and shared-memory traffic held the
+// contraction at 0.66 of its rate.  Few tiles split K (the parts are fp32 in the
+// workspace, combine_kernel adds them in their order).
 // Every wait is bounded; a tile whose wait ran out is written as NaN.
 #include <cstdint>
 
@@ -35,26 +43,20 @@ namespace {
 
 constexpr int kMaxK = 131071;     // |Σ| < 2^31
 constexpr int kFewTokens = 8;
-constexpr int kTileN = 128;       // channels per tile: the MMA's rows
+constexpr int kCtaN = 128;        // channels per CTA; 256 per pair: the MMA's rows
 constexpr int kMaxNT = 192;       // tokens per tile: 2 accumulators of 192 columns + 4 channel stages of 32 = 512
-constexpr int kBlockK = 64;
-constexpr int kWStageBytes = kTileN * kBlockK;
-constexpr int kAStages = 4;       // channel stages in TMEM, 32 columns each
-constexpr int kAColumn0 = 2 * kMaxNT;
-constexpr int kMaxStages = 16;
+constexpr int kBlockK = 128;      // one stage of the rings
+constexpr int kHalfK = 64;        // one stage of channels in TMEM: 32 columns
+constexpr int kWStageBytes = kCtaN * kBlockK;
+constexpr int kMaxAStages = 8;
+constexpr int kMaxStages = 12;
 constexpr int kRingBytes = 200 * 1024;
 constexpr int kTileThreads = 512;
-constexpr uint64_t kWaitNs = 1000000000ull;
+constexpr long long kWaitClocks = 2000000000ll;   // about a second (clock64: the nanosecond timer is slow to read)
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
-__device__ __forceinline__ uint64_t global_ns() {
-    uint64_t t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    return t;
-}
-
 // ---- few tokens ---------------------------------------------------------
 
 struct FewParams {
@@ -198,14 +200,14 @@ struct TileParams {
     CUtensorMap tx, tw;
     const float* sa;
     const float* sw;
-    void* out;
+    void* out;       // or the parts, float [splits][M][N]
     int64_t ldo;
-    int32_t M, N, kblocks, nt, m_tiles, n_tiles, stages;
+    int32_t M, N, halves, nt, m_tiles, n_tiles, group, splits, blocks_per_split, stages, a_stages;
 };
 
 struct TileShared {
     uint64_t x_full[kMaxStages], x_empty[kMaxStages], w_full[kMaxStages], w_empty[kMaxStages];
-    uint64_t a_full[kAStages], a_empty[kAStages], d_full[2], d_empty[2], idle;
+    uint64_t a_full[kMaxAStages], a_empty[kMaxAStages], d_full[2], d_empty[2], idle;
     uint32_t tmem;
     volatile int failed;
 };
@@ -216,6 +218,12 @@ __device__ __forceinline__ void bar_init(uint64_t* b, int count) {
 __device__ __forceinline__ void bar_arrive(uint64_t* b) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(b)) : "memory");
 }
+// Arrive on the barrier of the pair's first CTA.
+__device__ __forceinline__ void bar_arrive_first(uint64_t* b) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(b)));
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(r) : "memory");
+}
 __device__ __forceinline__ void bar_expect(uint64_t* b, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(b)), "r"(bytes) : "memory");
 }
@@ -223,7 +231,7 @@ __device__ __forceinline__ bool bar_poll(uint64_t* b, uint32_t parity) {
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 100000;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, 100000;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
         : "r"(smem_u32(b)), "r"(parity)
@@ -233,26 +241,28 @@ __device__ __forceinline__ bool bar_poll(uint64_t* b, uint32_t parity) {
 // Wait for the phase of `parity`; false once a wait of this CTA has run out.
 __device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, TileShared& s) {
     if (bar_poll(b, parity)) return true;
-    const uint64_t t0 = global_ns();
+    const long long t0 = clock64();
     while (!bar_poll(b, parity)) {
         if (s.failed) return false;
-        if (global_ns() - t0 > kWaitNs) {
+        if (clock64() - t0 > kWaitClocks) {
             s.failed = 1;
             return false;
         }
     }
     return true;
 }
-
 // The same for work of this CTA that is still in flight when it ends, whether or not a wait has run out before.
 __device__ __forceinline__ void bar_drain(uint64_t* b, uint32_t parity, TileShared& s) {
-    const uint64_t t0 = global_ns();
+    const long long t0 = clock64();
     while (!bar_poll(b, parity)) {
-        if (global_ns() - t0 > kWaitNs) {
+        if (clock64() - t0 > kWaitClocks) {
             s.failed = 1;
             return;
         }
     }
+}
+__device__ __forceinline__ void pair_sync() {
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
 __device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
@@ -272,13 +282,17 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
         "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
         : "memory");
 }
+// The barrier of both CTAs arrives when the MMAs issued so far are done.
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-                 : "memory");
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -316,120 +330,167 @@ struct Ring {
             ph ^= 1;
         }
     }
+    __device__ __forceinline__ void back(int n) {
+        if (i == 0) {
+            i = n;
+            ph ^= 1;
+        }
+        --i;
+    }
 };
 
-template <bool BF16>
+// The u-th piece of work: a tile and a range of K blocks.  Tiles go in groups
+// of `group` token tiles, channels outer within a group, so that the pairs
+// running at a time share both operands in L2.
+struct Piece {
+    int m0, n0, split, h0, h1;   // tokens, channels, part of K, halves of 64 of K
+};
+__device__ __forceinline__ Piece piece(const TileParams& p, int u) {
+    Piece w;
+    w.split = u % p.splits;
+    const int t = u / p.splits, per_group = p.group * p.n_tiles, g = t / per_group, r = t - g * per_group;
+    const int wide = min(p.group, p.m_tiles - g * p.group);
+    w.n0 = r / wide * 2 * kCtaN;
+    w.m0 = (g * p.group + r % wide) * p.nt;
+    w.h0 = w.split * p.blocks_per_split * 2;
+    w.h1 = min(p.halves, w.h0 + p.blocks_per_split * 2);
+    return w;
+}
+
+enum { kTileF32 = 0, kTileBf16 = 1, kTilePart = 2 };
+
+template <int OUT>
 __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_constant__ TileParams p) {
     extern __shared__ unsigned char raw[];
     __shared__ TileShared s;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = blockIdx.x & 1;
+    const int nth = p.nt / 2, x_half = nth * 128, x_stage = 2 * x_half;
     const uint32_t pad = (1024u - (smem_u32(raw) & 1023u)) & 1023u;
-    unsigned char* xs = raw + pad;                                   // [stages][nt][128]
-    unsigned char* wsm = xs + p.stages * p.nt * 128;                 // [stages][128][64]
+    unsigned char* xs = raw + pad;                                   // [stages][2][nt / 2][128]
+    unsigned char* wsm = xs + p.stages * x_stage;                    // [stages][128][128]
     if (threadIdx.x == 0) {
         for (int i = 0; i < p.stages; ++i) {
-            bar_init(&s.x_full[i], 1);
+            bar_init(&s.x_full[i], rank == 0 ? 2 : 1);               // its own copies, and the other CTA's word on its
             bar_init(&s.x_empty[i], 1);
             bar_init(&s.w_full[i], 1);
-            bar_init(&s.w_empty[i], 4);
+            bar_init(&s.w_empty[i], 8);
         }
-        for (int i = 0; i < kAStages; ++i) {
-            bar_init(&s.a_full[i], 4);
+        for (int i = 0; i < p.a_stages; ++i) {
+            bar_init(&s.a_full[i], 8);                               // four warps of either CTA
             bar_init(&s.a_empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             bar_init(&s.d_full[i], 1);
-            bar_init(&s.d_empty[i], 4);
+            bar_init(&s.d_empty[i], 8);
         }
         bar_init(&s.idle, 1);
         s.failed = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 0) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s.tmem)) : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s.tmem)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
     fence_before();
     __syncthreads();
+    pair_sync();
     fence_after();
-    const uint32_t tmem = s.tmem;
+    const uint32_t tmem = s.tmem, a_col0 = tmem + (2 * p.nt + 31) / 32 * 32;
     pdl_enter();
-    const int tiles = p.m_tiles * p.n_tiles;
+    const int pieces = p.m_tiles * p.n_tiles * p.splits, first = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
     if (warp == 0 && lane == 0) {                       // token producer
         Ring r;
         int issued = 0;
         bool ok = true;
-        for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-            const int m0 = (t % p.m_tiles) * p.nt;
-            for (int kb = 0; kb < p.kblocks; ++kb) {
+        for (int u = first; u < pieces && ok; u += pairs) {
+            const Piece w = piece(p, u);
+            for (int h = w.h0; h < w.h1; h += 2) {
                 if (!(ok = bar_wait(&s.x_empty[r.i], r.ph ^ 1, s))) break;
-                bar_expect(&s.x_full[r.i], p.nt * 128);
-                tma_load(xs + r.i * p.nt * 128, &p.tx, kb * kBlockK, m0, &s.x_full[r.i]);
+                const bool two = h + 1 < w.h1;
+                bar_expect(&s.x_full[r.i], two ? x_stage : x_half);
+                unsigned char* d = xs + r.i * x_stage;
+                tma_load(d, &p.tx, h * kHalfK, w.m0 + rank * nth, &s.x_full[r.i]);
+                if (two) tma_load(d + x_half, &p.tx, (h + 1) * kHalfK, w.m0 + rank * nth, &s.x_full[r.i]);
                 r.next(p.stages);
                 ++issued;
             }
         }
         // every copy has landed before the CTA gives its shared memory back
         for (int j = 0; j < p.stages && j < issued; ++j) {
-            if (r.i == 0) r.ph ^= 1;
-            r.i = r.i == 0 ? p.stages - 1 : r.i - 1;
+            r.back(p.stages);
             bar_drain(&s.x_full[r.i], r.ph, s);
         }
     } else if (warp == 2 && lane == 0) {                // channel producer
         Ring r;
         int issued = 0;
         bool ok = true;
-        for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-            const int n0 = (t / p.m_tiles) * kTileN;
-            for (int kb = 0; kb < p.kblocks; ++kb) {
+        for (int u = first; u < pieces && ok; u += pairs) {
+            const Piece w = piece(p, u);
+            for (int h = w.h0; h < w.h1; h += 2) {
                 if (!(ok = bar_wait(&s.w_empty[r.i], r.ph ^ 1, s))) break;
                 bar_expect(&s.w_full[r.i], kWStageBytes);
-                tma_load(wsm + r.i * kWStageBytes, &p.tw, kb * kBlockK, n0, &s.w_full[r.i]);
+                tma_load(wsm + r.i * kWStageBytes, &p.tw, h * kHalfK, w.n0 + rank * kCtaN, &s.w_full[r.i]);
                 r.next(p.stages);
                 ++issued;
             }
         }
         for (int j = 0; j < p.stages && j < issued; ++j) {
-            if (r.i == 0) r.ph ^= 1;
-            r.i = r.i == 0 ? p.stages - 1 : r.i - 1;
+            r.back(p.stages);
             bar_drain(&s.w_full[r.i], r.ph, s);
         }
-    } else if (warp == 1 && lane == 0) {                // issuer
+    } else if (warp == 1 && lane == 0 && rank == 0) {   // issuer
         Ring x, a, d;
-        const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(p.nt / 8) << 17) | ((kTileN / 16u) << 24);
+        const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(p.nt / 8) << 17) | ((2 * kCtaN / 16u) << 24);
         bool ok = true;
-        for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+        for (int u = first; u < pieces && ok; u += pairs) {
+            const Piece w = piece(p, u);
             if (!(ok = bar_wait(&s.d_empty[d.i], d.ph ^ 1, s))) break;
             fence_after();
-            const uint32_t acc = tmem + d.i * kMaxNT;
-            for (int kb = 0; kb < p.kblocks; ++kb) {
-                if (!(ok = bar_wait(&s.x_full[x.i], x.ph, s)) || !(ok = bar_wait(&s.a_full[a.i], a.ph, s))) break;
-                fence_after();
-                const uint64_t desc = smem_desc(smem_u32(xs + x.i * p.nt * 128));
-                const uint32_t at = tmem + kAColumn0 + a.i * 32;
+            const uint32_t acc = tmem + d.i * p.nt;
+            for (int h = w.h0; h < w.h1 && ok; h += 2) {
+                if (!(ok = bar_wait(&s.x_full[x.i], x.ph, s))) break;
+                for (int g = 0; g < 2 && h + g < w.h1; ++g) {
+                    if (!(ok = bar_wait(&s.a_full[a.i], a.ph, s))) break;
+                    fence_after();
+                    const uint64_t desc = smem_desc(smem_u32(xs + x.i * x_stage + g * x_half));
+                    const uint32_t at = a_col0 + a.i * 32;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) mma_ts(acc, at + 8 * k, desc + 2 * k, idesc, kb > 0 || k > 0);
+                    for (int k = 0; k < 4; ++k) mma_ts(acc, at + 8 * k, desc + 2 * k, idesc, h > w.h0 || g > 0 || k > 0);
+                    mma_commit(&s.a_empty[a.i]);
+                    a.next(p.a_stages);
+                }
                 mma_commit(&s.x_empty[x.i]);
-                mma_commit(&s.a_empty[a.i]);
                 x.next(p.stages);
-                a.next(kAStages);
             }
             if (ok) mma_commit(&s.d_full[d.i]);
             d.next(2);
         }
         mma_commit(&s.idle);
         bar_drain(&s.idle, 0, s);
+    } else if (warp == 1 && lane == 0) {                // the second CTA's tokens are there: told to the first
+        Ring x;
+        bool ok = true;
+        for (int u = first; u < pieces && ok; u += pairs) {
+            const Piece w = piece(p, u);
+            for (int h = w.h0; h < w.h1; h += 2) {
+                if (!(ok = bar_wait(&s.x_full[x.i], x.ph, s))) break;
+                bar_arrive_first(&s.x_full[x.i]);
+                x.next(p.stages);
+            }
+        }
     } else if (warp >= 4 && warp < 8) {                 // epilogue
         Ring d;
         const int q = warp & 3;
-        for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
-            const int m0 = (t % p.m_tiles) * p.nt;
-            const int64_t n = static_cast<int64_t>(t / p.m_tiles) * kTileN + q * 32 + lane;
+        for (int u = first; u < pieces; u += pairs) {
+            const Piece w = piece(p, u);
+            const int64_t n = w.n0 + rank * kCtaN + q * 32 + lane;
             const bool ok = bar_wait(&s.d_full[d.i], d.ph, s) && !s.failed;
             fence_after();
-            const float swn = n < p.N ? p.sw[n] : 0.0f;
-            const uint32_t acc = tmem + d.i * kMaxNT + (static_cast<uint32_t>(q * 32) << 16);
+            const float swn = OUT != kTilePart && n < p.N ? p.sw[n] : 0.0f;
+            float* part = static_cast<float*>(p.out) + static_cast<int64_t>(w.split) * p.M * p.N;
+            const uint32_t acc = tmem + d.i * p.nt + (static_cast<uint32_t>(q * 32) << 16);
             for (int c = 0; c < p.nt; c += 16) {
                 float v[16];
                 __syncwarp();
@@ -437,59 +498,90 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
                 if (c + 16 >= p.nt) {
                     fence_before();
                     __syncwarp();
-                    if (lane == 0) bar_arrive(&s.d_empty[d.i]);
+                    if (lane == 0) bar_arrive_first(&s.d_empty[d.i]);
                 }
                 if (n < p.N) {
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
-                        const int m = m0 + c + j;
-                        if (m < p.M)
-                            store_elem<BF16>(p.out, m * p.ldo + n, ok ? v[j] * __ldg(p.sa + m) * swn : __int_as_float(0x7fffffff));
+                        const int m = w.m0 + c + j;
+                        if (m >= p.M) break;
+                        if constexpr (OUT == kTilePart) {
+                            part[static_cast<int64_t>(m) * p.N + n] = ok ? v[j] : __int_as_float(0x7fffffff);
+                        } else {
+                            store_elem<OUT == kTileBf16>(p.out, m * p.ldo + n, ok ? v[j] * __ldg(p.sa + m) * swn : __int_as_float(0x7fffffff));
+                        }
                     }
                 }
             }
             d.next(2);
         }
-    } else if (warp >= 8) {                             // converters: warpgroup g takes every other k block
+    } else if (warp >= 8) {                             // converters: warpgroup g takes half g of each stage
         const int g = (warp - 8) >> 2, q = warp & 3, row = q * 32 + lane;
         Ring w, a;
         const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
-        int turn = 0;
         bool ok = true;
-        for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-            for (int kb = 0; kb < p.kblocks; ++kb, turn ^= 1) {
-                if (turn == g) {
-                    if (!(ok = __all_sync(0xffffffffu, bar_wait(&s.w_full[w.i], w.ph, s)))) break;
+        for (int u = first; u < pieces && ok; u += pairs) {
+            const Piece pc = piece(p, u);
+            for (int h = pc.h0; h < pc.h1; h += 2) {
+                if (!(ok = __all_sync(0xffffffffu, bar_wait(&s.w_full[w.i], w.ph, s)))) break;
+                const bool mine = h + g < pc.h1;
+                uint32_t r[32];
+                if (mine) {
                     const unsigned char* src = wsm + w.i * kWStageBytes + row * kBlockK;
-                    uint32_t r[32];
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        const int4 v = *reinterpret_cast<const int4*>(src + ((c ^ ((row >> 1) & 3)) << 4));
+                        const int4 v = *reinterpret_cast<const int4*>(src + (((4 * g + c) ^ (row & 7)) << 4));
                         widen4(v.x, r[8 * c], r[8 * c + 1]);
                         widen4(v.y, r[8 * c + 2], r[8 * c + 3]);
                         widen4(v.z, r[8 * c + 4], r[8 * c + 5]);
                         widen4(v.w, r[8 * c + 6], r[8 * c + 7]);
                     }
-                    __syncwarp();
-                    if (lane == 0) bar_arrive(&s.w_empty[w.i]);
+                }
+                __syncwarp();
+                if (lane == 0) bar_arrive(&s.w_empty[w.i]);
+                w.next(p.stages);
+                if (g == 1) a.next(p.a_stages);          // past half 0's stage
+                if (mine) {
                     if (!(ok = __all_sync(0xffffffffu, bar_wait(&s.a_empty[a.i], a.ph ^ 1, s)))) break;
                     fence_after();
-                    tmem_st32(tmem + kAColumn0 + a.i * 32 + lane_base, r);
+                    tmem_st32(a_col0 + a.i * 32 + lane_base, r);
                     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                     fence_before();
                     __syncwarp();
-                    if (lane == 0) bar_arrive(&s.a_full[a.i]);
+                    if (lane == 0) bar_arrive_first(&s.a_full[a.i]);
+                    a.next(p.a_stages);
                 }
-                w.next(p.stages);
-                a.next(kAStages);
+                if (g == 0 && h + 1 < pc.h1) a.next(p.a_stages);   // past half 1's
             }
         }
     }
     __syncwarp();
     fence_before();
     __syncthreads();
+    pair_sync();                                        // nothing of the pair's is in flight any more
     fence_after();
-    if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+struct CombineParams {
+    const float* part;
+    const float* sa;
+    const float* sw;
+    void* out;
+    int64_t ldo, M, N;
+    int32_t splits;
+};
+
+// out = (Σ over the parts, in their order)·scales.
+template <bool BF16>
+__global__ void __launch_bounds__(kThreads) combine_kernel(const __grid_constant__ CombineParams p) {
+    pdl_enter();
+    const int64_t n = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x, m = blockIdx.y;
+    if (n >= p.N) return;
+    float v = 0.0f;
+#pragma unroll 4
+    for (int i = 0; i < p.splits; ++i) v += p.part[(i * p.M + m) * p.N + n];
+    store_elem<BF16>(p.out, m * p.ldo + n, v * p.sa[m] * p.sw[n]);
 }
 
 // ---- host ----------------------------------------------------------------
@@ -549,6 +641,31 @@ int row_align(const void* p, int64_t ld, int64_t rows) {
 int64_t token_pitch(int32_t K) { return round_up(K, 8); }
 int64_t channel_pitch(int32_t K) { return round_up(K, 16); }
 size_t token_bytes(int64_t M, int32_t K) { return static_cast<size_t>(round_up(M * token_pitch(K) * 2, 256)); }
+size_t channel_bytes(int64_t N, int32_t K) { return static_cast<size_t>(round_up(N * channel_pitch(K), 256)); }
+
+// Tiles of more than kFewTokens tokens, and the parts of K where the tiles
+// alone leave pairs of SMs without work (at least kMinBlocks stages each).
+constexpr int kMinBlocks = 4;
+constexpr int kMaxSplits = 16;
+constexpr int kPairs = 76;        // of a full GB300: what splits are made for
+struct Tiles {
+    int nt, m_tiles, n_tiles, blocks, splits, per_split;
+};
+Tiles plan_tiles(int64_t M, int64_t N, int32_t K) {
+    Tiles t{};
+    const int64_t mt = (M + kMaxNT - 1) / kMaxNT;
+    t.nt = static_cast<int>(round_up((M + mt - 1) / mt, 16));
+    t.m_tiles = static_cast<int>((M + t.nt - 1) / t.nt);
+    t.n_tiles = static_cast<int>((N + 2 * kCtaN - 1) / (2 * kCtaN));
+    t.blocks = (K + kBlockK - 1) / kBlockK;
+    int64_t s = kPairs / (static_cast<int64_t>(t.m_tiles) * t.n_tiles);
+    if (s > t.blocks / kMinBlocks) s = t.blocks / kMinBlocks;
+    if (s > kMaxSplits) s = kMaxSplits;
+    if (s < 1) s = 1;
+    t.per_split = static_cast<int>((t.blocks + s - 1) / s);
+    t.splits = (t.blocks + t.per_split - 1) / t.per_split;
+    return t;
+}
 
 }  // namespace
 }  // namespace ddp
@@ -558,7 +675,8 @@ using namespace ddp;
 extern "C" size_t q8_matmul_workspace_bytes(int64_t M, int64_t N, int32_t K) {
     if (M < 0 || N < 0 || K < 0 || K > kMaxK || M > INT32_MAX || N > INT32_MAX) return 0;
     if (M <= kFewTokens || N == 0 || K == 0) return 16;
-    return token_bytes(M, K) + static_cast<size_t>(N * channel_pitch(K));
+    const Tiles t = plan_tiles(M, N, K);
+    return token_bytes(M, K) + channel_bytes(N, K) + (t.splits > 1 ? static_cast<size_t>(t.splits) * M * N * 4 : 0);
 }
 
 extern "C" int q8_matmul(const int8_t* a, int64_t lda, const float* a_scale, const int8_t* w, int64_t ldw,
@@ -618,29 +736,39 @@ extern "C" int q8_matmul(const int8_t* a, int64_t lda, const float* a_scale, con
     st = launch_pdl(widen_kernel, dim3(static_cast<unsigned>(wide < cap ? wide : cap)), kThreads, s, wp_);
     if (st != DDP_OK) return st;
 
+    const Tiles t = plan_tiles(M, N, K);
+    const int64_t pieces = static_cast<int64_t>(t.m_tiles) * t.n_tiles * t.splits;
+    if (pieces > INT32_MAX / 2) return DDP_ERR_UNSUPPORTED;
+    float* parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + token_bytes(M, K) + channel_bytes(N, K));
     TileParams p{};
-    p.m_tiles = static_cast<int32_t>((M + kMaxNT - 1) / kMaxNT);
-    p.nt = static_cast<int32_t>(round_up((M + p.m_tiles - 1) / p.m_tiles, 16));
-    p.m_tiles = static_cast<int32_t>((M + p.nt - 1) / p.nt);
-    p.n_tiles = static_cast<int32_t>((N + kTileN - 1) / kTileN);
-    if (static_cast<int64_t>(p.m_tiles) * p.n_tiles > INT32_MAX / 2) return DDP_ERR_UNSUPPORTED;
-    p.kblocks = (K + kBlockK - 1) / kBlockK;
+    p.nt = t.nt;
+    p.m_tiles = t.m_tiles;
+    p.n_tiles = t.n_tiles;
+    p.splits = t.splits;
+    p.blocks_per_split = t.per_split;
+    p.halves = (K + kHalfK - 1) / kHalfK;
+    p.group = 8;
     const int stage = p.nt * 128 + kWStageBytes;
     p.stages = kRingBytes / stage < kMaxStages ? kRingBytes / stage : kMaxStages;
+    const int a_room = (512 - (2 * p.nt + 31) / 32 * 32) / 32;
+    p.a_stages = a_room < kMaxAStages ? a_room : kMaxAStages;
     p.M = static_cast<int32_t>(M);
     p.N = static_cast<int32_t>(N);
     p.sa = a_scale;
     p.sw = w_scale;
-    p.out = out;
+    p.out = t.splits > 1 ? parts : out;
     p.ldo = ldo;
-    if ((st = encode(&p.tx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, x, K, M, xp * 2, kBlockK, p.nt,
+    if ((st = encode(&p.tx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, x, K, M, xp * 2, kHalfK, p.nt / 2,
                      CU_TENSOR_MAP_SWIZZLE_128B)) != DDP_OK)
         return st;
-    if ((st = encode(&p.tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, repack ? wr : w, K, N, repack ? wp : ldw, kBlockK, kTileN,
-                     CU_TENSOR_MAP_SWIZZLE_64B)) != DDP_OK)
+    if ((st = encode(&p.tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, repack ? wr : w, K, N, repack ? wp : ldw, kBlockK, kCtaN,
+                     CU_TENSOR_MAP_SWIZZLE_128B)) != DDP_OK)
         return st;
-    const int tiles = p.m_tiles * p.n_tiles;
-    return launch_smem(bf16 ? tile_kernel<true> : tile_kernel<false>,
-                       static_cast<unsigned>(tiles < d.sm_count ? tiles : d.sm_count), kTileThreads,
-                       static_cast<size_t>(p.stages) * stage + 1024, s, p);
+    const int64_t pairs = pieces < d.sm_count / 2 ? pieces : d.sm_count / 2;
+    st = launch_smem(t.splits > 1 ? tile_kernel<kTilePart> : bf16 ? tile_kernel<kTileBf16> : tile_kernel<kTileF32>,
+                     static_cast<unsigned>(2 * pairs), kTileThreads, static_cast<size_t>(p.stages) * stage + 1024, s, p, 2);
+    if (st != DDP_OK || t.splits == 1) return st;
+    const CombineParams q{parts, a_scale, w_scale, out, ldo, M, N, t.splits};
+    return launch_pdl(bf16 ? combine_kernel<true> : combine_kernel<false>,
+                      dim3(static_cast<unsigned>((N + kThreads - 1) / kThreads), static_cast<unsigned>(M)), kThreads, s, q);
 }

@@ -106,10 +106,11 @@ inline bool mats_same(const Mat& a, const Mat& b) {
     return a.p == b.p && a.esz == b.esz && (a.ld == b.ld || a.rows <= 1);
 }
 
-// Launch with dynamic shared memory and programmatic stream serialisation allowed (the kernels begin with
+// Launch with dynamic shared memory, in clusters where asked, and programmatic stream serialisation allowed (the kernels begin with
 // pdl_enter()); the opt-in beyond 48 KB is asked for only where it is needed.
 template <typename Params>
-int launch_smem(void (*kernel)(Params), unsigned grid, int block, size_t smem, cudaStream_t s, const Params& params) {
+int launch_smem(void (*kernel)(Params), unsigned grid, int block, size_t smem, cudaStream_t s, const Params& params,
+                unsigned cluster = 1) {
     cudaError_t e;
     if (smem > 48 * 1024 - 1024 &&
         (e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -120,11 +121,14 @@ int launch_smem(void (*kernel)(Params), unsigned grid, int block, size_t smem, c
     cfg.blockDim = dim3(static_cast<unsigned>(block));
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     if ((e = cudaLaunchKernelEx(&cfg, kernel, params)) != cudaSuccess) return cuda_fail(e);
     return check_launch();
 }
