@@ -17,8 +17,8 @@
 //     two producers  TMA, 128 of K at a time: the CTA's half of the tokens
 //                    [NT/2][2 x 64] fp16 and its 128 channels [128][128] int8
 //                    (both in the 128-byte swizzle), each into its own ring
-//     converters     two warpgroups, a channel row per thread, each its half
-//                    of the 128: 64 bytes from shared memory, widened in
+//     converters     four warpgroups, a channel row per thread, each its half
+//                    of every second stage: 64 bytes from shared memory, widened in
 //                    registers, stored to TMEM; channels thus cost 8 bits of
 //                    L2 and shared memory
 //     one issuer     (of the pair's first CTA) tcgen05.mma.cta_group::2, A
@@ -44,14 +44,15 @@ namespace {
 constexpr int kMaxK = 131071;     // |Σ| < 2^31
 constexpr int kFewTokens = 8;
 constexpr int kCtaN = 128;        // channels per CTA; 256 per pair: the MMA's rows
-constexpr int kMaxNT = 192;       // tokens per tile: 2 accumulators of 192 columns + 4 channel stages of 32 = 512
+constexpr int kMaxNT = 192;       // tokens per tile: 2 accumulators of 192 columns + 2 channel stages of 64 = 512
 constexpr int kBlockK = 128;      // one stage of the rings
-constexpr int kHalfK = 64;        // one stage of channels in TMEM: 32 columns
+constexpr int kHalfK = 64;        // a row of 128 bytes in fp16
 constexpr int kWStageBytes = kCtaN * kBlockK;
-constexpr int kMaxAStages = 8;
+constexpr int kMaxAStages = 4;      // stages of channels in TMEM, 64 columns each; at most the rings' stages
 constexpr int kMaxStages = 12;
 constexpr int kRingBytes = 200 * 1024;
-constexpr int kTileThreads = 512;
+constexpr int kConvGroups = 4;    // converter warpgroups: half (g & 1) of every second stage
+constexpr int kTileThreads = 256 + 128 * kConvGroups;
 constexpr long long kWaitClocks = 2000000000ll;   // about a second (clock64: the nanosecond timer is slow to read)
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
@@ -206,8 +207,9 @@ struct TileParams {
 };
 
 struct TileShared {
-    uint64_t x_full[kMaxStages], x_empty[kMaxStages], w_full[kMaxStages], w_empty[kMaxStages];
-    uint64_t a_full[kMaxAStages], a_empty[kMaxAStages], d_full[2], d_empty[2], idle;
+    uint64_t x_full[kMaxStages], w_full[kMaxStages], w_empty[kMaxStages];
+    uint64_t done[kMaxStages];   // a stage's MMAs: its tokens and its channels in TMEM may be overwritten
+    uint64_t a_full[kMaxAStages], d_full[2], d_empty[2], idle;
     uint32_t tmem;
     volatile int failed;
 };
@@ -222,7 +224,7 @@ __device__ __forceinline__ void bar_arrive(uint64_t* b) {
 __device__ __forceinline__ void bar_arrive_first(uint64_t* b) {
     uint32_t r;
     asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(b)));
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(r) : "memory");
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(r) : "memory");
 }
 __device__ __forceinline__ void bar_expect(uint64_t* b, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(b)), "r"(bytes) : "memory");
@@ -231,7 +233,7 @@ __device__ __forceinline__ bool bar_poll(uint64_t* b, uint32_t parity) {
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, 100000;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 100000;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
         : "r"(smem_u32(b)), "r"(parity)
@@ -372,13 +374,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
     if (threadIdx.x == 0) {
         for (int i = 0; i < p.stages; ++i) {
             bar_init(&s.x_full[i], rank == 0 ? 2 : 1);               // its own copies, and the other CTA's word on its
-            bar_init(&s.x_empty[i], 1);
+            bar_init(&s.done[i], 1);
             bar_init(&s.w_full[i], 1);
             bar_init(&s.w_empty[i], 8);
         }
         for (int i = 0; i < p.a_stages; ++i) {
-            bar_init(&s.a_full[i], 8);                               // four warps of either CTA
-            bar_init(&s.a_empty[i], 1);
+            bar_init(&s.a_full[i], 16);                              // eight warps of either CTA
         }
         for (int i = 0; i < 2; ++i) {
             bar_init(&s.d_full[i], 1);
@@ -407,7 +408,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
         for (int u = first; u < pieces && ok; u += pairs) {
             const Piece w = piece(p, u);
             for (int h = w.h0; h < w.h1; h += 2) {
-                if (!(ok = bar_wait(&s.x_empty[r.i], r.ph ^ 1, s))) break;
+                if (!(ok = bar_wait(&s.done[r.i], r.ph ^ 1, s))) break;
                 const bool two = h + 1 < w.h1;
                 bar_expect(&s.x_full[r.i], two ? x_stage : x_half);
                 unsigned char* d = xs + r.i * x_stage;
@@ -449,20 +450,18 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
             if (!(ok = bar_wait(&s.d_empty[d.i], d.ph ^ 1, s))) break;
             fence_after();
             const uint32_t acc = tmem + d.i * p.nt;
-            for (int h = w.h0; h < w.h1 && ok; h += 2) {
-                if (!(ok = bar_wait(&s.x_full[x.i], x.ph, s))) break;
-                for (int g = 0; g < 2 && h + g < w.h1; ++g) {
-                    if (!(ok = bar_wait(&s.a_full[a.i], a.ph, s))) break;
-                    fence_after();
-                    const uint64_t desc = smem_desc(smem_u32(xs + x.i * x_stage + g * x_half));
-                    const uint32_t at = a_col0 + a.i * 32;
+            for (int h = w.h0; h < w.h1; h += 2) {
+                if (!(ok = bar_wait(&s.x_full[x.i], x.ph, s)) || !(ok = bar_wait(&s.a_full[a.i], a.ph, s))) break;
+                fence_after();
+                const uint64_t desc = smem_desc(smem_u32(xs + x.i * x_stage));
+                const uint32_t at = a_col0 + a.i * 64;
+                const int nk = min(8, 4 * (w.h1 - h));
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) mma_ts(acc, at + 8 * k, desc + 2 * k, idesc, h > w.h0 || g > 0 || k > 0);
-                    mma_commit(&s.a_empty[a.i]);
-                    a.next(p.a_stages);
-                }
-                mma_commit(&s.x_empty[x.i]);
+                for (int k = 0; k < 8; ++k)
+                    if (k < nk) mma_ts(acc, at + 8 * k, desc + (k & 3) * 2 + (k >> 2) * (x_half >> 4), idesc, h > w.h0 || k > 0);
+                mma_commit(&s.done[x.i]);
                 x.next(p.stages);
+                a.next(p.a_stages);
             }
             if (ok) mma_commit(&s.d_full[d.i]);
             d.next(2);
@@ -515,43 +514,40 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
             }
             d.next(2);
         }
-    } else if (warp >= 8) {                             // converters: warpgroup g takes half g of each stage
-        const int g = (warp - 8) >> 2, q = warp & 3, row = q * 32 + lane;
-        Ring w, a;
+    } else if (warp >= 8) {                             // converters
+        const int g = (warp - 8) >> 2, half = g & 1, turn = g >> 1, q = warp & 3, row = q * 32 + lane;
+        Ring w, a, e;                                    // e: the stage that last held this one's columns of TMEM
         const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
+        int block = 0;
         bool ok = true;
         for (int u = first; u < pieces && ok; u += pairs) {
             const Piece pc = piece(p, u);
-            for (int h = pc.h0; h < pc.h1; h += 2) {
-                if (!(ok = __all_sync(0xffffffffu, bar_wait(&s.w_full[w.i], w.ph, s)))) break;
-                const bool mine = h + g < pc.h1;
-                uint32_t r[32];
-                if (mine) {
+            for (int h = pc.h0; h < pc.h1; h += 2, ++block) {
+                if (block % (kConvGroups / 2) == turn) {
+                    if (!(ok = __all_sync(0xffffffffu, bar_wait(&s.w_full[w.i], w.ph, s)))) break;
+                    uint32_t r[32];
                     const unsigned char* src = wsm + w.i * kWStageBytes + row * kBlockK;
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        const int4 v = *reinterpret_cast<const int4*>(src + (((4 * g + c) ^ (row & 7)) << 4));
+                        const int4 v = *reinterpret_cast<const int4*>(src + (((4 * half + c) ^ (row & 7)) << 4));
                         widen4(v.x, r[8 * c], r[8 * c + 1]);
                         widen4(v.y, r[8 * c + 2], r[8 * c + 3]);
                         widen4(v.z, r[8 * c + 4], r[8 * c + 5]);
                         widen4(v.w, r[8 * c + 6], r[8 * c + 7]);
                     }
-                }
-                __syncwarp();
-                if (lane == 0) bar_arrive(&s.w_empty[w.i]);
-                w.next(p.stages);
-                if (g == 1) a.next(p.a_stages);          // past half 0's stage
-                if (mine) {
-                    if (!(ok = __all_sync(0xffffffffu, bar_wait(&s.a_empty[a.i], a.ph ^ 1, s)))) break;
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(&s.w_empty[w.i]);
+                    if (block >= p.a_stages && !(ok = __all_sync(0xffffffffu, bar_wait(&s.done[e.i], e.ph, s)))) break;
                     fence_after();
-                    tmem_st32(a_col0 + a.i * 32 + lane_base, r);
+                    tmem_st32(a_col0 + a.i * 64 + half * 32 + lane_base, r);
                     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                     fence_before();
                     __syncwarp();
                     if (lane == 0) bar_arrive_first(&s.a_full[a.i]);
-                    a.next(p.a_stages);
                 }
-                if (g == 0 && h + 1 < pc.h1) a.next(p.a_stages);   // past half 1's
+                w.next(p.stages);
+                a.next(p.a_stages);
+                if (block >= p.a_stages) e.next(p.stages);
             }
         }
     }
@@ -750,7 +746,7 @@ extern "C" int q8_matmul(const int8_t* a, int64_t lda, const float* a_scale, con
     p.group = 8;
     const int stage = p.nt * 128 + kWStageBytes;
     p.stages = kRingBytes / stage < kMaxStages ? kRingBytes / stage : kMaxStages;
-    const int a_room = (512 - (2 * p.nt + 31) / 32 * 32) / 32;
+    const int a_room = (512 - (2 * p.nt + 31) / 32 * 32) / 64;
     p.a_stages = a_room < kMaxAStages ? a_room : kMaxAStages;
     p.M = static_cast<int32_t>(M);
     p.N = static_cast<int32_t>(N);
