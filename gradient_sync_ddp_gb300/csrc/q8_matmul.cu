@@ -210,6 +210,7 @@ struct TileShared {
     uint64_t x_full[kMaxStages], w_full[kMaxStages], w_empty[kMaxStages];
     uint64_t done[kMaxStages];   // a stage's MMAs: its tokens and its channels in TMEM may be overwritten
     uint64_t a_full[kMaxAStages], d_full[2], d_empty[2], idle;
+    float sa[4][kMaxNT];         // the tile's token scales, a copy for each epilogue warp
     uint32_t tmem;
     volatile int failed;
 };
@@ -482,35 +483,44 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
     } else if (warp >= 4 && warp < 8) {                 // epilogue
         Ring d;
         const int q = warp & 3;
+        float* sa = s.sa[q];
         for (int u = first; u < pieces; u += pairs) {
             const Piece w = piece(p, u);
             const int64_t n = w.n0 + rank * kCtaN + q * 32 + lane;
+            const int cols = min(p.nt, p.M - w.m0);
+            const bool in = n < p.N;
+            float swn = 1.0f;
+            __syncwarp();
+            if constexpr (OUT != kTilePart) {           // fetched while the tile is still being summed
+                if (in) swn = p.sw[n];
+                for (int m = lane; m < cols; m += 32) sa[m] = p.sa[w.m0 + m];
+            }
             const bool ok = bar_wait(&s.d_full[d.i], d.ph, s) && !s.failed;
             fence_after();
-            const float swn = OUT != kTilePart && n < p.N ? p.sw[n] : 0.0f;
-            float* part = static_cast<float*>(p.out) + static_cast<int64_t>(w.split) * p.M * p.N;
+            if (!ok) swn = __int_as_float(0x7fffffff);
+            __syncwarp();
+            const int64_t ld = OUT == kTilePart ? p.N : p.ldo;
+            constexpr int ES = OUT == kTileBf16 ? 2 : 4;
+            char* o = static_cast<char*>(p.out) + ((OUT == kTilePart ? static_cast<int64_t>(w.split) * p.M * p.N : 0) + w.m0 * ld + n) * ES;
             const uint32_t acc = tmem + d.i * p.nt + (static_cast<uint32_t>(q * 32) << 16);
             for (int c = 0; c < p.nt; c += 16) {
                 float v[16];
-                __syncwarp();
                 tmem_ld16(acc + c, v);
                 if (c + 16 >= p.nt) {
                     fence_before();
                     __syncwarp();
                     if (lane == 0) bar_arrive_first(&s.d_empty[d.i]);
                 }
-                if (n < p.N) {
+                if (c + 16 <= cols) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const int m = w.m0 + c + j;
-                        if (m >= p.M) break;
-                        if constexpr (OUT == kTilePart) {
-                            part[static_cast<int64_t>(m) * p.N + n] = ok ? v[j] : __int_as_float(0x7fffffff);
-                        } else {
-                            store_elem<OUT == kTileBf16>(p.out, m * p.ldo + n, ok ? v[j] * __ldg(p.sa + m) * swn : __int_as_float(0x7fffffff));
-                        }
-                    }
+                    for (int j = 0; j < 16; ++j, o += ld * ES)
+                        if (in) store_elem<OUT == kTileBf16>(o, 0, OUT == kTilePart ? v[j] * swn : v[j] * sa[c + j] * swn);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j, o += ld * ES)
+                        if (in && c + j < cols) store_elem<OUT == kTileBf16>(o, 0, OUT == kTilePart ? v[j] * swn : v[j] * sa[c + j] * swn);
                 }
+                __syncwarp();
             }
             d.next(2);
         }
