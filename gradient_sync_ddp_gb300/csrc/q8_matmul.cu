@@ -17,8 +17,8 @@
 //     two producers  TMA, 128 of K at a time: the CTA's half of the tokens
 //                    [NT/2][2 x 64] fp16 and its 128 channels [128][128] int8
 //                    (both in the 128-byte swizzle), each into its own ring
-//     converters     four warpgroups, a channel row per thread, each its half
-//                    of every second stage: 64 bytes from shared memory, widened in
+//     converters     two warpgroups, a channel row per thread, each its half
+//                    of the 128: 64 bytes from shared memory, widened in
 //                    registers, stored to TMEM; channels thus cost 8 bits of
 //                    L2 and shared memory
 //     one issuer     (of the pair's first CTA) tcgen05.mma.cta_group::2, A
@@ -44,15 +44,14 @@ namespace {
 constexpr int kMaxK = 131071;     // |Σ| < 2^31
 constexpr int kFewTokens = 8;
 constexpr int kCtaN = 128;        // channels per CTA; 256 per pair: the MMA's rows
-constexpr int kMaxNT = 192;       // tokens per tile: 2 accumulators of 192 columns + 2 channel stages of 64 = 512
+constexpr int kMaxNT = 256;       // tokens per tile: an accumulator of 256 columns + 4 channel stages of 64 = 512
 constexpr int kBlockK = 128;      // one stage of the rings
 constexpr int kHalfK = 64;        // a row of 128 bytes in fp16
 constexpr int kWStageBytes = kCtaN * kBlockK;
 constexpr int kMaxAStages = 4;      // stages of channels in TMEM, 64 columns each; at most the rings' stages
 constexpr int kMaxStages = 12;
-constexpr int kRingBytes = 200 * 1024;
-constexpr int kConvGroups = 4;    // converter warpgroups: half (g & 1) of every second stage
-constexpr int kTileThreads = 256 + 128 * kConvGroups;
+constexpr int kRingBytes = 212 * 1024;
+constexpr int kTileThreads = 640;  // 4 warps of single roles, 8 of the epilogue, 8 converters
 constexpr long long kWaitClocks = 2000000000ll;   // about a second (clock64: the nanosecond timer is slow to read)
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
@@ -203,14 +202,15 @@ struct TileParams {
     const float* sw;
     void* out;       // or the parts, float [splits][M][N]
     int64_t ldo;
-    int32_t M, N, halves, nt, m_tiles, n_tiles, group, splits, blocks_per_split, stages, a_stages;
+    int32_t M, N, halves, nt, m_tiles, n_tiles, group, splits, blocks_per_split, stages, a_stages, d_stages;
 };
 
 struct TileShared {
     uint64_t x_full[kMaxStages], w_full[kMaxStages], w_empty[kMaxStages];
+    uint64_t ready[kMaxStages];  // of the first CTA: both CTAs' tokens are in shared memory, their channels in TMEM
     uint64_t done[kMaxStages];   // a stage's MMAs: its tokens and its channels in TMEM may be overwritten
-    uint64_t a_full[kMaxAStages], d_full[2], d_empty[2], idle;
-    float sa[4][kMaxNT];         // the tile's token scales, a copy for each epilogue warp
+    uint64_t d_full[2], d_empty[2], idle;
+    float sa[8][kMaxNT / 2];     // token scales of each epilogue warp's columns
     uint32_t tmem;
     volatile int failed;
 };
@@ -235,6 +235,17 @@ __device__ __forceinline__ bool bar_poll(uint64_t* b, uint32_t parity) {
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 100000;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(b)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool bar_test(uint64_t* b, uint32_t parity) {   // does not wait
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
         : "r"(smem_u32(b)), "r"(parity)
@@ -374,17 +385,15 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
     unsigned char* wsm = xs + p.stages * x_stage;                    // [stages][128][128]
     if (threadIdx.x == 0) {
         for (int i = 0; i < p.stages; ++i) {
-            bar_init(&s.x_full[i], rank == 0 ? 2 : 1);               // its own copies, and the other CTA's word on its
+            bar_init(&s.x_full[i], 1);
+            bar_init(&s.ready[i], 18);                               // of either CTA: eight warps, and word of its tokens
             bar_init(&s.done[i], 1);
             bar_init(&s.w_full[i], 1);
             bar_init(&s.w_empty[i], 8);
         }
-        for (int i = 0; i < p.a_stages; ++i) {
-            bar_init(&s.a_full[i], 16);                              // eight warps of either CTA
-        }
         for (int i = 0; i < 2; ++i) {
             bar_init(&s.d_full[i], 1);
-            bar_init(&s.d_empty[i], 8);
+            bar_init(&s.d_empty[i], 16);
         }
         bar_init(&s.idle, 1);
         s.failed = 0;
@@ -398,7 +407,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
     __syncthreads();
     pair_sync();
     fence_after();
-    const uint32_t tmem = s.tmem, a_col0 = tmem + (2 * p.nt + 31) / 32 * 32;
+    const uint32_t tmem = s.tmem, a_col0 = tmem + (p.d_stages * p.nt + 31) / 32 * 32;
     pdl_enter();
     const int pieces = p.m_tiles * p.n_tiles * p.splits, first = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
@@ -443,121 +452,145 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
             bar_drain(&s.w_full[r.i], r.ph, s);
         }
     } else if (warp == 1 && lane == 0 && rank == 0) {   // issuer
-        Ring x, a, d;
+        Ring x, d;
+        int a = 0;
         const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(p.nt / 8) << 17) | ((2 * kCtaN / 16u) << 24);
-        bool ok = true;
+        bool ok = true, there = false;
         for (int u = first; u < pieces && ok; u += pairs) {
             const Piece w = piece(p, u);
             if (!(ok = bar_wait(&s.d_empty[d.i], d.ph ^ 1, s))) break;
-            fence_after();
             const uint32_t acc = tmem + d.i * p.nt;
             for (int h = w.h0; h < w.h1; h += 2) {
-                if (!(ok = bar_wait(&s.x_full[x.i], x.ph, s)) || !(ok = bar_wait(&s.a_full[a.i], a.ph, s))) break;
+                if (!there && !(ok = bar_wait(&s.ready[x.i], x.ph, s))) break;
                 fence_after();
                 const uint64_t desc = smem_desc(smem_u32(xs + x.i * x_stage));
-                const uint32_t at = a_col0 + a.i * 64;
-                const int nk = min(8, 4 * (w.h1 - h));
+                const uint32_t at = a_col0 + a * 64;
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (k < nk) mma_ts(acc, at + 8 * k, desc + (k & 3) * 2 + (k >> 2) * (x_half >> 4), idesc, h > w.h0 || k > 0);
+                for (int k = 0; k < 4; ++k) mma_ts(acc, at + 8 * k, desc + 2 * k, idesc, h > w.h0 || k > 0);
+                // A look at the next stage while these four run: a barrier costs 120 to 300 clocks to look at even
+                // where it is ready, in which the tensor cores would run dry (1140 clocks a stage, for MMAs of 768).
+                Ring y = x;
+                y.next(p.stages);
+                there = bar_test(&s.ready[y.i], y.ph);
+                if (h + 1 < w.h1) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) mma_ts(acc, at + 32 + 8 * k, desc + (x_half >> 4) + 2 * k, idesc, true);
+                }
                 mma_commit(&s.done[x.i]);
-                x.next(p.stages);
-                a.next(p.a_stages);
+                x = y;
+                a = a + 1 == p.a_stages ? 0 : a + 1;
             }
             if (ok) mma_commit(&s.d_full[d.i]);
-            d.next(2);
+            d.next(p.d_stages);
         }
         mma_commit(&s.idle);
         bar_drain(&s.idle, 0, s);
-    } else if (warp == 1 && lane == 0) {                // the second CTA's tokens are there: told to the first
+    } else if (warp == 3 && lane == 0) {                // this CTA's tokens are there: told to the first
         Ring x;
         bool ok = true;
         for (int u = first; u < pieces && ok; u += pairs) {
             const Piece w = piece(p, u);
             for (int h = w.h0; h < w.h1; h += 2) {
                 if (!(ok = bar_wait(&s.x_full[x.i], x.ph, s))) break;
-                bar_arrive_first(&s.x_full[x.i]);
+                bar_arrive_first(&s.ready[x.i]);
                 x.next(p.stages);
             }
         }
-    } else if (warp >= 4 && warp < 8) {                 // epilogue
+    } else if (warp >= 4 && warp < 12) {                // epilogue: warp's channels, half of the tokens
         Ring d;
-        const int q = warp & 3;
-        float* sa = s.sa[q];
+        const int q = warp & 3, c0 = warp < 8 ? 0 : (p.nt / 2 + 15) / 16 * 16, c1 = warp < 8 ? (p.nt / 2 + 15) / 16 * 16 : p.nt;
+        float* sa = s.sa[warp - 4];
+        const int64_t ld = OUT == kTilePart ? p.N : p.ldo;
+        constexpr int ES = OUT == kTileBf16 ? 2 : 4;
+        constexpr int BATCH = OUT == kTileBf16 ? 8 : 4;   // chunks of 16 columns held in 64 registers
         for (int u = first; u < pieces; u += pairs) {
             const Piece w = piece(p, u);
             const int64_t n = w.n0 + rank * kCtaN + q * 32 + lane;
-            const int cols = min(p.nt, p.M - w.m0);
+            const int cols = min(c1, p.M - w.m0);
             const bool in = n < p.N;
             float swn = 1.0f;
             __syncwarp();
             if constexpr (OUT != kTilePart) {           // fetched while the tile is still being summed
                 if (in) swn = p.sw[n];
-                for (int m = lane; m < cols; m += 32) sa[m] = p.sa[w.m0 + m];
+                for (int c = c0 + lane; c < cols; c += 32) sa[c - c0] = p.sa[w.m0 + c];
             }
             const bool ok = bar_wait(&s.d_full[d.i], d.ph, s) && !s.failed;
             fence_after();
             if (!ok) swn = __int_as_float(0x7fffffff);
             __syncwarp();
-            const int64_t ld = OUT == kTilePart ? p.N : p.ldo;
-            constexpr int ES = OUT == kTileBf16 ? 2 : 4;
-            char* o = static_cast<char*>(p.out) + ((OUT == kTilePart ? static_cast<int64_t>(w.split) * p.M * p.N : 0) + w.m0 * ld + n) * ES;
+            char* o = static_cast<char*>(p.out) + ((OUT == kTilePart ? static_cast<int64_t>(w.split) * p.M * p.N : 0) + (w.m0 + c0) * ld + n) * ES;
             const uint32_t acc = tmem + d.i * p.nt + (static_cast<uint32_t>(q * 32) << 16);
-            for (int c = 0; c < p.nt; c += 16) {
-                float v[16];
-                tmem_ld16(acc + c, v);
-                if (c + 16 >= p.nt) {
+            if (c0 >= c1 && lane == 0) bar_arrive_first(&s.d_empty[d.i]);   // a tile of 16 tokens
+            // The accumulator is read into registers and given back before anything is stored: the next tile waits for it.
+            for (int b = c0; b < c1; b += 16 * BATCH) {
+                uint32_t r[BATCH][ES == 2 ? 8 : 16];
+#pragma unroll
+                for (int i = 0; i < BATCH; ++i) {
+                    const int c = b + 16 * i;
+                    if (c >= c1) break;
+                    float v[16];
+                    tmem_ld16(acc + c, v);
+                    if constexpr (ES == 2) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) r[i][j] = pack2(v[2 * j] * sa[c - c0 + 2 * j] * swn, v[2 * j + 1] * sa[c - c0 + 2 * j + 1] * swn);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) r[i][j] = __float_as_uint(OUT == kTilePart ? v[j] * swn : v[j] * sa[c - c0 + j] * swn);
+                    }
+                }
+                if (b + 16 * BATCH >= c1) {
                     fence_before();
                     __syncwarp();
                     if (lane == 0) bar_arrive_first(&s.d_empty[d.i]);
                 }
-                if (c + 16 <= cols) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j, o += ld * ES)
-                        if (in) store_elem<OUT == kTileBf16>(o, 0, OUT == kTilePart ? v[j] * swn : v[j] * sa[c + j] * swn);
-                } else {
+                for (int i = 0; i < BATCH; ++i) {
+                    const int c = b + 16 * i;
+                    if (c >= cols) break;
 #pragma unroll
-                    for (int j = 0; j < 16; ++j, o += ld * ES)
-                        if (in && c + j < cols) store_elem<OUT == kTileBf16>(o, 0, OUT == kTilePart ? v[j] * swn : v[j] * sa[c + j] * swn);
+                    for (int j = 0; j < 16; ++j, o += ld * ES) {
+                        if (!in || c + j >= cols) continue;
+                        if constexpr (ES == 2) *reinterpret_cast<unsigned short*>(o) = static_cast<unsigned short>(r[i][j / 2] >> (16 * (j & 1)));
+                        else *reinterpret_cast<uint32_t*>(o) = r[i][j];
+                    }
                 }
-                __syncwarp();
             }
-            d.next(2);
+            d.next(p.d_stages);
         }
-    } else if (warp >= 8) {                             // converters
-        const int g = (warp - 8) >> 2, half = g & 1, turn = g >> 1, q = warp & 3, row = q * 32 + lane;
-        Ring w, a, e;                                    // e: the stage that last held this one's columns of TMEM
+    } else if (warp >= 12) {                            // converters
+        const int half = (warp - 12) >> 2, q = warp & 3, row = q * 32 + lane;
+        Ring w, e;                                       // e: the stage that last held this one's columns of TMEM
         const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
-        int block = 0;
+        int block = 0, a = 0;
         bool ok = true;
         for (int u = first; u < pieces && ok; u += pairs) {
             const Piece pc = piece(p, u);
             for (int h = pc.h0; h < pc.h1; h += 2, ++block) {
-                if (block % (kConvGroups / 2) == turn) {
-                    if (!(ok = __all_sync(0xffffffffu, bar_wait(&s.w_full[w.i], w.ph, s)))) break;
-                    uint32_t r[32];
-                    const unsigned char* src = wsm + w.i * kWStageBytes + row * kBlockK;
+                if (!(ok = __all_sync(0xffffffffu, bar_wait(&s.w_full[w.i], w.ph, s)))) break;
+                uint32_t r[32];
+                const unsigned char* src = wsm + w.i * kWStageBytes + row * kBlockK;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const int4 v = *reinterpret_cast<const int4*>(src + (((4 * half + c) ^ (row & 7)) << 4));
-                        widen4(v.x, r[8 * c], r[8 * c + 1]);
-                        widen4(v.y, r[8 * c + 2], r[8 * c + 3]);
-                        widen4(v.z, r[8 * c + 4], r[8 * c + 5]);
-                        widen4(v.w, r[8 * c + 6], r[8 * c + 7]);
-                    }
-                    __syncwarp();
-                    if (lane == 0) bar_arrive(&s.w_empty[w.i]);
-                    if (block >= p.a_stages && !(ok = __all_sync(0xffffffffu, bar_wait(&s.done[e.i], e.ph, s)))) break;
-                    fence_after();
-                    tmem_st32(a_col0 + a.i * 64 + half * 32 + lane_base, r);
-                    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-                    fence_before();
-                    __syncwarp();
-                    if (lane == 0) bar_arrive_first(&s.a_full[a.i]);
+                for (int c = 0; c < 4; ++c) {
+                    const int4 v = *reinterpret_cast<const int4*>(src + (((4 * half + c) ^ (row & 7)) << 4));
+                    widen4(v.x, r[8 * c], r[8 * c + 1]);
+                    widen4(v.y, r[8 * c + 2], r[8 * c + 3]);
+                    widen4(v.z, r[8 * c + 4], r[8 * c + 5]);
+                    widen4(v.w, r[8 * c + 6], r[8 * c + 7]);
                 }
+                __syncwarp();
+                if (lane == 0) bar_arrive(&s.w_empty[w.i]);
+                if (block >= p.a_stages) {
+                    if (!(ok = __all_sync(0xffffffffu, bar_wait(&s.done[e.i], e.ph, s)))) break;
+                    e.next(p.stages);
+                }
+                fence_after();
+                tmem_st32(a_col0 + a * 64 + half * 32 + lane_base, r);
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                fence_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive_first(&s.ready[w.i]);
                 w.next(p.stages);
-                a.next(p.a_stages);
-                if (block >= p.a_stages) e.next(p.stages);
+                a = a + 1 == p.a_stages ? 0 : a + 1;
             }
         }
     }
@@ -756,8 +789,8 @@ extern "C" int q8_matmul(const int8_t* a, int64_t lda, const float* a_scale, con
     p.group = 8;
     const int stage = p.nt * 128 + kWStageBytes;
     p.stages = kRingBytes / stage < kMaxStages ? kRingBytes / stage : kMaxStages;
-    const int a_room = (512 - (2 * p.nt + 31) / 32 * 32) / 64;
-    p.a_stages = a_room < kMaxAStages ? a_room : kMaxAStages;
+    p.d_stages = p.nt <= kMaxNT / 2 ? 2 : 1;        // narrow tiles: two accumulators
+    p.a_stages = p.stages < kMaxAStages ? p.stages : kMaxAStages;
     p.M = static_cast<int32_t>(M);
     p.N = static_cast<int32_t>(N);
     p.sa = a_scale;

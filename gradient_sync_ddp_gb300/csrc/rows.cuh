@@ -29,6 +29,12 @@ __device__ __forceinline__ char* row_ptr(void* base, int64_t row, int64_t ld) {
     return static_cast<char*>(base) + row * ld * (BF16 ? 2 : 4);
 }
 
+// Two values rounded to bf16 by one instruction, the first in the low half.
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
 // Sum / maximum over the CTA, in every thread; MaxOp leaves NaN out (its
 // callers carry NaN through a sum), MaxNanOp carries it.  `sh` holds one float per
 // warp and is free again when the call returns.
