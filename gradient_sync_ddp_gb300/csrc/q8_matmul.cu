@@ -275,6 +275,12 @@ __device__ __forceinline__ void bar_drain(uint64_t* b, uint32_t parity, TileShar
         }
     }
 }
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect() {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+    return ok != 0;
+}
 __device__ __forceinline__ void pair_sync() {
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
@@ -407,7 +413,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
     __syncthreads();
     pair_sync();
     fence_after();
-    const uint32_t tmem = s.tmem, a_col0 = tmem + (p.d_stages * p.nt + 31) / 32 * 32;
+    // all 512 columns are this pair's, from address 0 on
+    const uint32_t a_col0 = (p.d_stages * p.nt + 31) / 32 * 32, xs_addr = smem_u32(xs);
     pdl_enter();
     const int pieces = p.m_tiles * p.n_tiles * p.splits, first = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
@@ -451,40 +458,48 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
             r.back(p.stages);
             bar_drain(&s.w_full[r.i], r.ph, s);
         }
-    } else if (warp == 1 && lane == 0 && rank == 0) {   // issuer
+    } else if (warp == 1 && rank == 0) {                // issuer: the whole warp, so that descriptors stay in uniform registers
         Ring x, d;
         int a = 0;
         const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(p.nt / 8) << 17) | ((2 * kCtaN / 16u) << 24);
+        const bool one = elect();
         bool ok = true, there = false;
         for (int u = first; u < pieces && ok; u += pairs) {
             const Piece w = piece(p, u);
-            if (!(ok = bar_wait(&s.d_empty[d.i], d.ph ^ 1, s))) break;
-            const uint32_t acc = tmem + d.i * p.nt;
+            if (!(ok = __all_sync(0xffffffffu, bar_wait(&s.d_empty[d.i], d.ph ^ 1, s)))) break;
+            const uint32_t acc = d.i * p.nt;
             for (int h = w.h0; h < w.h1; h += 2) {
-                if (!there && !(ok = bar_wait(&s.ready[x.i], x.ph, s))) break;
+                if (!there && !(ok = __all_sync(0xffffffffu, bar_wait(&s.ready[x.i], x.ph, s)))) break;
                 fence_after();
-                const uint64_t desc = smem_desc(smem_u32(xs + x.i * x_stage));
+                const uint64_t desc = smem_desc(xs_addr + x.i * x_stage);
                 const uint32_t at = a_col0 + a * 64;
+                if (one) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) mma_ts(acc, at + 8 * k, desc + 2 * k, idesc, h > w.h0 || k > 0);
+                    for (int k = 0; k < 4; ++k) mma_ts(acc, at + 8 * k, desc + 2 * k, idesc, h > w.h0 || k > 0);
+                }
                 // A look at the next stage while these four run: a barrier costs 120 to 300 clocks to look at even
-                // where it is ready, in which the tensor cores would run dry (1140 clocks a stage, for MMAs of 768).
+                // where it is ready, in which the tensor cores would run dry.
                 Ring y = x;
                 y.next(p.stages);
-                there = bar_test(&s.ready[y.i], y.ph);
-                if (h + 1 < w.h1) {
+                there = __all_sync(0xffffffffu, bar_test(&s.ready[y.i], y.ph));
+                if (one) {
+                    if (h + 1 < w.h1) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) mma_ts(acc, at + 32 + 8 * k, desc + (x_half >> 4) + 2 * k, idesc, true);
+                        for (int k = 0; k < 4; ++k) mma_ts(acc, at + 32 + 8 * k, desc + (x_half >> 4) + 2 * k, idesc, true);
+                    }
+                    mma_commit(&s.done[x.i]);
                 }
-                mma_commit(&s.done[x.i]);
+                __syncwarp();
                 x = y;
                 a = a + 1 == p.a_stages ? 0 : a + 1;
             }
-            if (ok) mma_commit(&s.d_full[d.i]);
+            if (ok && one) mma_commit(&s.d_full[d.i]);
             d.next(p.d_stages);
         }
-        mma_commit(&s.idle);
-        bar_drain(&s.idle, 0, s);
+        if (one) {
+            mma_commit(&s.idle);
+            bar_drain(&s.idle, 0, s);
+        }
     } else if (warp == 3 && lane == 0) {                // this CTA's tokens are there: told to the first
         Ring x;
         bool ok = true;
@@ -519,7 +534,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
             if (!ok) swn = __int_as_float(0x7fffffff);
             __syncwarp();
             char* o = static_cast<char*>(p.out) + ((OUT == kTilePart ? static_cast<int64_t>(w.split) * p.M * p.N : 0) + (w.m0 + c0) * ld + n) * ES;
-            const uint32_t acc = tmem + d.i * p.nt + (static_cast<uint32_t>(q * 32) << 16);
+            const uint32_t acc = d.i * p.nt + (static_cast<uint32_t>(q * 32) << 16);
             if (c0 >= c1 && lane == 0) bar_arrive_first(&s.d_empty[d.i]);   // a tile of 16 tokens
             // The accumulator is read into registers and given back before anything is stored: the next tile waits for it.
             for (int b = c0; b < c1; b += 16 * BATCH) {
@@ -599,7 +614,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
     __syncthreads();
     pair_sync();                                        // nothing of the pair's is in flight any more
     fence_after();
-    if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(s.tmem) : "memory");
 }
 
 struct CombineParams {
