@@ -314,118 +314,163 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_loop_kernel(const __gr
     }
 }
 
-// Backward, rows of a CTA (warp) grid-stride; a thread's columns are the same
-// for every row, except with EDGE, where the aligned grid shifts from row to
-// row: there dγ's part is kept in shared memory, by column.
-template <bool BF16, bool DYBF16, int VPT, bool EDGE, bool WARP>
+// N values of a matrix as they lie in memory.
+template <bool BF16, int N>
+struct Packed {
+    static constexpr int W = N * (BF16 ? 2 : 4) / 4;
+    uint32_t w[W];
+    __device__ __forceinline__ void load(const char* p) {
+        if constexpr (W == 2) {
+            asm volatile("ld.global.cs.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p) : "memory");
+        } else {
+#pragma unroll
+            for (int q = 0; q < W / 4; ++q) {
+                const uint4 v = ld16<false>(p + 16 * q);
+                w[4 * q] = v.x;
+                w[4 * q + 1] = v.y;
+                w[4 * q + 2] = v.z;
+                w[4 * q + 3] = v.w;
+            }
+        }
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < W; ++i) w[i] = 0;
+    }
+    __device__ __forceinline__ float at(int e) const {
+        if constexpr (BF16) return e & 1 ? bf16_hi(w[e >> 1]) : bf16_lo(w[e >> 1]);
+        else return __uint_as_float(w[e]);
+    }
+};
+
+// Backward, aligned rows, grid-stride: a row's dy, h and dh are all on their
+// way before the first is used, and stay packed in registers.  A thread's
+// columns are the same for every row, so its part of dγ is in registers too.
+template <bool BF16, bool DYBF16, int VPT, bool WARP>
 __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : max_group(BF16, VPT))
     norm_grad_kernel(const __grid_constant__ NormGradParams a) {
     constexpr int ES = BF16 ? 2 : 4, VEC = 16 / ES, YS = DYBF16 ? 2 : 4;
-    extern __shared__ float part_sh[];   // [WARP ? kWarpRows : 1][D] where a.partial
+    extern __shared__ float part_sh[];   // WARP and a.partial: [kWarpRows][D]
     __shared__ float sh[32];
     pdl_enter();
-    const int G = WARP ? 32 : blockDim.x;
+    const int G = WARP ? 32 : blockDim.x, nvec = a.D / VEC;
     const int t = WARP ? threadIdx.x & 31 : threadIdx.x;
     const int w = WARP ? threadIdx.x >> 5 : 0;
     const bool want = a.partial != nullptr;
-    float* mine = part_sh + w * a.D;
-    float acc[EDGE ? 1 : VPT][EDGE ? 1 : VEC] = {};
-    if (EDGE && want) {
-        for (int d = t; d < a.D; d += G) mine[d] = 0.0f;
-        if (WARP) __syncwarp();
-        else __syncthreads();
-    }
+    float acc[VPT][VEC] = {};
     const int64_t stride = static_cast<int64_t>(gridDim.x) * (WARP ? kWarpRows : 1);
     for (int64_t row = static_cast<int64_t>(blockIdx.x) * (WARP ? kWarpRows : 1) + w; row < a.rows; row += stride) {
         const char* dy = row_ptr<DYBF16>(a.dy, row, a.lddy);
         const char* hp = row_ptr<BF16>(a.h, row, a.ldh);
         const char* dh = a.dh ? row_ptr<BF16>(a.dh, row, a.lddh) : nullptr;
         char* dx = row_ptr<BF16>(a.dx, row, a.lddx);
-        const RowShape s = row_shape<BF16, EDGE>(hp, a.D);
-        float g[VPT][VEC], n[VPT][VEC], ge = 0.0f, ne = 0.0f;
+        Packed<DYBF16, VEC> g[VPT];
+        Packed<BF16, VEC> h[VPT], r[VPT];
         const float rstd = a.rstd[row];
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int v = t + i * G;
-            if (v < s.nvec) {
-                load_n<DYBF16, VEC>(dy + (s.lead + v * VEC) * YS, g[i]);
-                load_n<BF16, VEC>(hp + (s.lead + v * VEC) * ES, n[i]);
+            if (v < nvec) {
+                g[i].load(dy + v * VEC * YS);
+                h[i].load(hp + v * VEC * ES);
+                if (dh) r[i].load(dh + v * VEC * ES);
+                else r[i].zero();
             } else {
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) g[i][e] = n[i][e] = 0.0f;
+                g[i].zero();
+                h[i].zero();
             }
-        }
-        const bool has_edge = EDGE && t < s.edges;
-        const int de = EDGE ? edge_elem<VEC>(s, t) : 0;
-        if (has_edge) {
-            ge = load_elem<DYBF16>(dy, de);
-            ne = load_elem<BF16>(hp, de) * rstd;
         }
         float sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int v = t + i * G;
-            if (v >= s.nvec) break;
-            const int d0 = s.lead + v * VEC;
+            if (v >= nvec) break;
             float gm[VEC];
-            load_gamma<EDGE, VEC>(a.gamma, d0, gm);
+            load_gamma<false, VEC>(a.gamma, v * VEC, gm);
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
-                n[i][e] *= rstd;
-                if constexpr (EDGE) {
-                    if (want) mine[d0 + e] = fmaf(g[i][e], n[i][e], mine[d0 + e]);
-                } else {
-                    acc[i][e] = fmaf(g[i][e], n[i][e], acc[i][e]);
-                }
-                g[i][e] *= gm[e];
-                sum = fmaf(g[i][e], n[i][e], sum);
+                const float gn = g[i].at(e) * (h[i].at(e) * rstd);
+                acc[i][e] += gn;
+                sum = fmaf(gn, gm[e], sum);
             }
-        }
-        if (has_edge) {
-            if (want) mine[de] = fmaf(ge, ne, mine[de]);
-            if (a.gamma) ge *= a.gamma[de];
-            sum = fmaf(ge, ne, sum);
         }
         const float c = (WARP ? warp_all<SumOp>(sum) : block_all<SumOp>(sum, sh)) / a.D;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int v = t + i * G;
-            if (v >= s.nvec) break;
-            float o[VEC];
-            if (dh != nullptr) {
-                load_n<BF16, VEC>(dh + (s.lead + v * VEC) * ES, o);
+            if (v >= nvec) break;
+            float gm[VEC], o[VEC];
+            load_gamma<false, VEC>(a.gamma, v * VEC, gm);
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) o[e] = fmaf(rstd, g[i][e] - n[i][e] * c, o[e]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) o[e] = rstd * (g[i][e] - n[i][e] * c);
-            }
-            store_n<BF16, VEC>(dx + (s.lead + v * VEC) * ES, o);
+            for (int e = 0; e < VEC; ++e) o[e] = fmaf(rstd, g[i].at(e) * gm[e] - h[i].at(e) * rstd * c, r[i].at(e));
+            store_n<BF16, VEC>(dx + v * VEC * ES, o);
         }
-        if (has_edge) store_elem<BF16>(dx, de, fmaf(rstd, ge - ne * c, dh ? load_elem<BF16>(dh, de) : 0.0f));
-        if (EDGE && WARP) __syncwarp();   // another lane takes over a column
     }
     if (!want) return;
     float* out = a.partial + static_cast<int64_t>(blockIdx.x) * a.D;
-    if constexpr (!EDGE) {
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int v = t + i * G;
-            if (v * VEC >= a.D) break;
-            float* d = (WARP ? mine : out) + v * VEC;
+    for (int i = 0; i < VPT; ++i) {
+        const int v = t + i * G;
+        if (v >= nvec) break;
+        float4* d = reinterpret_cast<float4*>((WARP ? part_sh + w * a.D : out) + v * VEC);
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) d[e] = acc[i][e];
-        }
-        if (!WARP) return;
+        for (int q = 0; q < VEC / 4; ++q) d[q] = make_float4(acc[i][4 * q], acc[i][4 * q + 1], acc[i][4 * q + 2], acc[i][4 * q + 3]);
     }
-    __syncthreads();
-    for (int d = threadIdx.x; d < a.D; d += blockDim.x) {
-        float v = part_sh[d];
-        if constexpr (WARP) {
+    if constexpr (WARP) {
+        __syncthreads();
+        for (int d = threadIdx.x; d < a.D; d += 32 * kWarpRows) {
+            float v = part_sh[d];
 #pragma unroll
             for (int i = 1; i < kWarpRows; ++i) v += part_sh[i * a.D + d];
+            out[d] = v;
         }
-        out[d] = v;
+    }
+}
+
+// Backward, rows that lie anywhere: an element at a time, each thread the
+// same EPT columns of every row.
+template <bool BF16, bool DYBF16, int EPT>
+__global__ void __launch_bounds__(1024) norm_grad_elem_kernel(const __grid_constant__ NormGradParams a) {
+    __shared__ float sh[32];
+    pdl_enter();
+    const int G = blockDim.x, t = threadIdx.x;
+    float acc[EPT] = {};
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        const void* dy = row_ptr<DYBF16>(a.dy, row, a.lddy);
+        const void* hp = row_ptr<BF16>(a.h, row, a.ldh);
+        const void* dh = a.dh ? row_ptr<BF16>(a.dh, row, a.lddh) : nullptr;
+        void* dx = row_ptr<BF16>(a.dx, row, a.lddx);
+        float g[EPT], n[EPT], r[EPT];
+        const float rstd = a.rstd[row];
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) {
+            const int d = t + i * G;
+            const bool in = d < a.D;
+            g[i] = in ? load_elem<DYBF16>(dy, d) : 0.0f;
+            n[i] = in ? load_elem<BF16>(hp, d) : 0.0f;
+            r[i] = in && dh ? load_elem<BF16>(dh, d) : 0.0f;
+        }
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) {
+            const int d = t + i * G;
+            n[i] *= rstd;
+            acc[i] = fmaf(g[i], n[i], acc[i]);
+            if (a.gamma && d < a.D) g[i] *= __ldg(a.gamma + d);
+            sum = fmaf(g[i], n[i], sum);
+        }
+        const float c = block_all<SumOp>(sum, sh) / a.D;
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) {
+            const int d = t + i * G;
+            if (d < a.D) store_elem<BF16>(dx, d, fmaf(rstd, g[i] - n[i] * c, r[i]));
+        }
+    }
+    if (a.partial == nullptr) return;
+#pragma unroll
+    for (int i = 0; i < EPT; ++i) {
+        const int d = t + i * G;
+        if (d < a.D) a.partial[static_cast<int64_t>(blockIdx.x) * a.D + d] = acc[i];
     }
 }
 
@@ -435,22 +480,24 @@ struct GammaParams {
     int32_t n, D;
 };
 
-// dγ[d] = Σ over the CTAs' parts, in a fixed order: 32 columns per CTA, 32
-// threads per column over interleaved parts, then those 32 in order.
+// dγ[d] = Σ over the CTAs' parts, in a fixed order: 16 columns per CTA, 64
+// threads per column over interleaved parts, then those 64 by halves.
 __global__ void __launch_bounds__(1024) norm_gamma_kernel(const __grid_constant__ GammaParams a) {
-    __shared__ float sh[32][33];
+    __shared__ float sh[64][17];
     pdl_enter();
-    const int c = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const int d = blockIdx.x * 32 + c;
+    const int c = threadIdx.x & 15, w = threadIdx.x >> 4;
+    const int d = blockIdx.x * 16 + c;
     float s = 0.0f;
     if (d < a.D) {
-#pragma unroll 8
-        for (int i = w; i < a.n; i += 32) s += a.partial[static_cast<int64_t>(i) * a.D + d];
+#pragma unroll 10
+        for (int i = w; i < a.n; i += 64) s += a.partial[static_cast<int64_t>(i) * a.D + d];
     }
     sh[w][c] = s;
     __syncthreads();
-    s = warp_all<SumOp>(sh[c][w]);     // warp w: column w's 32 sums
-    if (c == 0 && blockIdx.x * 32 + w < a.D) a.dgamma[blockIdx.x * 32 + w] = s;
+    if (threadIdx.x >= 512) return;
+    const int col = threadIdx.x >> 5, l = threadIdx.x & 31;      // a warp per column
+    s = warp_all<SumOp>(sh[l][col] + sh[l + 32][col]);
+    if (l == 0 && blockIdx.x * 16 + col < a.D) a.dgamma[blockIdx.x * 16 + col] = s;
 }
 
 constexpr int kGradCtas = 608;   // at most this many parts of dγ
@@ -486,7 +533,7 @@ Group pick_group(int64_t rows, int D, bool bf16, int sms) {
     const int vec = bf16 ? 8 : 4, nv = (D + vec - 1) / vec;
     if (nv <= 32) return {1, 32, true};
     const bool few = rows < 2ll * sms;
-    if (!few && nv <= 128) return {nv <= 64 ? 2 : 4, 32, true};
+    if (!few && nv <= 128) return {(nv + 31) / 32, 32, true};
     for (int vpt = few ? 1 : 2; vpt <= 4; vpt *= 2) {
         const int t = ((nv + vpt - 1) / vpt + 31) / 32 * 32;
         if (t <= max_group(bf16, vpt)) return {vpt, t, false};
@@ -496,7 +543,7 @@ Group pick_group(int64_t rows, int D, bool bf16, int sms) {
 
 template <bool BF16, int OUT, bool EDGE>
 void (*fwd_kernel(const Group& g))(NormParams) {
-    if (g.warp) return g.vpt == 1 ? norm_kernel<BF16, OUT, 1, EDGE, true> : g.vpt == 2 ? norm_kernel<BF16, OUT, 2, EDGE, true> : norm_kernel<BF16, OUT, 4, EDGE, true>;
+    if (g.warp) return g.vpt == 1 ? norm_kernel<BF16, OUT, 1, EDGE, true> : g.vpt == 2 ? norm_kernel<BF16, OUT, 2, EDGE, true> : g.vpt == 3 ? norm_kernel<BF16, OUT, 3, EDGE, true> : norm_kernel<BF16, OUT, 4, EDGE, true>;
     return g.vpt == 1 ? norm_kernel<BF16, OUT, 1, EDGE, false> : g.vpt == 2 ? norm_kernel<BF16, OUT, 2, EDGE, false> : norm_kernel<BF16, OUT, 4, EDGE, false>;
 }
 template <bool BF16, int OUT>
@@ -504,15 +551,42 @@ void (*fwd_kernel(Lay lay, const Group& g))(NormParams) {
     if (lay == Lay::kDifferent || g.threads == 0) return norm_loop_kernel<BF16, OUT>;
     return lay == Lay::kAligned ? fwd_kernel<BF16, OUT, false>(g) : fwd_kernel<BF16, OUT, true>(g);
 }
-template <bool BF16, bool DYBF16, bool EDGE>
-void (*bwd_kernel(const Group& g))(NormGradParams) {
-    if (g.warp) return g.vpt == 1 ? norm_grad_kernel<BF16, DYBF16, 1, EDGE, true> : g.vpt == 2 ? norm_grad_kernel<BF16, DYBF16, 2, EDGE, true> : norm_grad_kernel<BF16, DYBF16, 4, EDGE, true>;
-    return g.vpt == 1 ? norm_grad_kernel<BF16, DYBF16, 1, EDGE, false> : g.vpt == 2 ? norm_grad_kernel<BF16, DYBF16, 2, EDGE, false> : norm_grad_kernel<BF16, DYBF16, 4, EDGE, false>;
+template <bool BF16, bool DYBF16>
+void (*bwd_vec(const Group& g))(NormGradParams) {
+    if (g.warp) return g.vpt == 1 ? norm_grad_kernel<BF16, DYBF16, 1, true> : g.vpt == 2 ? norm_grad_kernel<BF16, DYBF16, 2, true> : g.vpt == 3 ? norm_grad_kernel<BF16, DYBF16, 3, true> : norm_grad_kernel<BF16, DYBF16, 4, true>;
+    return g.vpt == 1 ? norm_grad_kernel<BF16, DYBF16, 1, false> : g.vpt == 2 ? norm_grad_kernel<BF16, DYBF16, 2, false> : norm_grad_kernel<BF16, DYBF16, 4, false>;
 }
 template <bool BF16, bool DYBF16>
-void (*bwd_kernel(Lay lay, const Group& g))(NormGradParams) {
-    if (lay == Lay::kDifferent || g.threads == 0) return norm_grad_loop_kernel<BF16, DYBF16>;
-    return lay == Lay::kAligned ? bwd_kernel<BF16, DYBF16, false>(g) : bwd_kernel<BF16, DYBF16, true>(g);
+void (*bwd_elem(int ept))(NormGradParams) {
+    return ept == 1 ? norm_grad_elem_kernel<BF16, DYBF16, 1> : ept == 2 ? norm_grad_elem_kernel<BF16, DYBF16, 2> : ept <= 4 ? norm_grad_elem_kernel<BF16, DYBF16, 4> : norm_grad_elem_kernel<BF16, DYBF16, 8>;
+}
+
+// How rmsnorm_backward runs: kernel, threads, CTAs, shared memory.
+struct GradPlan {
+    void (*kernel)(NormGradParams);
+    int threads, ctas;
+    size_t smem;
+};
+template <bool BF16, bool DYBF16>
+GradPlan grad_plan(Lay lay, int64_t rows, int D, bool want, int sms) {
+    const Group g = pick_group(rows, D, BF16, sms);
+    GradPlan p{norm_grad_loop_kernel<BF16, DYBF16>, kNormThreads, 0, 0};
+    int64_t rows_per_cta = 1;
+    if (lay == Lay::kAligned && g.threads != 0) {
+        p.kernel = bwd_vec<BF16, DYBF16>(g);
+        p.threads = g.warp ? 32 * kWarpRows : g.threads;
+        rows_per_cta = g.warp ? kWarpRows : 1;
+        p.smem = g.warp && want ? static_cast<size_t>(kWarpRows) * D * 4 : 0;
+    } else if (D <= 8192) {
+        const int ept = D <= 128 ? 1 : D <= 512 ? 2 : D <= 4096 ? 4 : 8;
+        p.kernel = bwd_elem<BF16, DYBF16>(ept);
+        p.threads = ((D + ept - 1) / ept + 31) / 32 * 32;
+    }
+    const int per_sm = p.threads >= 1024 ? 1 : p.threads >= 512 ? 2 : p.threads > 256 ? 3 : 4;
+    const int64_t cap = static_cast<int64_t>(sms) * per_sm < kGradCtas ? sms * per_sm : kGradCtas;
+    const int64_t ctas = (rows + rows_per_cta - 1) / rows_per_cta;
+    p.ctas = static_cast<int>(ctas < cap ? ctas : cap);
+    return p;
 }
 
 int forward(const void* x, int64_t ldx, const void* residual, int64_t ldr, int32_t in_dtype, const float* gamma,
@@ -617,22 +691,15 @@ extern "C" int rmsnorm_backward(const void* dy, int64_t lddy, int32_t dy_dtype, 
         const bool b = h_dtype == DDP_BF16, c = dy_dtype == DDP_BF16;
         const Mat* const mats[4] = {&mh, &my, &md, &mo};
         const Lay lay = layout(mats, 4, D, b ? 8 : 4, gamma);
-        const Group g = pick_group(rows, D, b, d.sm_count);
-        const bool loop = lay == Lay::kDifferent || g.threads == 0;
-        void (*kernel)(NormGradParams) = b ? (c ? bwd_kernel<true, true>(lay, g) : bwd_kernel<true, false>(lay, g))
-                                           : (c ? bwd_kernel<false, true>(lay, g) : bwd_kernel<false, false>(lay, g));
-        const int threads = loop ? kNormThreads : g.warp ? 32 * kWarpRows : g.threads;
-        const int64_t ctas = !loop && g.warp ? (rows + kWarpRows - 1) / kWarpRows : rows;
-        const int per_sm = threads >= 1024 ? 1 : threads >= 512 ? 2 : threads > 256 ? 3 : 4;
-        const int64_t cap = static_cast<int64_t>(d.sm_count) * per_sm < kGradCtas ? d.sm_count * per_sm : kGradCtas;
-        parts = static_cast<int>(ctas < cap ? ctas : cap);
-        const size_t smem = loop || !dgamma || (lay == Lay::kAligned && !g.warp)
-                                ? 0 : static_cast<size_t>(g.warp ? kWarpRows : 1) * D * 4;
-        if ((st = launch_smem(kernel, static_cast<unsigned>(parts), threads, smem, s, p)) != DDP_OK) return st;
+        const bool want = dgamma != nullptr;
+        const GradPlan g = b ? (c ? grad_plan<true, true>(lay, rows, D, want, d.sm_count) : grad_plan<true, false>(lay, rows, D, want, d.sm_count))
+                             : (c ? grad_plan<false, true>(lay, rows, D, want, d.sm_count) : grad_plan<false, false>(lay, rows, D, want, d.sm_count));
+        parts = g.ctas;
+        if ((st = launch_smem(g.kernel, static_cast<unsigned>(g.ctas), g.threads, g.smem, s, p)) != DDP_OK) return st;
     }
     if (dgamma) {
         const GammaParams q{static_cast<const float*>(workspace), dgamma, parts, D};
-        return launch_pdl(norm_gamma_kernel, dim3(static_cast<unsigned>((D + 31) / 32)), 1024, s, q);
+        return launch_pdl(norm_gamma_kernel, dim3(static_cast<unsigned>((D + 15) / 16)), 1024, s, q);
     }
     return DDP_OK;
 }
