@@ -160,7 +160,7 @@ __device__ __forceinline__ void load_gamma(const float* gamma, int d, float (&o)
     }
 }
 
-constexpr int kWarpRows = 8;      // rows per CTA of the warp-per-row kernels
+constexpr int kWarpRows = 8;      // rows per CTA of the warp-per-row forward kernels
 constexpr int max_group(bool bf16, int vpt) { return vpt * (bf16 ? 8 : 4) > 16 ? 512 : 1024; }
 
 // Forward: VPT vectors per thread.  WARP: a warp per row, kWarpRows per CTA; else a CTA per row.
@@ -346,11 +346,17 @@ struct Packed {
 // Backward, aligned rows, grid-stride: a row's dy, h and dh are all on their
 // way before the first is used, and stay packed in registers.  A thread's
 // columns are the same for every row, so its part of dγ is in registers too.
-template <bool BF16, bool DYBF16, int VPT, bool WARP>
-__global__ void __launch_bounds__(WARP ? 32 * kWarpRows : max_group(BF16, VPT))
+// AHEAD: the next row is fetched before this one is reduced.
+// Rows per CTA of the warp-per-row kernel: one CTA per SM, so that dγ has few
+// parts and a warp has 128 registers (8192 x 768 bf16: 13.9 us with 16 warps, 14.6 with 8 and two CTAs per SM, 16.0 with
+// 4 and four; three CTAs of 8 spill).
+constexpr int kGradRows = 16;
+
+template <bool BF16, bool DYBF16, int VPT, bool WARP, bool AHEAD>
+__global__ void __launch_bounds__(WARP ? 32 * kGradRows : AHEAD ? 512 : max_group(BF16, VPT))
     norm_grad_kernel(const __grid_constant__ NormGradParams a) {
     constexpr int ES = BF16 ? 2 : 4, VEC = 16 / ES, YS = DYBF16 ? 2 : 4;
-    extern __shared__ float part_sh[];   // WARP and a.partial: [kWarpRows][D]
+    extern __shared__ float part_sh[];   // WARP and a.partial: [kGradRows][D]
     __shared__ float sh[32];
     pdl_enter();
     const int G = WARP ? 32 : blockDim.x, nvec = a.D / VEC;
@@ -358,27 +364,33 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : max_group(BF16, VPT))
     const int w = WARP ? threadIdx.x >> 5 : 0;
     const bool want = a.partial != nullptr;
     float acc[VPT][VEC] = {};
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * (WARP ? kWarpRows : 1);
-    for (int64_t row = static_cast<int64_t>(blockIdx.x) * (WARP ? kWarpRows : 1) + w; row < a.rows; row += stride) {
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * (WARP ? kGradRows : 1);
+    Packed<DYBF16, VEC> g[VPT], g2[AHEAD ? VPT : 1];
+    Packed<BF16, VEC> h[VPT], r[VPT], h2[AHEAD ? VPT : 1], r2[AHEAD ? VPT : 1];
+    float rstd = 0.0f, rstd2 = 0.0f;
+    auto fetch = [&](int64_t row, Packed<DYBF16, VEC>* gg, Packed<BF16, VEC>* hh, Packed<BF16, VEC>* rr, float& rs) {
         const char* dy = row_ptr<DYBF16>(a.dy, row, a.lddy);
         const char* hp = row_ptr<BF16>(a.h, row, a.ldh);
         const char* dh = a.dh ? row_ptr<BF16>(a.dh, row, a.lddh) : nullptr;
-        char* dx = row_ptr<BF16>(a.dx, row, a.lddx);
-        Packed<DYBF16, VEC> g[VPT];
-        Packed<BF16, VEC> h[VPT], r[VPT];
-        const float rstd = a.rstd[row];
+        rs = a.rstd[row];
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int v = t + i * G;
             if (v < nvec) {
-                g[i].load(dy + v * VEC * YS);
-                h[i].load(hp + v * VEC * ES);
-                if (dh) r[i].load(dh + v * VEC * ES);
-                else r[i].zero();
-            } else {
-                g[i].zero();
-                h[i].zero();
+                gg[i].load(dy + v * VEC * YS);
+                hh[i].load(hp + v * VEC * ES);
+                if (dh) rr[i].load(dh + v * VEC * ES);
+                else rr[i].zero();
             }
+        }
+    };
+    int64_t row = static_cast<int64_t>(blockIdx.x) * (WARP ? kGradRows : 1) + w;
+    if (AHEAD && row < a.rows) fetch(row, g, h, r, rstd);
+    for (; row < a.rows; row += stride) {
+        if constexpr (AHEAD) {
+            if (row + stride < a.rows) fetch(row + stride, g2, h2, r2, rstd2);
+        } else {
+            fetch(row, g, h, r, rstd);
         }
         float sum = 0.0f;
 #pragma unroll
@@ -395,6 +407,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : max_group(BF16, VPT))
             }
         }
         const float c = (WARP ? warp_all<SumOp>(sum) : block_all<SumOp>(sum, sh)) / a.D;
+        char* dx = row_ptr<BF16>(a.dx, row, a.lddx);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int v = t + i * G;
@@ -404,6 +417,15 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : max_group(BF16, VPT))
 #pragma unroll
             for (int e = 0; e < VEC; ++e) o[e] = fmaf(rstd, g[i].at(e) * gm[e] - h[i].at(e) * rstd * c, r[i].at(e));
             store_n<BF16, VEC>(dx + v * VEC * ES, o);
+        }
+        if constexpr (AHEAD) {
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                g[i] = g2[i];
+                h[i] = h2[i];
+                r[i] = r2[i];
+            }
+            rstd = rstd2;
         }
     }
     if (!want) return;
@@ -418,60 +440,58 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : max_group(BF16, VPT))
     }
     if constexpr (WARP) {
         __syncthreads();
-        for (int d = threadIdx.x; d < a.D; d += 32 * kWarpRows) {
+        for (int d = threadIdx.x; d < a.D; d += 32 * kGradRows) {
             float v = part_sh[d];
 #pragma unroll
-            for (int i = 1; i < kWarpRows; ++i) v += part_sh[i * a.D + d];
+            for (int i = 1; i < kGradRows; ++i) v += part_sh[i * a.D + d];
             out[d] = v;
         }
     }
 }
 
 // Backward, rows that lie anywhere: an element at a time, each thread the
-// same EPT columns of every row.
-template <bool BF16, bool DYBF16, int EPT>
-__global__ void __launch_bounds__(1024) norm_grad_elem_kernel(const __grid_constant__ NormGradParams a) {
+// same EPT columns of every row (γ and its part of dγ in registers), G threads.
+template <bool BF16, bool DYBF16, int G, int EPT>
+__global__ void __launch_bounds__(G, G * EPT <= 512 ? 1024 / G : G <= 512 ? (EPT <= 4 ? 3 : 2) : 1)
+    norm_grad_elem_kernel(const __grid_constant__ NormGradParams a) {
+    constexpr int ES = BF16 ? 2 : 4, YS = DYBF16 ? 2 : 4;
     __shared__ float sh[32];
     pdl_enter();
-    const int G = blockDim.x, t = threadIdx.x;
-    float acc[EPT] = {};
+    const int t = threadIdx.x;
+    float acc[EPT] = {}, gm[EPT];
+#pragma unroll
+    for (int i = 0; i < EPT; ++i) gm[i] = t + i * G < a.D && a.gamma ? __ldg(a.gamma + t + i * G) : 1.0f;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-        const void* dy = row_ptr<DYBF16>(a.dy, row, a.lddy);
-        const void* hp = row_ptr<BF16>(a.h, row, a.ldh);
-        const void* dh = a.dh ? row_ptr<BF16>(a.dh, row, a.lddh) : nullptr;
-        void* dx = row_ptr<BF16>(a.dx, row, a.lddx);
+        const char* dy = row_ptr<DYBF16>(a.dy, row, a.lddy) + t * YS;
+        const char* hp = row_ptr<BF16>(a.h, row, a.ldh) + t * ES;
+        const char* dh = row_ptr<BF16>(a.dh, row, a.lddh) + t * ES;
         float g[EPT], n[EPT], r[EPT];
         const float rstd = a.rstd[row];
 #pragma unroll
         for (int i = 0; i < EPT; ++i) {
-            const int d = t + i * G;
-            const bool in = d < a.D;
-            g[i] = in ? load_elem<DYBF16>(dy, d) : 0.0f;
-            n[i] = in ? load_elem<BF16>(hp, d) : 0.0f;
-            r[i] = in && dh ? load_elem<BF16>(dh, d) : 0.0f;
+            const bool in = t + i * G < a.D;
+            g[i] = in ? load_elem<DYBF16>(dy + i * G * YS, 0) : 0.0f;
+            n[i] = in ? load_elem<BF16>(hp + i * G * ES, 0) : 0.0f;
+            r[i] = in && a.dh ? load_elem<BF16>(dh + i * G * ES, 0) : 0.0f;
         }
         float sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < EPT; ++i) {
-            const int d = t + i * G;
             n[i] *= rstd;
             acc[i] = fmaf(g[i], n[i], acc[i]);
-            if (a.gamma && d < a.D) g[i] *= __ldg(a.gamma + d);
+            g[i] *= gm[i];
             sum = fmaf(g[i], n[i], sum);
         }
         const float c = block_all<SumOp>(sum, sh) / a.D;
+        char* dx = row_ptr<BF16>(a.dx, row, a.lddx) + t * ES;
 #pragma unroll
-        for (int i = 0; i < EPT; ++i) {
-            const int d = t + i * G;
-            if (d < a.D) store_elem<BF16>(dx, d, fmaf(rstd, g[i] - n[i] * c, r[i]));
-        }
+        for (int i = 0; i < EPT; ++i)
+            if (t + i * G < a.D) store_elem<BF16>(dx + i * G * ES, 0, fmaf(rstd, g[i] - n[i] * c, r[i]));
     }
     if (a.partial == nullptr) return;
 #pragma unroll
-    for (int i = 0; i < EPT; ++i) {
-        const int d = t + i * G;
-        if (d < a.D) a.partial[static_cast<int64_t>(blockIdx.x) * a.D + d] = acc[i];
-    }
+    for (int i = 0; i < EPT; ++i)
+        if (t + i * G < a.D) a.partial[static_cast<int64_t>(blockIdx.x) * a.D + t + i * G] = acc[i];
 }
 
 struct GammaParams {
@@ -553,12 +573,22 @@ void (*fwd_kernel(Lay lay, const Group& g))(NormParams) {
 }
 template <bool BF16, bool DYBF16>
 void (*bwd_vec(const Group& g))(NormGradParams) {
-    if (g.warp) return g.vpt == 1 ? norm_grad_kernel<BF16, DYBF16, 1, true> : g.vpt == 2 ? norm_grad_kernel<BF16, DYBF16, 2, true> : g.vpt == 3 ? norm_grad_kernel<BF16, DYBF16, 3, true> : norm_grad_kernel<BF16, DYBF16, 4, true>;
-    return g.vpt == 1 ? norm_grad_kernel<BF16, DYBF16, 1, false> : g.vpt == 2 ? norm_grad_kernel<BF16, DYBF16, 2, false> : norm_grad_kernel<BF16, DYBF16, 4, false>;
+    if (g.warp) return g.vpt == 1 ? norm_grad_kernel<BF16, DYBF16, 1, true, false> : g.vpt == 2 ? norm_grad_kernel<BF16, DYBF16, 2, true, false> : g.vpt == 3 ? norm_grad_kernel<BF16, DYBF16, 3, true, false> : norm_grad_kernel<BF16, DYBF16, 4, true, false>;
+    // fetching ahead needs more than 64 registers: 8192 x 4096 bf16 at 52 us with it, 53 without
+    if (g.threads <= 512 && g.vpt <= 2) return g.vpt == 1 ? norm_grad_kernel<BF16, DYBF16, 1, false, true> : norm_grad_kernel<BF16, DYBF16, 2, false, true>;
+    return g.vpt == 1 ? norm_grad_kernel<BF16, DYBF16, 1, false, false> : g.vpt == 2 ? norm_grad_kernel<BF16, DYBF16, 2, false, false> : norm_grad_kernel<BF16, DYBF16, 4, false, false>;
 }
+// Element kernels by width: threads, kernel.
 template <bool BF16, bool DYBF16>
-void (*bwd_elem(int ept))(NormGradParams) {
-    return ept == 1 ? norm_grad_elem_kernel<BF16, DYBF16, 1> : ept == 2 ? norm_grad_elem_kernel<BF16, DYBF16, 2> : ept <= 4 ? norm_grad_elem_kernel<BF16, DYBF16, 4> : norm_grad_elem_kernel<BF16, DYBF16, 8>;
+int bwd_elem(int D, void (**k)(NormGradParams)) {
+    if (D <= 128) return *k = norm_grad_elem_kernel<BF16, DYBF16, 128, 1>, 128;
+    if (D <= 512) return *k = norm_grad_elem_kernel<BF16, DYBF16, 128, 4>, 128;
+    if (D <= 1024) return *k = norm_grad_elem_kernel<BF16, DYBF16, 256, 4>, 256;
+    if (D <= 2048) return *k = norm_grad_elem_kernel<BF16, DYBF16, 512, 4>, 512;
+    if (D <= 512 * 6) return *k = norm_grad_elem_kernel<BF16, DYBF16, 512, 6>, 512;
+    if (D <= 4608) return *k = norm_grad_elem_kernel<BF16, DYBF16, 512, 9>, 512;
+    if (D <= 8192) return *k = norm_grad_elem_kernel<BF16, DYBF16, 1024, 8>, 1024;
+    return *k = norm_grad_loop_kernel<BF16, DYBF16>, kNormThreads;
 }
 
 // How rmsnorm_backward runs: kernel, threads, CTAs, shared memory.
@@ -568,25 +598,23 @@ struct GradPlan {
     size_t smem;
 };
 template <bool BF16, bool DYBF16>
-GradPlan grad_plan(Lay lay, int64_t rows, int D, bool want, int sms) {
+int grad_plan(Lay lay, int64_t rows, int D, bool want, int sms, GradPlan* p) {
     const Group g = pick_group(rows, D, BF16, sms);
-    GradPlan p{norm_grad_loop_kernel<BF16, DYBF16>, kNormThreads, 0, 0};
     int64_t rows_per_cta = 1;
+    p->smem = 0;
     if (lay == Lay::kAligned && g.threads != 0) {
-        p.kernel = bwd_vec<BF16, DYBF16>(g);
-        p.threads = g.warp ? 32 * kWarpRows : g.threads;
-        rows_per_cta = g.warp ? kWarpRows : 1;
-        p.smem = g.warp && want ? static_cast<size_t>(kWarpRows) * D * 4 : 0;
-    } else if (D <= 8192) {
-        const int ept = D <= 128 ? 1 : D <= 512 ? 2 : D <= 4096 ? 4 : 8;
-        p.kernel = bwd_elem<BF16, DYBF16>(ept);
-        p.threads = ((D + ept - 1) / ept + 31) / 32 * 32;
+        p->kernel = bwd_vec<BF16, DYBF16>(g);
+        p->threads = g.warp ? 32 * kGradRows : g.threads;
+        rows_per_cta = g.warp ? kGradRows : 1;
+        p->smem = g.warp && want ? static_cast<size_t>(kGradRows) * D * 4 : 0;
+    } else {
+        p->threads = bwd_elem<BF16, DYBF16>(D, &p->kernel);
     }
-    const int per_sm = p.threads >= 1024 ? 1 : p.threads >= 512 ? 2 : p.threads > 256 ? 3 : 4;
-    const int64_t cap = static_cast<int64_t>(sms) * per_sm < kGradCtas ? sms * per_sm : kGradCtas;
+    // one wave, and few enough parts of dγ
     const int64_t ctas = (rows + rows_per_cta - 1) / rows_per_cta;
-    p.ctas = static_cast<int>(ctas < cap ? ctas : cap);
-    return p;
+    const int st = one_wave_grid(reinterpret_cast<const void*>(p->kernel), p->threads, ctas, &p->ctas);
+    if (p->ctas > kGradCtas) p->ctas = kGradCtas;
+    return st;
 }
 
 int forward(const void* x, int64_t ldx, const void* residual, int64_t ldr, int32_t in_dtype, const float* gamma,
@@ -692,8 +720,10 @@ extern "C" int rmsnorm_backward(const void* dy, int64_t lddy, int32_t dy_dtype, 
         const Mat* const mats[4] = {&mh, &my, &md, &mo};
         const Lay lay = layout(mats, 4, D, b ? 8 : 4, gamma);
         const bool want = dgamma != nullptr;
-        const GradPlan g = b ? (c ? grad_plan<true, true>(lay, rows, D, want, d.sm_count) : grad_plan<true, false>(lay, rows, D, want, d.sm_count))
-                             : (c ? grad_plan<false, true>(lay, rows, D, want, d.sm_count) : grad_plan<false, false>(lay, rows, D, want, d.sm_count));
+        GradPlan g;
+        st = b ? (c ? grad_plan<true, true>(lay, rows, D, want, d.sm_count, &g) : grad_plan<true, false>(lay, rows, D, want, d.sm_count, &g))
+               : (c ? grad_plan<false, true>(lay, rows, D, want, d.sm_count, &g) : grad_plan<false, false>(lay, rows, D, want, d.sm_count, &g));
+        if (st != DDP_OK) return st;
         parts = g.ctas;
         if ((st = launch_smem(g.kernel, static_cast<unsigned>(g.ctas), g.threads, g.smem, s, p)) != DDP_OK) return st;
     }
