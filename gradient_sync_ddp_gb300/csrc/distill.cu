@@ -31,6 +31,8 @@ constexpr int kTopPerThread = kMaxTop / kDistillThreads;
 constexpr int kMaxCluster = 8;
 constexpr int kHash = 2 * kMaxTop;
 constexpr int kScanTop = 32;          // up to this many entries repeats are found by scanning all pairs
+constexpr float kLog2eLow = 1.9259629911e-8f;   // log2(e) − kLog2e
+constexpr float kMasked = 1.0e4f;     // logits beyond this are no reference
 constexpr float kFar = 1.0e37f;       // beyond this, z·c may overflow: exponents from (z − max)·c instead
 
 struct DistillParams {
@@ -80,7 +82,7 @@ __device__ __forceinline__ void block_all2(float& a, float& b, float2* sh) {
     __syncthreads();
 }
 
-// Running maximum m of z and Σ 2^(z·c − mc), mc = m·c kept within ±kFar.
+// Largest m of z and Σ 2^(z·c − mc), mc = m·c kept within ±kFar.
 struct Running {
     float m = -INFINITY, mc = 0.0f, s = 0.0f;
     __device__ __forceinline__ void raise(float to, float c) {
@@ -117,43 +119,69 @@ __device__ __forceinline__ int edge(const Slice& s, int e) {
     return s.v0 + (e < s.lead ? e : e + s.nvec * (BF16 ? 8 : 4));
 }
 
-// dz = g·2^(exponent) over a slice, the exponent as FAR says.
-template <bool BF16, bool FAR>
-__device__ __forceinline__ void write_grad(const Slice& s, char* dz, float c, float M, float m, float ls, float g) {
-    constexpr int ES = BF16 ? 2 : 4, VEC = 16 / ES, U = 4;
-    const float off = FAR ? ls : M + ls;
-    auto f = [&](float z) { return g * pow2(FAR ? fmaf(z - m, c, -off) : fmaf(z, c, -off)); };
-    const char* zv = s.base + static_cast<int64_t>(s.v0 + s.lead) * ES;
-    char* dv = dz + static_cast<int64_t>(s.v0 + s.lead) * ES;
-    const bool whole = (reinterpret_cast<uintptr_t>(dv) & 15) == 0;
-    for (int i0 = threadIdx.x; i0 < s.nvec; i0 += kDistillThreads * U) {
+// body(vector index, values) for every 16-byte vector of the slice that is this thread's, U loads in flight.
+template <bool BF16, bool KEEP, class F>
+__device__ __forceinline__ void each_vector(const Slice& s, F body) {
+    constexpr int U = 6;
+    const char* zv = s.base + static_cast<int64_t>(s.v0 + s.lead) * (BF16 ? 2 : 4);
+    int i = threadIdx.x;
+    for (; i + (U - 1) * kDistillThreads < s.nvec; i += U * kDistillThreads) {
         uint4 v[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int i = i0 + u * kDistillThreads;
-            if (i < s.nvec) v[u] = ld16<false>(zv + static_cast<int64_t>(i) * 16);
+            const char* p = zv + static_cast<int64_t>(i + u * kDistillThreads) * 16;
+            v[u] = KEEP ? ld16_keep(p) : ld16<false>(p);
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int i = i0 + u * kDistillThreads;
-            if (i >= s.nvec) break;
-            float o[VEC];
+        for (int u = 0; u < U; ++u) body(i + u * kDistillThreads, v[u]);
+    }
+    uint4 v[U - 1];
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) o[e] = f(vec_elem<BF16>(v[u], e));
-            if (whole) {
-                uint4 w;
-                if constexpr (BF16) w = make_uint4(pack2(o[0], o[1]), pack2(o[2], o[3]), pack2(o[4], o[5]), pack2(o[6], o[7]));
-                else w = f4_bits(o[0], o[1], o[2], o[3]);
-                st16(dv + static_cast<int64_t>(i) * 16, w);
-            } else {
+    for (int u = 0; u < U - 1; ++u) {
+        const char* p = zv + static_cast<int64_t>(i + u * kDistillThreads) * 16;
+        if (i + u * kDistillThreads < s.nvec) v[u] = KEEP ? ld16_keep(p) : ld16<false>(p);
+    }
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) store_elem<BF16>(dv, static_cast<int64_t>(i) * VEC + e, o[e]);
+    for (int u = 0; u < U - 1; ++u)
+        if (i + u * kDistillThreads < s.nvec) body(i + u * kDistillThreads, v[u]);
+}
+
+// dz = g·q over a slice; the exponent of q as FAR says.  A bf16 dz has |g| in the exponent and its sign set
+// afterwards; an fp32 dz keeps them apart, for the larger exponent would round more.
+template <bool BF16, bool FAR, bool KEEP>
+__device__ __forceinline__ void write_grad(const Slice& s, char* dz, float c, float M, float m, float ls, float g) {
+    constexpr int ES = BF16 ? 2 : 4, VEC = 16 / ES;
+    const float off = (FAR ? ls : M + ls) - log2f(fabsf(g));
+    const uint32_t sign = BF16 && g < 0.0f ? 0x80008000u : 0u;
+    auto f = [&](float z) {
+        if constexpr (BF16) return pow2(FAR ? fmaf(z - m, c, -off) : fmaf(z, c, -off));
+        else return g * pow2((FAR ? (z - m) * c : fmaf(z, c, -M)) - ls);
+    };
+    char* dv = dz + static_cast<int64_t>(s.v0 + s.lead) * ES;
+    const bool whole = (reinterpret_cast<uintptr_t>(dv) & 15) == 0;
+    each_vector<BF16, KEEP>(s, [&](int i, const uint4& v) {
+        float o[VEC];
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) o[e] = f(vec_elem<BF16>(v, e));
+        uint4 w;
+        if constexpr (BF16) w = make_uint4(pack2(o[0], o[1]), pack2(o[2], o[3]), pack2(o[4], o[5]), pack2(o[6], o[7]));
+        else w = f4_bits(o[0], o[1], o[2], o[3]);
+        if constexpr (BF16) w = make_uint4(w.x ^ sign, w.y ^ sign, w.z ^ sign, w.w ^ sign);
+        if (whole) {
+            st16(dv + static_cast<int64_t>(i) * 16, w);
+        } else {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                const uint32_t x = e * ES / 4 == 0 ? w.x : e * ES / 4 == 1 ? w.y : e * ES / 4 == 2 ? w.z : w.w;
+                if constexpr (BF16) reinterpret_cast<unsigned short*>(dv)[static_cast<int64_t>(i) * VEC + e] = static_cast<unsigned short>(x >> (16 * (e & 1)));
+                else reinterpret_cast<uint32_t*>(dv)[static_cast<int64_t>(i) * VEC + e] = x;
             }
         }
-    }
+    });
     if (threadIdx.x < s.lead + s.tail) {
         const int v = edge<BF16>(s, threadIdx.x);
-        store_elem<BF16>(dz, v, f(load_elem<BF16>(s.base, v)));
+        const float o = f(load_elem<BF16>(s.base, v));
+        store_elem<BF16>(dz, v, BF16 && g < 0.0f ? -o : o);
     }
 }
 
@@ -173,8 +201,8 @@ __device__ __forceinline__ void write_zero(const Slice& s, char* dz) {
 }
 
 template <bool BF16, bool FWD, bool BWD>
-__global__ void __launch_bounds__(kDistillThreads) distill_kernel(const __grid_constant__ DistillParams a) {
-    constexpr int ES = BF16 ? 2 : 4, VEC = 16 / ES, U = 4;
+__global__ void __launch_bounds__(kDistillThreads, 4) distill_kernel(const __grid_constant__ DistillParams a) {
+    constexpr int VEC = BF16 ? 8 : 4;
     __shared__ float2 sh[kDistillThreads / 32];
     __shared__ float s_part[2];                      // this CTA's (m, s), read by its cluster
     __shared__ int s_idx[kMaxTop];
@@ -211,36 +239,56 @@ __global__ void __launch_bounds__(kDistillThreads) distill_kernel(const __grid_c
         if ((FWD && rank == 0) || (i >= v0 && i < v1)) zi[u] = load_elem<BF16>(z, i);
     }
 
+    // The sum takes no maximum: fp32 holds 2^±126 about any reference near the thread's logits, and its first vector
+    // gives one (0 where that is masked).  A token that a thread's sum leaves the middle of that range for (logits 40
+    // nats above the reference, or masked references and very low logits) is summed again with a running maximum.
     Running run;
     if constexpr (FWD) {
-        const char* zv = z + static_cast<int64_t>(s.v0 + s.lead) * ES;
-        for (int i0 = tid; i0 < s.nvec; i0 += kDistillThreads * U) {
-            uint4 v[U];
+        float s1 = 0.0f;
+        bool begun = false;
+        each_vector<BF16, true>(s, [&](int, const uint4& v) {
+            float x[VEC];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int i = i0 + u * kDistillThreads;
-                if (i < s.nvec) v[u] = ld16_keep(zv + static_cast<int64_t>(i) * 16);
+            for (int e = 0; e < VEC; ++e) x[e] = vec_elem<BF16>(v, e);
+            if (!begun) {
+                begun = true;
+                float top = x[0];
+#pragma unroll
+                for (int e = 1; e < VEC; ++e) top = fmaxf(top, x[e]);
+                run.m = top > -kMasked ? fminf(top, kMasked) : 0.0f;
+                run.mc = run.m * a.c;
             }
+            float lo = 0.0f, hi = 0.0f;
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (i0 + u * kDistillThreads >= s.nvec) break;
-                float x[VEC], top = -INFINITY;
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    x[e] = vec_elem<BF16>(v[u], e);
-                    top = fmaxf(top, x[e]);
-                }
-                run.raise(top, a.c);
-                float part = 0.0f;
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) part += pow2(fmaf(x[e], a.c, -run.mc));
-                run.s += part;
+            for (int e = 0; e < VEC; e += 2) {
+                lo += pow2(fmaf(x[e], a.c, -run.mc));
+                hi += pow2(fmaf(x[e + 1], a.c, -run.mc));
             }
-        }
+            run.s += lo;
+            s1 += hi;
+        });
+        run.s += s1;
+        bool out = begun && !(run.s > 1.0e-18f && run.s < 1.0e18f);
         if (tid < s.lead + s.tail) {
             const float x = load_elem<BF16>(z, edge<BF16>(s, tid));
             run.raise(x, a.c);
             run.s += pow2(fmaf(x, a.c, -run.mc));
+        }
+        if (__syncthreads_or(out)) {
+            run = Running();
+            each_vector<BF16, true>(s, [&](int, const uint4& v) {
+                float top = -INFINITY;
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) top = fmaxf(top, vec_elem<BF16>(v, e));
+                run.raise(top, a.c);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) run.s += pow2(fmaf(vec_elem<BF16>(v, e), a.c, -run.mc));
+            });
+            if (tid < s.lead + s.tail) {
+                const float x = load_elem<BF16>(z, edge<BF16>(s, tid));
+                run.raise(x, a.c);
+                run.s += pow2(fmaf(x, a.c, -run.mc));
+            }
         }
     }
 
@@ -278,7 +326,7 @@ __global__ void __launch_bounds__(kDistillThreads) distill_kernel(const __grid_c
                 sum += ps[r] == 0.0f ? 0.0f : ps[r] * pow2(fminf(fmaxf(pm[r] * a.c, -kFar), kFar) - M);
         }
     } else {
-        M = a.lse_in[row] * kLog2e;
+        M = a.lse_in[row] * kLog2e;      // with what the product rounds off, below
         m = a.lse_in[row] * a.tau;
     }
     // Logits whose product with c may overflow (a row that a mask of the type's lowest value leaves whole): differences first.
@@ -291,7 +339,8 @@ __global__ void __launch_bounds__(kDistillThreads) distill_kernel(const __grid_c
             sum = all;
         }
     }
-    const float ls = FWD ? log2f(sum) : 0.0f;        // q_v = 2^(z·c − M − ls)
+    // q_v = 2^(z·c − M − ls)
+    const float ls = FWD ? log2f(sum) : far ? 0.0f : fmaf(a.lse_in[row], kLog2e, -M) + a.lse_in[row] * kLog2eLow;
     auto q2 = [&](float x) { return (far ? (x - m) * a.c : fmaf(x, a.c, -M)) - ls; };
     if constexpr (FWD) {
         if (rank == 0) {
@@ -318,8 +367,8 @@ __global__ void __launch_bounds__(kDistillThreads) distill_kernel(const __grid_c
         if (!some || g == 0.0f) {
             write_zero<BF16>(s, dz);
         } else {
-            if (far) write_grad<BF16, true>(s, dz, a.c, M, m, ls, g);
-            else write_grad<BF16, false>(s, dz, a.c, M, m, ls, g);
+            if (far) write_grad<BF16, true, !FWD>(s, dz, a.c, M, m, ls, g);
+            else write_grad<BF16, false, !FWD>(s, dz, a.c, M, m, ls, g);
             // the entries: p into shared memory, repeated indices found there
             const bool hash = a.k > kScanTop;
             if (hash)

@@ -91,21 +91,31 @@ __device__ __forceinline__ int4 load16(const int8_t* p, int valid, int align) {
 constexpr int kFewThreads = 256;
 constexpr int kFewChunk = 4096;   // bytes of K of every token in shared memory at a time
 
-// LPR lanes per channel row, R rows per lane group at a time.
-template <int M, int LPR, int R, bool BF16>
+// LPR lanes per channel row, R rows per lane group at a time, U vectors of
+// each in flight: R·U·16 bytes per lane.
+template <int M, int LPR, int R, int U, bool BF16>
 __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant__ FewParams p) {
     extern __shared__ int4 tok[];   // [M][chunk / 16]
     pdl_enter();
     constexpr int GROUPS = kFewThreads / LPR;
     const int g = threadIdx.x / LPR, l = threadIdx.x % LPR;
     const int chunk_vec = min(kFewChunk, (p.K + 15) / 16 * 16) / 16;
-    const bool one_chunk = p.K <= kFewChunk;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * GROUPS * R;
-    for (int64_t n0 = static_cast<int64_t>(blockIdx.x) * GROUPS * R; n0 < p.N; n0 += step) {
+    const int64_t step = static_cast<int64_t>(gridDim.x) * GROUPS * R, begin = static_cast<int64_t>(blockIdx.x) * GROUPS * R;
+    for (int64_t n0 = begin; n0 < p.N; n0 += step) {
         int acc[R][M] = {};
         for (int k0 = 0; k0 < p.K; k0 += kFewChunk) {
             const int kn = min(kFewChunk, p.K - k0), nv = (kn + 15) / 16;
-            if (!one_chunk || n0 == static_cast<int64_t>(blockIdx.x) * GROUPS * R) {
+            auto fetch = [&](int v, int4 (&w)[R]) {
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const int64_t n = n0 + g + static_cast<int64_t>(r) * GROUPS;
+                    w[r] = n < p.N && v < nv ? load16(p.w + n * p.ldw + k0 + 16 * v, kn - 16 * v, p.w_align) : make_int4(0, 0, 0, 0);
+                }
+            };
+            int4 w[U][R];                       // the first channels are on their way before the tokens are staged
+#pragma unroll
+            for (int u = 0; u < U; ++u) fetch(l + u * LPR, w[u]);
+            if (p.K > kFewChunk || n0 == begin) {
                 __syncthreads();
                 for (int i = threadIdx.x; i < M * nv; i += kFewThreads) {
                     const int m = i / nv, v = i - m * nv;
@@ -113,24 +123,27 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant_
                 }
                 __syncthreads();
             }
-            for (int v = l; v < nv; v += LPR) {
-                int4 w[R];
+            for (int v0 = l;; ) {
 #pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    const int64_t n = n0 + g + static_cast<int64_t>(r) * GROUPS;
-                    w[r] = n < p.N ? load16(p.w + n * p.ldw + k0 + 16 * v, kn - 16 * v, p.w_align) : make_int4(0, 0, 0, 0);
-                }
+                for (int u = 0; u < U; ++u) {
+                    const int v = v0 + u * LPR;
+                    if (v >= nv) break;
 #pragma unroll
-                for (int m = 0; m < M; ++m) {
-                    const int4 t = tok[m * chunk_vec + v];
+                    for (int m = 0; m < M; ++m) {
+                        const int4 t = tok[m * chunk_vec + v];
 #pragma unroll
-                    for (int r = 0; r < R; ++r) {
-                        acc[r][m] = __dp4a(w[r].x, t.x, acc[r][m]);
-                        acc[r][m] = __dp4a(w[r].y, t.y, acc[r][m]);
-                        acc[r][m] = __dp4a(w[r].z, t.z, acc[r][m]);
-                        acc[r][m] = __dp4a(w[r].w, t.w, acc[r][m]);
+                        for (int r = 0; r < R; ++r) {
+                            acc[r][m] = __dp4a(w[u][r].x, t.x, acc[r][m]);
+                            acc[r][m] = __dp4a(w[u][r].y, t.y, acc[r][m]);
+                            acc[r][m] = __dp4a(w[u][r].z, t.z, acc[r][m]);
+                            acc[r][m] = __dp4a(w[u][r].w, t.w, acc[r][m]);
+                        }
                     }
                 }
+                v0 += U * LPR;
+                if (v0 >= nv) break;
+#pragma unroll
+                for (int u = 0; u < U; ++u) fetch(v0 + u * LPR, w[u]);
             }
         }
 #pragma unroll
@@ -671,17 +684,18 @@ int encode(CUtensorMap* map, CUtensorMapDataType type, const void* base, int64_t
     return r == CUDA_SUCCESS ? DDP_OK : cuda_fail(cudaErrorInvalidValue);
 }
 
-template <int LPR, int R, bool BF16>
+constexpr int kFewLanes = 16, kFewRows = 2, kFewFlight = 4;
+template <bool BF16>
 void (*few_by_tokens(int M))(FewParams) {
     switch (M) {
-        case 1: return few_kernel<1, LPR, R, BF16>;
-        case 2: return few_kernel<2, LPR, R, BF16>;
-        case 3: return few_kernel<3, LPR, R, BF16>;
-        case 4: return few_kernel<4, LPR, R, BF16>;
-        case 5: return few_kernel<5, LPR, R, BF16>;
-        case 6: return few_kernel<6, LPR, R, BF16>;
-        case 7: return few_kernel<7, LPR, R, BF16>;
-        default: return few_kernel<8, LPR, R, BF16>;
+        case 1: return few_kernel<1, kFewLanes, kFewRows, kFewFlight, BF16>;
+        case 2: return few_kernel<2, kFewLanes, kFewRows, kFewFlight, BF16>;
+        case 3: return few_kernel<3, kFewLanes, kFewRows, kFewFlight, BF16>;
+        case 4: return few_kernel<4, kFewLanes, kFewRows, kFewFlight, BF16>;
+        case 5: return few_kernel<5, kFewLanes, kFewRows, kFewFlight, BF16>;
+        case 6: return few_kernel<6, kFewLanes, kFewRows, kFewFlight, BF16>;
+        case 7: return few_kernel<7, kFewLanes, kFewRows, kFewFlight, BF16>;
+        default: return few_kernel<8, kFewLanes, kFewRows, kFewFlight, BF16>;
     }
 }
 
@@ -767,11 +781,10 @@ extern "C" int q8_matmul(const int8_t* a, int64_t lda, const float* a_scale, con
             const FewParams p{a ? a + m * lda : nullptr, w, a_scale + m, w_scale,
                               static_cast<char*>(out) + m * ldo * (bf16 ? 2 : 4), lda, ldw, ldo, N, K, rows,
                               row_align(w, ldw, N), row_align(a ? a + m * lda : nullptr, lda, rows)};
-            constexpr int LPR = 16, R = 2;
-            const int64_t rows_per_cta = kFewThreads / LPR * R;
+            constexpr int64_t rows_per_cta = kFewThreads / kFewLanes * kFewRows;
             const int64_t need_ctas = (N + rows_per_cta - 1) / rows_per_cta, cap = 8ll * d.sm_count;
             const int64_t kc = K < kFewChunk ? round_up(K, 16) : kFewChunk;
-            st = launch_smem(bf16 ? few_by_tokens<LPR, R, true>(rows) : few_by_tokens<LPR, R, false>(rows),
+            st = launch_smem(bf16 ? few_by_tokens<true>(rows) : few_by_tokens<false>(rows),
                              static_cast<unsigned>(need_ctas < cap ? need_ctas : cap), kFewThreads,
                              static_cast<size_t>(rows * kc), s, p);
             if (st != DDP_OK) return st;
