@@ -543,25 +543,60 @@ _lib.distill_topk_forward_backward.argtypes = _DISTILL_ARGS + [_P, _P, _P, _P, _
 _lib.distill_topk_forward_backward.restype = _c.c_int
 
 
+# These calls are short, so what a call costs on the host counts: torch's names are looked up once, and the current
+# stream's handle is asked for without building a Stream object (2.9 us of a 14 us call).
+class _Torch:
+    f32 = bf16 = i8 = i32 = i64 = None
+    codes = {}
+
+    @classmethod
+    def load(cls):
+        import torch
+        cls.codes = {torch.float32: F32, torch.bfloat16: BF16}
+        cls.f32, cls.bf16, cls.i8, cls.i32, cls.i64 = (torch.float32, torch.bfloat16, torch.int8, torch.int32,
+                                                       torch.int64)
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is None:
+            cls.stream = staticmethod(lambda: torch.cuda.current_stream().cuda_stream)
+        else:
+            cls.stream = staticmethod(lambda: raw(torch.cuda.current_device()))
+
+
+def _launch_stream(stream) -> int:
+    if stream is None:
+        return _Torch.stream()
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _code(t) -> int:
+    c = _Torch.codes.get(t.dtype)
+    if c is None:
+        if not _Torch.codes:
+            _Torch.load()
+            return _code(t)
+        raise TypeError(f"unsupported dtype {t.dtype}")
+    return c
+
+
 def _mat(t, name: str, shape=None, dtype=None):
     """(address, leading dimension) of a 2-D row-major tensor; None -> (NULL, 0)."""
     if t is None:
         return None, 0
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+    st = t.stride()
+    if len(st) != 2 or (st[1] != 1 and t.shape[1] > 1):
         raise ValueError(f"{name}: need a 2-D tensor with unit column stride")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, need {tuple(shape)}")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, need {dtype}")
-    return t.data_ptr(), t.stride(0)
+    return t.data_ptr(), st[0]
 
 
 def _vec(t, name: str, n: int):
     """Address of a contiguous float32 vector of n elements; None -> NULL."""
     if t is None:
         return None
-    import torch
-    if t.dtype != torch.float32:
+    if t.dtype != _Torch.f32:
         raise TypeError(f"{name}: dtype {t.dtype}, need torch.float32")
     if t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name}: need {n} contiguous elements")
@@ -575,28 +610,27 @@ def _bytes(ws) -> int:
 def rmsnorm_forward(x, gamma, y, eps: float = 1e-6, residual=None, h_out=None, rstd_out=None, stream=None) -> None:
     """y = h * rstd * gamma with h = x + residual, rstd = 1/sqrt(mean(h^2) + eps) per row of [rows, D] matrices
     (fp32 or bf16, row strides as they are); h_out receives the sum, rstd_out (float32 [rows]) the statistics."""
-    rows, D = x.shape
+    code, (rows, D) = _code(x), x.shape
     px, ldx = _mat(x, "x")
     pr, ldr = _mat(residual, "residual", x.shape, x.dtype)
     ph, ldh = _mat(h_out, "h_out", x.shape, x.dtype)
     py, ldy = _mat(y, "y", x.shape)
-    _check(_lib.rmsnorm_forward(px, ldx, pr, ldr, _dtype_code(x), _vec(gamma, "gamma", D), rows, D, eps, ph, ldh,
-                                py, ldy, _dtype_code(y), _vec(rstd_out, "rstd_out", rows), _stream_ptr(stream)),
+    _check(_lib.rmsnorm_forward(px, ldx, pr, ldr, code, _vec(gamma, "gamma", D), rows, D, eps, ph, ldh,
+                                py, ldy, _code(y), _vec(rstd_out, "rstd_out", rows), _launch_stream(stream)),
            "rmsnorm_forward")
 
 
 def rmsnorm_forward_q8(x, gamma, q, scale, eps: float = 1e-6, residual=None, h_out=None, rstd_out=None,
                        stream=None) -> None:
     """rmsnorm_forward with its output in 8 bits: q (int8 [rows, D]) times scale (float32 [rows]) stands for y."""
-    import torch
-    rows, D = x.shape
+    code, (rows, D) = _code(x), x.shape
     px, ldx = _mat(x, "x")
     pr, ldr = _mat(residual, "residual", x.shape, x.dtype)
     ph, ldh = _mat(h_out, "h_out", x.shape, x.dtype)
-    pq, ldq = _mat(q, "q", x.shape, torch.int8)
-    _check(_lib.rmsnorm_forward_q8(px, ldx, pr, ldr, _dtype_code(x), _vec(gamma, "gamma", D), rows, D, eps, ph, ldh,
+    pq, ldq = _mat(q, "q", x.shape, _Torch.i8)
+    _check(_lib.rmsnorm_forward_q8(px, ldx, pr, ldr, code, _vec(gamma, "gamma", D), rows, D, eps, ph, ldh,
                                    pq, ldq, _vec(scale, "scale", rows), _vec(rstd_out, "rstd_out", rows),
-                                   _stream_ptr(stream)),
+                                   _launch_stream(stream)),
            "rmsnorm_forward_q8")
 
 
@@ -607,14 +641,14 @@ def rmsnorm_backward_workspace_bytes(rows: int, D: int) -> int:
 def rmsnorm_backward(dy, h, rstd, gamma, dx, dgamma=None, workspace=None, dh=None, stream=None) -> None:
     """Gradient of rmsnorm_forward: dx (of x and of residual alike; dh is what reaches h by other ways) and dgamma
     (float32 [D]; needs a workspace of rmsnorm_backward_workspace_bytes(rows, D) bytes)."""
-    rows, D = h.shape
+    code, (rows, D) = _code(h), h.shape
     ph, ldh = _mat(h, "h")
     py, ldy = _mat(dy, "dy", h.shape)
     pd, ldd = _mat(dh, "dh", h.shape, h.dtype)
     po, ldo = _mat(dx, "dx", h.shape, h.dtype)
-    _check(_lib.rmsnorm_backward(py, ldy, _dtype_code(dy), ph, ldh, _dtype_code(h), _vec(rstd, "rstd", rows),
+    _check(_lib.rmsnorm_backward(py, ldy, _code(dy), ph, ldh, code, _vec(rstd, "rstd", rows),
                                  _vec(gamma, "gamma", D), pd, ldd, rows, D, po, ldo, _vec(dgamma, "dgamma", D),
-                                 _ptr(workspace), _bytes(workspace), _stream_ptr(stream)),
+                                 _ptr(workspace), _bytes(workspace), _launch_stream(stream)),
            "rmsnorm_backward")
 
 
@@ -625,31 +659,29 @@ def q8_matmul_workspace_bytes(M: int, N: int, K: int) -> int:
 def q8_matmul(a, a_scale, w, w_scale, out, workspace, stream=None) -> None:
     """out[m, n] = (sum_k a[m, k] * w[n, k]) * a_scale[m] * w_scale[n]: int8 tokens a [M, K] and channels w [N, K],
     float32 scales, out [M, N] fp32 or bf16; workspace of q8_matmul_workspace_bytes(M, N, K) bytes."""
-    import torch
-    M, K = a.shape
-    pa, lda = _mat(a, "a", None, torch.int8)
-    pw, ldw = _mat(w, "w", None, torch.int8)
+    code, (M, K) = _code(out), a.shape
+    pa, lda = _mat(a, "a", None, _Torch.i8)
+    pw, ldw = _mat(w, "w", None, _Torch.i8)
     if w.shape[1] != K:
         raise ValueError(f"w: shape {tuple(w.shape)}, need [N, {K}]")
     N = w.shape[0]
     po, ldo = _mat(out, "out", (M, N))
     _check(_lib.q8_matmul(pa, lda, _vec(a_scale, "a_scale", M), pw, ldw, _vec(w_scale, "w_scale", N), M, N, K, po, ldo,
-                          _dtype_code(out), _ptr(workspace), _bytes(workspace), _stream_ptr(stream)),
+                          code, _ptr(workspace), _bytes(workspace), _launch_stream(stream)),
            "q8_matmul")
 
 
 def _distill_args(logits, index, teacher, temperature):
-    import torch
-    T, V = logits.shape
+    code, (T, V) = _code(logits), logits.shape
     pz, ldz = _mat(logits, "logits")
     pi, ldi = _mat(index, "index")
-    if index.dtype not in (torch.int32, torch.int64):
+    if index.dtype != _Torch.i64 and index.dtype != _Torch.i32:
         raise TypeError(f"index: dtype {index.dtype}, need torch.int32 or torch.int64")
     k = index.shape[1]
     if index.shape[0] != T:
         raise ValueError(f"index: shape {tuple(index.shape)}, need [{T}, k]")
     pt, ldt = _mat(teacher, "teacher", index.shape)
-    return T, (pz, ldz, _dtype_code(logits), pi, ldi, 8 * index.element_size(), pt, ldt, _dtype_code(teacher), T, V, k,
+    return T, (pz, ldz, code, pi, ldi, 8 * index.element_size(), pt, ldt, _code(teacher), T, V, k,
                temperature)
 
 
@@ -658,7 +690,7 @@ def distill_topk_forward(logits, index, teacher, loss, lse=None, temperature: fl
     (an index outside the vocabulary is no entry), q that of logits [T, V], both at the temperature; loss and lse
     are float32 [T]."""
     T, args = _distill_args(logits, index, teacher, temperature)
-    _check(_lib.distill_topk_forward(*args, _vec(loss, "loss", T), _vec(lse, "lse", T), _stream_ptr(stream)),
+    _check(_lib.distill_topk_forward(*args, _vec(loss, "loss", T), _vec(lse, "lse", T), _launch_stream(stream)),
            "distill_topk_forward")
 
 
@@ -667,7 +699,7 @@ def distill_topk_backward(logits, index, teacher, lse, dloss, dlogits, temperatu
     T, args = _distill_args(logits, index, teacher, temperature)
     pd, ldd = _mat(dlogits, "dlogits", logits.shape, logits.dtype)
     _check(_lib.distill_topk_backward(*args, _vec(lse, "lse", T), _vec(dloss, "dloss", T), pd, ldd,
-                                      _stream_ptr(stream)),
+                                      _launch_stream(stream)),
            "distill_topk_backward")
 
 
@@ -677,7 +709,7 @@ def distill_topk_forward_backward(logits, index, teacher, dloss, loss, lse, dlog
     T, args = _distill_args(logits, index, teacher, temperature)
     pd, ldd = _mat(dlogits, "dlogits", logits.shape, logits.dtype)
     _check(_lib.distill_topk_forward_backward(*args, _vec(dloss, "dloss", T), _vec(loss, "loss", T),
-                                              _vec(lse, "lse", T), pd, ldd, _stream_ptr(stream)),
+                                              _vec(lse, "lse", T), pd, ldd, _launch_stream(stream)),
            "distill_topk_forward_backward")
 
 
