@@ -1,8 +1,9 @@
 // Product of 8-bit integers with a scale for each token and each channel:
 //   out[m, n] = (Σ_k a[m, k]·w[n, k]) · a_scale[m] · w_scale[n]
 //
-// Up to kFewTokens tokens: the channels are streamed once and multiplied with
-// dp4a into exact 32-bit integers (few_kernel); bound by HBM.
+// Up to kFewTokens tokens: the channels are streamed once and multiplied into
+// exact 32-bit integers, with dp4a (few_kernel) or, from 3 tokens on, the
+// warp-wide 8-bit tensor instruction (few_mma_kernel); bound by HBM, or by that instruction's low rate.
 //
 // More tokens: GB300's tensor cores run 8-bit integers far below their 16-bit
 // rate, and an 8-bit integer is exact in fp16, as is a product of two in
@@ -68,11 +69,14 @@ struct FewParams {
     int64_t lda, ldw, ldo, N;
     int32_t K, M;
     int32_t w_align, a_align;   // 16, 4 or 1: what the rows' addresses are multiples of
+    int32_t split;              // mma_kernel: warps that share 16 channels, a power of two up to kFewWarps
 };
 
-// 16 bytes at p of which the first `valid` exist, the others read as 0.
-__device__ __forceinline__ int4 load16(const int8_t* p, int valid, int align) {
+// 16 bytes at p of which the first `valid` exist, the others read as 0; KEEP: the caches keep them.
+template <bool KEEP>
+__device__ __forceinline__ int4 load16_any(const int8_t* p, int valid, int align) {
     if (valid >= 16 && align == 16) {
+        if constexpr (KEEP) return __ldg(reinterpret_cast<const int4*>(p));
         const uint4 v = ld16<true>(p);
         return make_int4(static_cast<int>(v.x), static_cast<int>(v.y), static_cast<int>(v.z), static_cast<int>(v.w));
     }
@@ -87,8 +91,10 @@ __device__ __forceinline__ int4 load16(const int8_t* p, int valid, int align) {
     }
     return make_int4(r[0], r[1], r[2], r[3]);
 }
+__device__ __forceinline__ int4 load16(const int8_t* p, int valid, int align) { return load16_any<false>(p, valid, align); }
+__device__ __forceinline__ int4 load16_keep(const int8_t* p, int valid, int align) { return load16_any<true>(p, valid, align); }
 
-constexpr int kFewThreads = 256;
+constexpr int kFewThreads = 256, kFewWarps = kFewThreads / 32;
 constexpr int kFewChunk = 4096;   // bytes of K of every token in shared memory at a time
 
 // LPR lanes per channel row, R rows per lane group at a time, U vectors of
@@ -158,6 +164,67 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant_
                     store_elem<BF16>(p.out, m * p.ldo + n, static_cast<float>(s) * p.sa[m] * p.sw[n]);
             }
         }
+    }
+}
+
+__device__ __forceinline__ void mma_s8(int (&c)[4], int a0, int a1, int a2, int a3, int b0, int b1) {
+    asm volatile("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// A warp takes 16 channels and every SK-th block of 64 of K, up to 8 tokens, U
+// blocks in flight.  The sum over k does not care in which order k goes as long
+// as both operands agree, so a lane's 16 bytes of a row are the words of two
+// MMAs as they come from memory: no shared memory, no shuffles.
+template <bool BF16>
+__global__ void __launch_bounds__(kFewThreads) few_mma_kernel(const __grid_constant__ FewParams p) {
+    constexpr int U = 3;
+    __shared__ int part[kFewWarps][4][32];
+    pdl_enter();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+    const int sk = p.split, s = warp % sk;
+    const int64_t n0 = (static_cast<int64_t>(blockIdx.x) * (kFewWarps / sk) + warp / sk) * 16;
+    const int64_t na = n0 + g, nb = na + 8;
+    const int8_t* wa = p.w + na * p.ldw + 16 * q;
+    const int8_t* wb = p.w + nb * p.ldw + 16 * q;
+    const int8_t* ta = p.a + g * p.lda + 16 * q;
+    int acc[4] = {};
+    const int blocks = (p.K + 63) / 64;
+    const int4 zero = make_int4(0, 0, 0, 0);
+    for (int b0 = s; b0 < blocks; b0 += U * sk) {
+        int4 a[U], b[U], t[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int k = (b0 + u * sk) * 64, valid = p.K - k - 16 * q;
+            a[u] = na < p.N && valid > 0 ? load16(wa + k, valid, p.w_align) : zero;
+            b[u] = nb < p.N && valid > 0 ? load16(wb + k, valid, p.w_align) : zero;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int k = (b0 + u * sk) * 64, valid = p.K - k - 16 * q;
+            t[u] = g < p.M && valid > 0 ? load16_keep(ta + k, valid, p.a_align) : zero;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            mma_s8(acc, a[u].x, b[u].x, a[u].y, b[u].y, t[u].x, t[u].y);
+            mma_s8(acc, a[u].z, b[u].z, a[u].w, b[u].w, t[u].z, t[u].w);
+        }
+    }
+    if (sk > 1) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) part[warp][j][lane] = acc[j];
+        __syncthreads();
+        if (s != 0) return;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            for (int w = 1; w < sk; ++w) acc[j] += part[warp + w][j][lane];
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int m = 2 * q + (j & 1);
+        const int64_t n = j < 2 ? na : nb;
+        if (m < p.M && n < p.N) store_elem<BF16>(p.out, m * p.ldo + n, static_cast<float>(acc[j]) * p.sa[m] * p.sw[n]);
     }
 }
 
@@ -684,19 +751,18 @@ int encode(CUtensorMap* map, CUtensorMapDataType type, const void* base, int64_t
     return r == CUDA_SUCCESS ? DDP_OK : cuda_fail(cudaErrorInvalidValue);
 }
 
-constexpr int kFewLanes = 16, kFewRows = 2, kFewFlight = 4;
+// dp4a for up to kDotTokens.  Lanes per row, rows at a time and vectors in flight by K (us): 50257 x 768 at 8.3 with
+// (16, 2, 3), 13.2 with (32, 1, 8); 8192 x 4096 at 8.0 and 6.2.  From 3 tokens on the 8-bit tensor instruction is ahead:
+// 8 tokens of 8192 x 4096 17.7 by dp4a, 10.3; of 50257 x 768 19.3, 12.0 (1 token there 11.7).
+constexpr int kDotTokens = 2;
+struct DotPlan {
+    void (*kernel)(FewParams);
+    int rows;   // per CTA
+};
 template <bool BF16>
-void (*few_by_tokens(int M))(FewParams) {
-    switch (M) {
-        case 1: return few_kernel<1, kFewLanes, kFewRows, kFewFlight, BF16>;
-        case 2: return few_kernel<2, kFewLanes, kFewRows, kFewFlight, BF16>;
-        case 3: return few_kernel<3, kFewLanes, kFewRows, kFewFlight, BF16>;
-        case 4: return few_kernel<4, kFewLanes, kFewRows, kFewFlight, BF16>;
-        case 5: return few_kernel<5, kFewLanes, kFewRows, kFewFlight, BF16>;
-        case 6: return few_kernel<6, kFewLanes, kFewRows, kFewFlight, BF16>;
-        case 7: return few_kernel<7, kFewLanes, kFewRows, kFewFlight, BF16>;
-        default: return few_kernel<8, kFewLanes, kFewRows, kFewFlight, BF16>;
-    }
+DotPlan dot_plan(int M, int32_t K) {
+    if (K <= 1024) return {M == 1 ? few_kernel<1, 16, 2, 3, BF16> : few_kernel<2, 16, 2, 3, BF16>, kFewThreads / 16 * 2};
+    return {M == 1 ? few_kernel<1, 32, 1, 8, BF16> : few_kernel<2, 32, 1, 8, BF16>, kFewThreads / 32};
 }
 
 int row_align(const void* p, int64_t ld, int64_t rows) {
@@ -778,15 +844,23 @@ extern "C" int q8_matmul(const int8_t* a, int64_t lda, const float* a_scale, con
         // K == 0 takes the same path in slices of kFewTokens tokens: nothing is summed
         for (int64_t m = 0; m < M; m += kFewTokens) {
             const int32_t rows = static_cast<int32_t>(M - m < kFewTokens ? M - m : kFewTokens);
-            const FewParams p{a ? a + m * lda : nullptr, w, a_scale + m, w_scale,
-                              static_cast<char*>(out) + m * ldo * (bf16 ? 2 : 4), lda, ldw, ldo, N, K, rows,
-                              row_align(w, ldw, N), row_align(a ? a + m * lda : nullptr, lda, rows)};
-            constexpr int64_t rows_per_cta = kFewThreads / kFewLanes * kFewRows;
-            const int64_t need_ctas = (N + rows_per_cta - 1) / rows_per_cta, cap = 8ll * d.sm_count;
-            const int64_t kc = K < kFewChunk ? round_up(K, 16) : kFewChunk;
-            st = launch_smem(bf16 ? few_by_tokens<true>(rows) : few_by_tokens<false>(rows),
-                             static_cast<unsigned>(need_ctas < cap ? need_ctas : cap), kFewThreads,
-                             static_cast<size_t>(rows * kc), s, p);
+            FewParams p{a ? a + m * lda : nullptr, w, a_scale + m, w_scale,
+                        static_cast<char*>(out) + m * ldo * (bf16 ? 2 : 4), lda, ldw, ldo, N, K, rows,
+                        row_align(w, ldw, N), row_align(a ? a + m * lda : nullptr, lda, rows), 1};
+            if (rows <= kDotTokens) {
+                const DotPlan plan = bf16 ? dot_plan<true>(rows, K) : dot_plan<false>(rows, K);
+                const int64_t need_ctas = (N + plan.rows - 1) / plan.rows, cap = 8ll * d.sm_count;
+                const int64_t kc = K < kFewChunk ? round_up(K, 16) : kFewChunk;
+                st = launch_smem(plan.kernel, static_cast<unsigned>(need_ctas < cap ? need_ctas : cap), kFewThreads,
+                                 static_cast<size_t>(rows * kc), s, p);
+            } else {
+                // enough warps to fill the SMs, each with four blocks of K at least
+                const int64_t groups = (N + 15) / 16, blocks = (K + 63) / 64;
+                while (p.split < kFewWarps && groups * p.split < 16ll * d.sm_count && blocks >= 4 * p.split) p.split *= 2;
+                const int64_t per_cta = kFewWarps / p.split;
+                st = launch_pdl(bf16 ? few_mma_kernel<true> : few_mma_kernel<false>,
+                                dim3(static_cast<unsigned>((groups + per_cta - 1) / per_cta)), kFewThreads, s, p);
+            }
             if (st != DDP_OK) return st;
         }
         return DDP_OK;
