@@ -68,20 +68,6 @@ __device__ __forceinline__ float cluster_read(const float* p, uint32_t rank) {
     return v;
 }
 
-// Two values over the CTA at once, in every thread; `sh` as in block_all.
-template <class OpA, class OpB>
-__device__ __forceinline__ void block_all2(float& a, float& b, float2* sh) {
-    a = warp_all<OpA>(a);
-    b = warp_all<OpB>(b);
-    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = make_float2(a, b);
-    __syncthreads();
-    const bool in = (threadIdx.x & 31) < kDistillThreads / 32;
-    const float2 v = in ? sh[threadIdx.x & 31] : make_float2(OpA::id(), OpB::id());
-    a = warp_all<OpA>(v.x);
-    b = warp_all<OpB>(v.y);
-    __syncthreads();
-}
-
 // Largest m of z and Σ 2^(z·c − mc), mc = m·c kept within ±kFar.
 struct Running {
     float m = -INFINITY, mc = 0.0f, s = 0.0f;

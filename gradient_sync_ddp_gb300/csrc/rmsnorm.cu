@@ -139,25 +139,39 @@ __device__ __forceinline__ void store_n(char* p, const float (&o)[N]) {
         *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
     }
 }
-// γ of VEC columns from d on (1 without γ); vectors where its columns lie on 16 bytes.
+// γ of VEC columns from d on (1 without γ).  EDGE: d is any column, the same
+// modulo 4 for a row's vectors; the 16-byte pieces that cover them, shifted
+// (one 4-byte load per column instead cost 8 passes of 32 sectors per warp).
 template <bool EDGE, int VEC>
-__device__ __forceinline__ void load_gamma(const float* gamma, int d, float (&o)[VEC]) {
+__device__ __forceinline__ void load_gamma(const float* gamma, int D, int d, float (&o)[VEC]) {
     if (gamma == nullptr) {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) o[e] = 1.0f;
-    } else if constexpr (EDGE) {
+        return;
+    }
+    const int s = EDGE ? (d + static_cast<int>(reinterpret_cast<uintptr_t>(gamma) / 4)) & 3 : 0, b = d - s;
+    if (EDGE && (b < 0 || b + VEC + 4 > D)) {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) o[e] = __ldg(gamma + d + e);
-    } else {
-#pragma unroll
-        for (int q = 0; q < VEC / 4; ++q) {
-            const float4 v = __ldg(reinterpret_cast<const float4*>(gamma + d) + q);
-            o[4 * q] = v.x;
-            o[4 * q + 1] = v.y;
-            o[4 * q + 2] = v.z;
-            o[4 * q + 3] = v.w;
-        }
+        return;
     }
+    float f[VEC + 4];
+#pragma unroll
+    for (int q = 0; q < VEC / 4 + (EDGE ? 1 : 0); ++q) {
+        const float4 v = __ldg(reinterpret_cast<const float4*>(gamma + b) + q);
+        f[4 * q] = v.x;
+        f[4 * q + 1] = v.y;
+        f[4 * q + 2] = v.z;
+        f[4 * q + 3] = v.w;
+    }
+    if constexpr (EDGE) {
+#pragma unroll
+        for (int e = 0; e < VEC + 3; ++e) f[e] = s & 1 ? f[e + 1] : f[e];
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) f[e] = s & 2 ? f[e + 2] : f[e];
+    }
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) o[e] = f[e];
 }
 
 constexpr int kWarpRows = 8;      // rows per CTA of the warp-per-row forward kernels
@@ -168,7 +182,7 @@ template <bool BF16, int OUT, int VPT, bool EDGE, bool WARP>
 __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : max_group(BF16, VPT))
     norm_kernel(const __grid_constant__ NormParams a) {
     constexpr int ES = BF16 ? 2 : 4, VEC = 16 / ES, YS = OUT == kOutQ8 ? 1 : OUT == kOutBf16 ? 2 : 4;
-    __shared__ float sh[32];
+    __shared__ float2 sh[32];
     pdl_enter();
     const int G = WARP ? 32 : blockDim.x;
     const int t = WARP ? threadIdx.x & 31 : threadIdx.x;
@@ -220,7 +234,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : max_group(BF16, VPT))
         const int v = t + i * G;
         if (v >= s.nvec) break;
         float g[VEC];
-        load_gamma<EDGE, VEC>(a.gamma, s.lead + v * VEC, g);
+        load_gamma<EDGE, VEC>(a.gamma, a.D, s.lead + v * VEC, g);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
             h[i][e] *= g[e];
@@ -231,18 +245,22 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : max_group(BF16, VPT))
         he = a.gamma ? he * a.gamma[de] : he;
         if constexpr (OUT == kOutQ8) mx = max_nan(mx, fabsf(he));
     }
-    ss = WARP ? warp_all<SumOp>(ss) : block_all<SumOp>(ss, sh);
+    if constexpr (OUT == kOutQ8) {
+        if constexpr (WARP) ss = warp_all<SumOp>(ss), mx = warp_all<MaxNanOp>(mx);
+        else block_all2<SumOp, MaxNanOp>(ss, mx, sh);
+    } else {
+        ss = WARP ? warp_all<SumOp>(ss) : block_all<SumOp>(ss, reinterpret_cast<float*>(sh));
+    }
     const float rstd = 1.0f / sqrtf(ss / a.D + a.eps);
     if (t == 0 && a.rstd) a.rstd[row] = rstd;
     if constexpr (OUT == kOutQ8) {
-        mx = WARP ? warp_all<MaxNanOp>(mx) : block_all<MaxNanOp>(mx, sh);
         const float sc = mx * rstd / 127.0f;
         const float inv = sc > 0.0f && sc < INFINITY ? rstd / sc : 0.0f;
         if (t == 0) a.scale[row] = sc;
-        auto quant = [&](float v) {
-            const int q = __float2int_rn(fminf(fmaxf(v * inv, -127.0f), 127.0f));
-            return static_cast<uint32_t>(inv > 0.0f ? q : 0) & 0xffu;
-        };
+        // |h·γ·inv| <= 127 up to rounding, so that adding 1.5·2^23 leaves the nearest integer (ties to even) in the low
+        // byte, with one rounding and no conversion instruction (those run at a quarter of the rate).
+        constexpr float kMagic = 12582912.0f;
+        auto quant = [&](float v) { return inv > 0.0f ? __float_as_uint(fmaf(v, inv, kMagic)) : 0u; };
         char* y = static_cast<char*>(a.y) + row * a.ldy;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
@@ -251,12 +269,13 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : max_group(BF16, VPT))
             uint32_t w[VEC / 4];
 #pragma unroll
             for (int q = 0; q < VEC / 4; ++q)
-                w[q] = quant(h[i][4 * q]) | quant(h[i][4 * q + 1]) << 8 | quant(h[i][4 * q + 2]) << 16 | quant(h[i][4 * q + 3]) << 24;
+                w[q] = __byte_perm(__byte_perm(quant(h[i][4 * q]), quant(h[i][4 * q + 1]), 0x0040),
+                                   __byte_perm(quant(h[i][4 * q + 2]), quant(h[i][4 * q + 3]), 0x0040), 0x5410);
             char* d = y + s.lead + v * VEC;
             if constexpr (VEC == 8) *reinterpret_cast<uint2*>(d) = make_uint2(w[0], w[VEC / 4 - 1]);
             else *reinterpret_cast<uint32_t*>(d) = w[0];
         }
-        if (has_edge) y[de] = static_cast<char>(quant(he));
+        if (has_edge) y[de] = static_cast<char>(quant(he) & 0xffu);
     } else {
         char* y = row_ptr<OUT == kOutBf16>(a.y, row, a.ldy);
 #pragma unroll
@@ -398,7 +417,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kGradRows : AHEAD ? 512 : max_grou
             const int v = t + i * G;
             if (v >= nvec) break;
             float gm[VEC];
-            load_gamma<false, VEC>(a.gamma, v * VEC, gm);
+            load_gamma<false, VEC>(a.gamma, a.D, v * VEC, gm);
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
                 const float gn = g[i].at(e) * (h[i].at(e) * rstd);
@@ -413,7 +432,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kGradRows : AHEAD ? 512 : max_grou
             const int v = t + i * G;
             if (v >= nvec) break;
             float gm[VEC], o[VEC];
-            load_gamma<false, VEC>(a.gamma, v * VEC, gm);
+            load_gamma<false, VEC>(a.gamma, a.D, v * VEC, gm);
 #pragma unroll
             for (int e = 0; e < VEC; ++e) o[e] = fmaf(rstd, g[i].at(e) * gm[e] - h[i].at(e) * rstd * c, r[i].at(e));
             store_n<BF16, VEC>(dx + v * VEC * ES, o);

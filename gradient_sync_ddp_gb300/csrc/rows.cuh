@@ -76,6 +76,20 @@ __device__ __forceinline__ float block_all(float v, float* sh) {
     return r;
 }
 
+// Two values over the CTA at once, in every thread; `sh`, one pair per warp, as in block_all.
+template <class OpA, class OpB>
+__device__ __forceinline__ void block_all2(float& a, float& b, float2* sh) {
+    a = warp_all<OpA>(a);
+    b = warp_all<OpB>(b);
+    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = make_float2(a, b);
+    __syncthreads();
+    const bool in = (threadIdx.x & 31) < (blockDim.x + 31) >> 5;
+    const float2 v = in ? sh[threadIdx.x & 31] : make_float2(OpA::id(), OpB::id());
+    a = warp_all<OpA>(v.x);
+    b = warp_all<OpB>(v.y);
+    __syncthreads();
+}
+
 // ---- host: a matrix argument of a call --------------------------------
 
 struct Mat {
