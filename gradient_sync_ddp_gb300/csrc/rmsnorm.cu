@@ -211,8 +211,10 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : max_group(BF16, VPT))
             for (int e = 0; e < VEC; ++e) h[i][e] += rr[e];
         }
     }
-    const bool has_edge = EDGE && t < s.edges;
-    const int de = EDGE ? edge_elem<VEC>(s, t) : 0;
+    // the last warp has the fewest vectors: elsewhere the ends would cost the row a second memory latency
+    const int te = G - 1 - t;
+    const bool has_edge = EDGE && te < s.edges;
+    const int de = EDGE ? edge_elem<VEC>(s, te) : 0;
     if (has_edge) he = load_elem<BF16>(x, de) + (r ? load_elem<BF16>(r, de) : 0.0f);
     float ss = he * he, mx = 0.0f;
 #pragma unroll
