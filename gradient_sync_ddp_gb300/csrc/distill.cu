@@ -32,6 +32,7 @@ constexpr int kMaxCluster = 8;
 constexpr int kHash = 2 * kMaxTop;
 constexpr int kScanTop = 32;          // up to this many entries repeats are found by scanning all pairs
 constexpr float kLog2eLow = 1.9259629911e-8f;   // log2(e) − kLog2e
+constexpr int64_t kRowsInL2 = 90ll << 20;   // of the rows in hand, so that the second pass finds them there
 constexpr float kMasked = 1.0e4f;     // logits beyond this are no reference
 constexpr float kFar = 1.0e37f;       // beyond this, z·c may overflow: exponents from (z − max)·c instead
 
@@ -55,6 +56,34 @@ __device__ __forceinline__ float pow2(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
+}
+
+// Pairs of fp32 values in one register pair: one instruction for two multiply-adds or additions.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t pow2_pair(uint64_t x) {
+    float lo, hi;
+    unpair(x, lo, hi);
+    return pair(pow2(lo), pow2(hi));
+}
+// The e-th pair of a vector's values.
+template <bool BF16>
+__device__ __forceinline__ uint64_t vec_pair(const uint4& v, int e) {
+    return pair(vec_elem<BF16>(v, 2 * e), vec_elem<BF16>(v, 2 * e + 1));
 }
 
 __device__ __forceinline__ void cluster_sync() {
@@ -132,13 +161,26 @@ __device__ __forceinline__ void each_vector(const Slice& s, F body) {
         if (i + u * kDistillThreads < s.nvec) body(i + u * kDistillThreads, v[u]);
 }
 
+// A vector of dz to an address that is not on 16 bytes.
+template <bool BF16>
+__device__ __forceinline__ void store_vec_anywhere(char* d, const uint4& w) {
+#pragma unroll
+    for (int e = 0; e < (BF16 ? 8 : 4); ++e) {
+        const int q = BF16 ? e / 2 : e;
+        const uint32_t x = q == 0 ? w.x : q == 1 ? w.y : q == 2 ? w.z : w.w;
+        if constexpr (BF16) reinterpret_cast<unsigned short*>(d)[e] = static_cast<unsigned short>(x >> (16 * (e & 1)));
+        else reinterpret_cast<uint32_t*>(d)[e] = x;
+    }
+}
+
 // dz = g·q over a slice; the exponent of q as FAR says.  A bf16 dz has |g| in the exponent and its sign set
 // afterwards; an fp32 dz keeps them apart, for the larger exponent would round more.
 template <bool BF16, bool FAR, bool KEEP>
-__device__ __forceinline__ void write_grad(const Slice& s, char* dz, float c, float M, float m, float ls, float g) {
+__device__ __forceinline__ void write_grad(const Slice& s, char* dz, float c, float M, float m, float ls, float g, bool has_edge, int ve, float xe) {
     constexpr int ES = BF16 ? 2 : 4, VEC = 16 / ES;
     const float off = (FAR ? ls : M + ls) - log2f(fabsf(g));
     const uint32_t sign = BF16 && g < 0.0f ? 0x80008000u : 0u;
+    const uint64_t c2 = pair(c, c), n2 = pair(-off, -off);
     auto f = [&](float z) {
         if constexpr (BF16) return pow2(FAR ? fmaf(z - m, c, -off) : fmaf(z, c, -off));
         else return g * pow2((FAR ? (z - m) * c : fmaf(z, c, -M)) - ls);
@@ -147,27 +189,22 @@ __device__ __forceinline__ void write_grad(const Slice& s, char* dz, float c, fl
     const bool whole = (reinterpret_cast<uintptr_t>(dv) & 15) == 0;
     each_vector<BF16, KEEP>(s, [&](int i, const uint4& v) {
         float o[VEC];
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) o[e] = f(vec_elem<BF16>(v, e));
         uint4 w;
-        if constexpr (BF16) w = make_uint4(pack2(o[0], o[1]), pack2(o[2], o[3]), pack2(o[4], o[5]), pack2(o[6], o[7]));
-        else w = f4_bits(o[0], o[1], o[2], o[3]);
-        if constexpr (BF16) w = make_uint4(w.x ^ sign, w.y ^ sign, w.z ^ sign, w.w ^ sign);
-        if (whole) {
-            st16(dv + static_cast<int64_t>(i) * 16, w);
+        if constexpr (BF16 && !FAR) {
+#pragma unroll
+            for (int e = 0; e < VEC / 2; ++e) unpair(pow2_pair(fma2(vec_pair<BF16>(v, e), c2, n2)), o[2 * e], o[2 * e + 1]);
         } else {
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                const uint32_t x = e * ES / 4 == 0 ? w.x : e * ES / 4 == 1 ? w.y : e * ES / 4 == 2 ? w.z : w.w;
-                if constexpr (BF16) reinterpret_cast<unsigned short*>(dv)[static_cast<int64_t>(i) * VEC + e] = static_cast<unsigned short>(x >> (16 * (e & 1)));
-                else reinterpret_cast<uint32_t*>(dv)[static_cast<int64_t>(i) * VEC + e] = x;
-            }
+            for (int e = 0; e < VEC; ++e) o[e] = f(vec_elem<BF16>(v, e));
         }
+        if constexpr (BF16) w = make_uint4(pack2(o[0], o[1]) ^ sign, pack2(o[2], o[3]) ^ sign, pack2(o[4], o[5]) ^ sign, pack2(o[6], o[7]) ^ sign);
+        else w = f4_bits(o[0], o[1], o[2], o[3]);
+        if (whole) st16(dv + static_cast<int64_t>(i) * 16, w);
+        else store_vec_anywhere<BF16>(dv + static_cast<int64_t>(i) * 16, w);
     });
-    if (threadIdx.x < s.lead + s.tail) {
-        const int v = edge<BF16>(s, threadIdx.x);
-        const float o = f(load_elem<BF16>(s.base, v));
-        store_elem<BF16>(dz, v, BF16 && g < 0.0f ? -o : o);
+    if (has_edge) {
+        const float o = f(xe);
+        store_elem<BF16>(dz, ve, BF16 && g < 0.0f ? -o : o);
     }
 }
 
@@ -186,14 +223,28 @@ __device__ __forceinline__ void write_zero(const Slice& s, char* dz) {
     if (threadIdx.x < s.lead + s.tail) store_elem<BF16>(dz, edge<BF16>(s, threadIdx.x), 0.0f);
 }
 
+// Two values over the CTA, in every thread, with one barrier: `sh` is not used again before another.
+template <class OpA, class OpB>
+__device__ __forceinline__ void once_all2(float& a, float& b, float2* sh) {
+    a = warp_all<OpA>(a);
+    b = warp_all<OpB>(b);
+    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = make_float2(a, b);
+    __syncthreads();
+    const float2 v = (threadIdx.x & 31) < kDistillThreads / 32 ? sh[threadIdx.x & 31] : make_float2(OpA::id(), OpB::id());
+    a = warp_all<OpA>(v.x);
+    b = warp_all<OpB>(v.y);
+}
+
 template <bool BF16, bool FWD, bool BWD>
 __global__ void __launch_bounds__(kDistillThreads, 4) distill_kernel(const __grid_constant__ DistillParams a) {
     constexpr int VEC = BF16 ? 8 : 4;
-    __shared__ float2 sh[kDistillThreads / 32];
+    __shared__ float2 sh[3][kDistillThreads / 32];
     __shared__ float s_part[2];                      // this CTA's (m, s), read by its cluster
-    __shared__ int s_idx[kMaxTop];
-    __shared__ float s_p[kMaxTop];
+    __shared__ float s_loss[kDistillThreads / 32];
+    __shared__ int s_idx[BWD ? kMaxTop : 1];
+    __shared__ float s_p[BWD ? kMaxTop : 1];
     __shared__ int s_hash[BWD ? kHash : 1];
+    __shared__ int s_twice;
     pdl_enter();
     const int tid = threadIdx.x;
     const int64_t row = blockIdx.x / a.cluster;
@@ -204,63 +255,84 @@ __global__ void __launch_bounds__(kDistillThreads, 4) distill_kernel(const __gri
     const int v0 = min(a.V, rank * per), v1 = min(a.V, v0 + per);
     const Slice s = make_slice<BF16>(z, v0, v1);
 
-    // the teacher's entries, in registers until the pass over z is done
-    int idx[kTopPerThread];
-    float t[kTopPerThread], zi[kTopPerThread];
+    // The teacher's entries: on their way during the pass over z, looked at after it.
+    int64_t raw[kTopPerThread];
+    float t[kTopPerThread];
 #pragma unroll
     for (int u = 0; u < kTopPerThread; ++u) {
         const int j = tid + u * kDistillThreads;
-        idx[u] = -1;
+        raw[u] = -1;
         t[u] = -INFINITY;
-        zi[u] = 0.0f;
         if (j >= a.k) continue;
         const int64_t e = row * a.ldi + j;
-        const int64_t i = a.i_64 ? static_cast<const int64_t*>(a.index)[e]
-                                 : static_cast<int64_t>(static_cast<const int32_t*>(a.index)[e]);
-        if (i < 0 || i >= a.V) continue;
-        idx[u] = static_cast<int>(i);
+        raw[u] = a.i_64 ? static_cast<const int64_t*>(a.index)[e] : static_cast<int64_t>(static_cast<const int32_t*>(a.index)[e]);
         t[u] = a.t_bf16 ? load_elem<true>(row_ptr<true>(a.teacher, row, a.ldt), j)
                         : load_elem<false>(row_ptr<false>(a.teacher, row, a.ldt), j);
-        // only what this CTA writes or sums: another's slice may hold gradients already
-        if ((FWD && rank == 0) || (i >= v0 && i < v1)) zi[u] = load_elem<BF16>(z, i);
+    }
+    const float up = BWD && a.dloss ? a.dloss[row] : 1.0f;
+    const float lse_in = FWD ? 0.0f : a.lse_in[row];
+    const bool has_edge = tid < s.lead + s.tail;
+    const int ve = has_edge ? edge<BF16>(s, tid) : 0;
+    const float xe = has_edge ? load_elem<BF16>(z, ve) : 0.0f;
+    const bool hash = a.k > kScanTop;
+    if constexpr (BWD) {
+        if (hash)
+            for (int i = tid; i < kHash; i += kDistillThreads) s_hash[i] = -1;
+        if (tid == 0) s_twice = hash ? 0 : 1;
     }
 
     // The sum takes no maximum: fp32 holds 2^±126 about any reference near the thread's logits, and its first vector
     // gives one (0 where that is masked).  A token that a thread's sum leaves the middle of that range for (logits 40
     // nats above the reference, or masked references and very low logits) is summed again with a running maximum.
     Running run;
+    bool out = false;
     if constexpr (FWD) {
-        float s1 = 0.0f;
+        const uint64_t c2 = pair(a.c, a.c);
+        uint64_t s2 = 0, n2 = 0;
         bool begun = false;
         each_vector<BF16, true>(s, [&](int, const uint4& v) {
-            float x[VEC];
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) x[e] = vec_elem<BF16>(v, e);
             if (!begun) {
                 begun = true;
-                float top = x[0];
+                float top = vec_elem<BF16>(v, 0);
 #pragma unroll
-                for (int e = 1; e < VEC; ++e) top = fmaxf(top, x[e]);
+                for (int e = 1; e < VEC; ++e) top = fmaxf(top, vec_elem<BF16>(v, e));
                 run.m = top > -kMasked ? fminf(top, kMasked) : 0.0f;
                 run.mc = run.m * a.c;
+                n2 = pair(-run.mc, -run.mc);
             }
-            float lo = 0.0f, hi = 0.0f;
+            uint64_t part = pow2_pair(fma2(vec_pair<BF16>(v, 0), c2, n2));
 #pragma unroll
-            for (int e = 0; e < VEC; e += 2) {
-                lo += pow2(fmaf(x[e], a.c, -run.mc));
-                hi += pow2(fmaf(x[e + 1], a.c, -run.mc));
-            }
-            run.s += lo;
-            s1 += hi;
+            for (int e = 1; e < VEC / 2; ++e) part = add2(part, pow2_pair(fma2(vec_pair<BF16>(v, e), c2, n2)));
+            s2 = add2(s2, part);
         });
-        run.s += s1;
-        bool out = begun && !(run.s > 1.0e-18f && run.s < 1.0e18f);
-        if (tid < s.lead + s.tail) {
-            const float x = load_elem<BF16>(z, edge<BF16>(s, tid));
-            run.raise(x, a.c);
-            run.s += pow2(fmaf(x, a.c, -run.mc));
+        float s_lo, s_hi;
+        unpair(s2, s_lo, s_hi);
+        run.s = s_lo + s_hi;
+        out = begun && !(run.s > 1.0e-18f && run.s < 1.0e18f);
+        if (has_edge) {
+            run.raise(xe, a.c);
+            run.s += pow2(fmaf(xe, a.c, -run.mc));
         }
-        if (__syncthreads_or(out)) {
+    }
+
+    // what the entries are, and the logits at those that this CTA writes or sums (another's slice may hold gradients)
+    int idx[kTopPerThread];
+    float zi[kTopPerThread];
+    float tm = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < kTopPerThread; ++u) {
+        const bool in = raw[u] >= 0 && raw[u] < a.V;
+        idx[u] = in ? static_cast<int>(raw[u]) : -1;
+        if (!in) t[u] = -INFINITY;
+        zi[u] = in && ((FWD && rank == 0) || (idx[u] >= v0 && idx[u] < v1)) ? load_elem<BF16>(z, idx[u]) : 0.0f;
+        tm = max_nan(tm, t[u]);
+    }
+
+    // maxima of the logits and of the entries, then their sums
+    float m = out ? INFINITY : run.m;
+    once_all2<MaxOp, MaxNanOp>(m, tm, sh[0]);
+    if constexpr (FWD) {
+        if (m == INFINITY) {                             // again, with a running maximum (or a logit is infinite)
             run = Running();
             each_vector<BF16, true>(s, [&](int, const uint4& v) {
                 float top = -INFINITY;
@@ -270,26 +342,36 @@ __global__ void __launch_bounds__(kDistillThreads, 4) distill_kernel(const __gri
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) run.s += pow2(fmaf(vec_elem<BF16>(v, e), a.c, -run.mc));
             });
-            if (tid < s.lead + s.tail) {
-                const float x = load_elem<BF16>(z, edge<BF16>(s, tid));
-                run.raise(x, a.c);
-                run.s += pow2(fmaf(x, a.c, -run.mc));
+            if (has_edge) {
+                run.raise(xe, a.c);
+                run.s += pow2(fmaf(xe, a.c, -run.mc));
             }
+            m = run.m;
+            float none = 0.0f;
+            __syncthreads();
+            once_all2<MaxOp, SumOp>(m, none, sh[0]);
         }
     }
-
-    // maxima of the logits and of the entries, then their sums
-    float m = run.m, tm = -INFINITY;
-#pragma unroll
-    for (int u = 0; u < kTopPerThread; ++u) tm = max_nan(tm, t[u]);
-    block_all2<MaxOp, MaxNanOp>(m, tm, sh);
     const bool some = !(tm == -INFINITY);
     float ts = 0.0f;
 #pragma unroll
     for (int u = 0; u < kTopPerThread; ++u) ts += some && idx[u] >= 0 ? pow2((t[u] - tm) * a.c) : 0.0f;
+    if constexpr (BWD) {                                 // repeated indices: seen where two entries meet in a slot
+        if (hash) {
+#pragma unroll
+            for (int u = 0; u < kTopPerThread; ++u) {
+                if (idx[u] < 0) continue;
+                for (uint32_t h = (static_cast<uint32_t>(idx[u]) * 2654435761u) >> 21;; h = (h + 1) & (kHash - 1)) {
+                    const int old = atomicCAS(&s_hash[h], -1, idx[u]);
+                    if (old == idx[u]) s_twice = 1;
+                    if (old == -1 || old == idx[u]) break;
+                }
+            }
+        }
+    }
     float M = fminf(fmaxf(m * a.c, -kFar), kFar);
     float sum = run.s == 0.0f ? 0.0f : run.s * pow2(run.mc - M);
-    block_all2<SumOp, SumOp>(sum, ts, sh);
+    once_all2<SumOp, SumOp>(sum, ts, sh[1]);
     if constexpr (FWD) {
         if (a.cluster > 1) {
             if (tid == 0) {
@@ -312,78 +394,57 @@ __global__ void __launch_bounds__(kDistillThreads, 4) distill_kernel(const __gri
                 sum += ps[r] == 0.0f ? 0.0f : ps[r] * pow2(fminf(fmaxf(pm[r] * a.c, -kFar), kFar) - M);
         }
     } else {
-        M = a.lse_in[row] * kLog2e;      // with what the product rounds off, below
-        m = a.lse_in[row] * a.tau;
+        M = lse_in * kLog2e;                             // with what the product rounds off, below
+        m = lse_in * a.tau;
     }
     // Logits whose product with c may overflow (a row that a mask of the type's lowest value leaves whole): differences first.
     const bool far = !(fabsf(m) * fmaxf(a.c, 1.0f) < kFar) && fabsf(m) < INFINITY;
     if constexpr (FWD) {
-        if (far) {                                   // rare, and every CTA of the token sums the whole row itself
+        if (far) {                                       // rare, and every CTA of the token sums the whole row itself
             float all = 0.0f, none = 0.0f;
             for (int v = tid; v < a.V; v += kDistillThreads) all += pow2((load_elem<BF16>(z, v) - m) * a.c);
-            block_all2<SumOp, SumOp>(all, none, sh);
+            once_all2<SumOp, SumOp>(all, none, sh[2]);
             sum = all;
+            if (BWD && a.cluster > 1) cluster_sync();    // every read of the row lies before any write
         }
     }
     // q_v = 2^(z·c − M − ls)
-    const float ls = FWD ? log2f(sum) : far ? 0.0f : fmaf(a.lse_in[row], kLog2e, -M) + a.lse_in[row] * kLog2eLow;
+    const float ls = FWD ? log2f(sum) : far ? 0.0f : fmaf(lse_in, kLog2e, -M) + lse_in * kLog2eLow;
     auto q2 = [&](float x) { return (far ? (x - m) * a.c : fmaf(x, a.c, -M)) - ls; };
     if constexpr (FWD) {
         if (rank == 0) {
             const float lts = log2f(ts);
-            float l = 0.0f, none = 0.0f;
+            float l = 0.0f;
 #pragma unroll
             for (int u = 0; u < kTopPerThread; ++u) {
                 const float lp = (t[u] - tm) * a.c, p = some && idx[u] >= 0 ? pow2(lp) / ts : 0.0f;
                 if (p != 0.0f) l += p * (lp - lts - q2(zi[u]));
             }
-            block_all2<SumOp, SumOp>(l, none, sh);
-            if (tid == 0) {
-                a.loss[row] = some ? l * kLn2 * a.tau * a.tau : 0.0f;
-                if (a.lse) a.lse[row] = far ? m / a.tau + ls * kLn2 : (M + ls) * kLn2;
-            }
+            l = warp_all<SumOp>(l);
+            if ((tid & 31) == 0) s_loss[tid >> 5] = l;
         }
     }
     if constexpr (BWD) {
-        const float g = (a.dloss ? a.dloss[row] : 1.0f) * a.tau;
+        const float g = up * a.tau;
         char* dz = row_ptr<BF16>(a.dz, row, a.lddz);
-        // every read of z beyond this thread's own elements lies before any write: far above re-reads the whole row
-        if (FWD && far && a.cluster > 1) cluster_sync();
-        __syncthreads();
-        if (!some || g == 0.0f) {
-            write_zero<BF16>(s, dz);
-        } else {
-            if (far) write_grad<BF16, true, !FWD>(s, dz, a.c, M, m, ls, g);
-            else write_grad<BF16, false, !FWD>(s, dz, a.c, M, m, ls, g);
-            // the entries: p into shared memory, repeated indices found there
-            const bool hash = a.k > kScanTop;
-            if (hash)
-                for (int i = tid; i < kHash; i += kDistillThreads) s_hash[i] = -1;
+        const bool zero = !some || g == 0.0f;
+        if (zero) write_zero<BF16>(s, dz);
+        else if (far) write_grad<BF16, true, !FWD>(s, dz, a.c, M, m, ls, g, has_edge, ve, xe);
+        else write_grad<BF16, false, !FWD>(s, dz, a.c, M, m, ls, g, has_edge, ve, xe);
 #pragma unroll
-            for (int u = 0; u < kTopPerThread; ++u) {
-                const int j = tid + u * kDistillThreads;
-                if (j >= a.k) continue;
-                s_idx[j] = idx[u];
-                s_p[j] = idx[u] >= 0 ? pow2((t[u] - tm) * a.c) / ts : 0.0f;
-            }
-            __syncthreads();
-            bool twice = !hash;
-            if (hash) {
-#pragma unroll
-                for (int u = 0; u < kTopPerThread; ++u) {
-                    if (idx[u] < 0) continue;
-                    for (uint32_t h = (static_cast<uint32_t>(idx[u]) * 2654435761u) >> 21;; h = (h + 1) & (kHash - 1)) {
-                        const int old = atomicCAS(&s_hash[h], -1, idx[u]);
-                        twice |= old == idx[u];
-                        if (old == -1 || old == idx[u]) break;
-                    }
-                }
-                twice = __syncthreads_or(twice);
-            }
+        for (int u = 0; u < kTopPerThread; ++u) {
+            const int j = tid + u * kDistillThreads;
+            if (j >= a.k) continue;
+            s_idx[j] = idx[u];
+            s_p[j] = idx[u] >= 0 ? pow2((t[u] - tm) * a.c) / ts : 0.0f;
+        }
+        __syncthreads();                                 // before the entries are rewritten
+        if (!zero) {
+            const bool twice = s_twice != 0;
 #pragma unroll
             for (int u = 0; u < kTopPerThread; ++u) {
                 const int j = tid + u * kDistillThreads, i = idx[u];
-                if (i < v0 || i >= v1) continue;     // absent ones are negative
+                if (i < v0 || i >= v1) continue;         // absent ones are negative
                 float p = twice ? 0.0f : s_p[j];
                 bool first = true;
                 if (twice) {
@@ -396,8 +457,19 @@ __global__ void __launch_bounds__(kDistillThreads, 4) distill_kernel(const __gri
                 if (first) store_elem<BF16>(dz, i, g * (pow2(q2(zi[u])) - p));
             }
         }
+    } else {
+        __syncthreads();
     }
-    if (FWD && a.cluster > 1) cluster_sync();        // no CTA ends while another reads its part
+    if constexpr (FWD) {
+        if (rank == 0 && tid == 0) {
+            float l = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kDistillThreads / 32; ++w) l += s_loss[w];
+            a.loss[row] = some ? l * kLn2 * a.tau * a.tau : 0.0f;
+            if (a.lse) a.lse[row] = far ? m / a.tau + ls * kLn2 : (M + ls) * kLn2;
+        }
+        if (a.cluster > 1) cluster_sync();               // no CTA ends while another reads its part
+    }
 }
 
 bool dtype_ok(int32_t t) { return t == DDP_F32 || t == DDP_BF16; }
@@ -442,7 +514,9 @@ int distill(const void* z, int64_t ldz, int32_t dtype, const void* index, int64_
     // one CTA per token fills the GPU from about two CTAs per SM; fewer tokens are split into slices of at least
     // 2048 logits each
     int cluster = 1;
-    while (cluster < kMaxCluster && T * cluster < 2ll * d.sm_count && V / (2 * cluster) >= 2048) cluster *= 2;
+    while (cluster < kMaxCluster && V / (2 * cluster) >= 2048 &&
+           (T * cluster < 2ll * d.sm_count || (fwd && bwd && 4ll * d.sm_count / cluster * V * es > kRowsInL2)))
+        cluster *= 2;
     if (T * cluster > INT32_MAX) return DDP_ERR_UNSUPPORTED;
     const DistillParams p{z, index, teacher, lse_in, dloss, loss, lse, dz, ldz, ldi, ldt, lddz, T, V, k, tau, c,
                           t_dtype == DDP_BF16, index_bits == 64, cluster};
