@@ -10,12 +10,17 @@
 // all of them -infinity) has loss and gradient 0, and the gradient of one
 // whose dloss is 0 is 0, whatever its logits hold.
 //
-// One launch.  A CTA takes a token (a cluster of CTAs, when tokens are too few
-// to fill the GPU, each a slice of the vocabulary): one pass over z keeps a
-// running maximum and a sum of exponentials per thread; the CTA (cluster)
-// joins them; a second pass writes dz = dloss·τ·q, reading z again while it is
-// still in L2; last, the at most k entries of dz that hold a p are rewritten.
-// HBM sees z once and dz once.  Rows need not start on 16-byte boundaries
+// One launch.  A CTA takes a token (a cluster of CTAs, each a slice of the
+// vocabulary, when tokens are too few to fill the GPU or too long for the rows
+// in hand to stay in L2): one pass over z sums exponentials about a reference
+// per thread; the CTA (cluster) joins them; a second pass writes dz =
+// dloss·τ·q, reading z again while it is still in L2; last, the at most k
+// entries of dz that hold a p are rewritten.  HBM sees z once and dz once:
+// 8192 x 50257 bf16, 1.65 GB in 297 us, 0.83 of the copy rate; gradient alone
+// 2049 x 32003 46 us, 0.86; loss alone 129 x 50257 fp32 7.4 us.  What bounds it
+// is the time a token's dependent steps take (loads, two sums over the CTA,
+// loads from L2) with four tokens in hand per SM: more of them miss L2, and rows
+// kept in shared memory instead (two per SM) took 373 us.  Rows need not start on 16-byte boundaries
 // (an odd vocabulary): a row is its 16-byte vectors and up to 2·(VEC − 1)
 // elements at its ends.
 #include <cstdint>

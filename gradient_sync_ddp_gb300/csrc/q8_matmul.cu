@@ -3,7 +3,9 @@
 //
 // Up to kFewTokens tokens: the channels are streamed once and multiplied into
 // exact 32-bit integers, with dp4a (few_kernel) or, from 3 tokens on, the
-// warp-wide 8-bit tensor instruction (few_mma_kernel); bound by HBM, or by that instruction's low rate.
+// warp-wide 8-bit tensor instruction (few_mma_kernel).  Bound by HBM (1 token,
+// 8192 x 4096: 33.6 MB in 6.2 us; 16384 x 8192: 22 us, 0.90 of the copy rate)
+// or that instruction's low rate (8 tokens, 8192 x 4096: 10.2 us).
 //
 // More tokens: GB300's tensor cores run 8-bit integers far below their 16-bit
 // rate, and an 8-bit integer is exact in fp16, as is a product of two in
@@ -14,23 +16,31 @@
 //   widen_kernel   tokens to fp16 in the workspace (channels whose rows TMA
 //                  cannot address are repacked there too, still in 8 bits)
 //   tile_kernel    persistent, a pair of CTAs (two SMs) per tile of 256
-//                  channels x NT tokens, roles by warp in each CTA:
+//                  channels x NT <= 256 tokens, roles by warp in each CTA:
 //     two producers  TMA, 128 of K at a time: the CTA's half of the tokens
-//                    [NT/2][2 x 64] fp16 and its 128 channels [128][128] int8
+//                    [2 x 64][NT/2] fp16 and its 128 channels [128][128] int8
 //                    (both in the 128-byte swizzle), each into its own ring
 //     converters     two warpgroups, a channel row per thread, each its half
 //                    of the 128: 64 bytes from shared memory, widened in
 //                    registers, stored to TMEM; channels thus cost 8 bits of
 //                    L2 and shared memory
 //     one issuer     (of the pair's first CTA) tcgen05.mma.cta_group::2, A
-//                    from TMEM, B from shared memory, accumulators fp32 in
-//                    TMEM, two of them
-//     epilogue       one warpgroup: TMEM -> scales -> out, under the next
-//                    tile's contraction
-// The pair halves what a tile's tokens cost: with one CTA per tile, L2 -> SM
-// traffic (65 bytes per clock and SM) and shared-memory traffic held the
-// contraction at 0.66 of its rate.  Few tiles split K (the parts are fp32 in the
-// workspace, combine_kernel adds them in their order).
+//                    from TMEM, B from shared memory, fp32 accumulator in TMEM
+//     epilogue       two warpgroups: TMEM -> scales -> registers, which frees
+//                    the accumulator; stored under the next tile's contraction
+// 8192 x 16384 x 4096: 549 us in bursts, 604 held (the clock falls): 2.0 and
+// 1.8 PFLOP/s, 1.05 and 0.96 of the 16-bit rate measured with cuBLAS.  What
+// that took, each by its measurement: 64-token-deep tiles of one CTA 870 us,
+// held by L2 -> SM traffic (65 bytes per clock and SM); the pair halves what
+// tokens cost; arrivals across the pair without release (1438 -> 1063); one
+// commit per stage (845 -> 753); token scales staged for the epilogue (-> 715);
+// NT = 256 with one accumulator, for a 192-wide MMA took as long as a 256-wide
+// one (-> 620); the issuing warp converged, descriptors in uniform registers:
+// 130 -> 45 clocks to issue an MMA (-> 562).
+// Few tiles split K (the parts are fp32 in the workspace, combine_kernel adds
+// them in their order).  37 x 8192 x 4096: 17.5 us, of which the widening 2, the
+// tiles 11.5 (K passes in 16 stages of about 1000 clocks: W's DRAM reads), the
+// parts and their sum 4.
 // Every wait is bounded; a tile whose wait ran out is written as NaN.
 #include <cstdint>
 
@@ -730,7 +740,7 @@ EncodeFn encode_fn() {
     static EncodeFn fn = [] {
         void* f = nullptr;
         cudaDriverEntryPointQueryResult r;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &r) != cudaSuccess ||
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess ||
             r != cudaDriverEntryPointSuccess)
             f = nullptr;
         return reinterpret_cast<EncodeFn>(f);
@@ -840,30 +850,32 @@ extern "C" int q8_matmul(const int8_t* a, int64_t lda, const float* a_scale, con
     int st = current_device_info(&d);
     if (st != DDP_OK) return st;
 
-    if (M <= kFewTokens || K == 0) {
-        // K == 0 takes the same path in slices of kFewTokens tokens: nothing is summed
-        for (int64_t m = 0; m < M; m += kFewTokens) {
-            const int32_t rows = static_cast<int32_t>(M - m < kFewTokens ? M - m : kFewTokens);
-            FewParams p{a ? a + m * lda : nullptr, w, a_scale + m, w_scale,
-                        static_cast<char*>(out) + m * ldo * (bf16 ? 2 : 4), lda, ldw, ldo, N, K, rows,
-                        row_align(w, ldw, N), row_align(a ? a + m * lda : nullptr, lda, rows), 1};
-            if (rows <= kDotTokens) {
-                const DotPlan plan = bf16 ? dot_plan<true>(rows, K) : dot_plan<false>(rows, K);
-                const int64_t need_ctas = (N + plan.rows - 1) / plan.rows, cap = 8ll * d.sm_count;
-                const int64_t kc = K < kFewChunk ? round_up(K, 16) : kFewChunk;
-                st = launch_smem(plan.kernel, static_cast<unsigned>(need_ctas < cap ? need_ctas : cap), kFewThreads,
-                                 static_cast<size_t>(rows * kc), s, p);
-            } else {
-                // enough warps to fill the SMs, each with four blocks of K at least
-                const int64_t groups = (N + 15) / 16, blocks = (K + 63) / 64;
-                while (p.split < kFewWarps && groups * p.split < 16ll * d.sm_count && blocks >= 4 * p.split) p.split *= 2;
-                const int64_t per_cta = kFewWarps / p.split;
-                st = launch_pdl(bf16 ? few_mma_kernel<true> : few_mma_kernel<false>,
-                                dim3(static_cast<unsigned>((groups + per_cta - 1) / per_cta)), kFewThreads, s, p);
-            }
+    if (K == 0) {                                       // a sum of no parts
+        for (int64_t m = 0; m < M; m += 65535) {
+            const int64_t rows = M - m < 65535 ? M - m : 65535;
+            const CombineParams q{nullptr, a_scale + m, w_scale, static_cast<char*>(out) + m * ldo * (bf16 ? 2 : 4), ldo, rows, N, 0};
+            st = launch_pdl(bf16 ? combine_kernel<true> : combine_kernel<false>,
+                            dim3(static_cast<unsigned>((N + kThreads - 1) / kThreads), static_cast<unsigned>(rows)), kThreads, s, q);
             if (st != DDP_OK) return st;
         }
         return DDP_OK;
+    }
+    if (M <= kFewTokens) {
+        const int32_t rows = static_cast<int32_t>(M);
+        FewParams p{a, w, a_scale, w_scale, out, lda, ldw, ldo, N, K, rows, row_align(w, ldw, N), row_align(a, lda, M), 1};
+        if (rows <= kDotTokens) {
+            const DotPlan plan = bf16 ? dot_plan<true>(rows, K) : dot_plan<false>(rows, K);
+            const int64_t need_ctas = (N + plan.rows - 1) / plan.rows, cap = 8ll * d.sm_count;
+            const int64_t kc = K < kFewChunk ? round_up(K, 16) : kFewChunk;
+            return launch_smem(plan.kernel, static_cast<unsigned>(need_ctas < cap ? need_ctas : cap), kFewThreads,
+                               static_cast<size_t>(rows * kc), s, p);
+        }
+        // enough warps to fill the SMs, each with four blocks of K at least
+        const int64_t groups = (N + 15) / 16, blocks = (K + 63) / 64;
+        while (p.split < kFewWarps && groups * p.split < 16ll * d.sm_count && blocks >= 4 * p.split) p.split *= 2;
+        const int64_t per_cta = kFewWarps / p.split;
+        return launch_pdl(bf16 ? few_mma_kernel<true> : few_mma_kernel<false>,
+                          dim3(static_cast<unsigned>((groups + per_cta - 1) / per_cta)), kFewThreads, s, p);
     }
 
     __half* x = static_cast<__half*>(workspace);

@@ -115,6 +115,9 @@ def test_empty_and_scales(g):
     o = torch.full((4, 6), 9.0, device="cuda")
     run(g, a, scales(4, 15), w, scales(6, 16), o)
     assert torch.all(o == 0)
+    o = torch.full((70000, 3), 9.0, device="cuda", dtype=torch.bfloat16)         # more tokens than one launch's rows
+    run(g, ints(70000, 0, 13), scales(70000, 15), ints(3, 0, 14), scales(3, 16), o)
+    assert torch.all(o == 0)
     run(g, ints(0, 8, 17), scales(0, 1), ints(6, 8, 18), scales(6, 16), torch.empty(0, 6, device="cuda"))
     run(g, ints(4, 8, 17), scales(4, 1), ints(0, 8, 18), scales(0, 16), torch.empty(4, 0, device="cuda"))
     # a scale of 0, a negative one, and a NaN that stays in its token or channel

@@ -226,6 +226,20 @@ def test_special_rows(g, D):
     check_q8(x[[0, 5]], None, None, 1e-6, q[[0, 5]], scale[[0, 5]])
 
 
+@pytest.mark.parametrize("D", [48, 515, 40000])
+def test_q8_of_tiny_and_huge_rows(g, D):
+    """Rows whose scale is far from 1: 127 / max would overflow, or the maximum is near the type's end."""
+    x = rand((5, D), 51)
+    x[1] *= 1e-36
+    x[2] *= 1e-33
+    x[3] *= 1e16
+    gamma = torch.ones(D, device="cuda")
+    q, scale = torch.full((5, D), 77, device="cuda", dtype=torch.int8), torch.empty(5, device="cuda")
+    g.rmsnorm_forward_q8(x, gamma, q, scale, 1.0)
+    sync()
+    check_q8(x, None, gamma, 1.0, q, scale)
+
+
 def test_empty(g):
     x = torch.empty(0, 64, device="cuda")
     g.rmsnorm_forward(x, None, torch.empty_like(x))
