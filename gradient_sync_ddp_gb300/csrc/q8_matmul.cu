@@ -38,9 +38,9 @@
 // one (-> 620); the issuing warp converged, descriptors in uniform registers:
 // 130 -> 45 clocks to issue an MMA (-> 562).
 // Few tiles split K (the parts are fp32 in the workspace, combine_kernel adds
-// them in their order).  37 x 8192 x 4096: 17.5 us, of which the widening 2, the
-// tiles 11.5 (K passes in 16 stages of about 1000 clocks: W's DRAM reads), the
-// parts and their sum 4.
+// them in their order).  37 x 8192 x 4096: 16 us, bound by the steps of the
+// pipeline itself: launches and TMEM 6 us, then 16 stages at about 850 clocks of
+// barriers each (12.6 us are left without loads, conversions and MMAs).
 // Every wait is bounded; a tile whose wait ran out is written as NaN.
 #include <cstdint>
 
@@ -60,11 +60,14 @@ constexpr int kBlockK = 128;      // one stage of the rings
 constexpr int kHalfK = 64;        // a row of 128 bytes in fp16
 constexpr int kWStageBytes = kCtaN * kBlockK;
 constexpr int kMaxAStages = 4;      // stages of channels in TMEM, 64 columns each; at most the rings' stages
-constexpr int kMaxStages = 12;
+constexpr int kMaxStages = 6;        // narrow tiles: 37 x 8192 x 4096 at 16.0 us with 6, 16.3 with 12
 constexpr int kRingBytes = 212 * 1024;
+// A tile CTA takes all of its SM's TMEM, so never two on one SM: each asks for more than half of the shared memory.
+constexpr size_t kMinTileSmem = 128 * 1024;
 constexpr int kTileThreads = 640;  // 4 warps of single roles, 8 of the epilogue, 8 converters
 constexpr long long kWaitClocks = 2000000000ll;   // about a second (clock64: the nanosecond timer is slow to read)
 
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
@@ -259,8 +262,12 @@ __device__ __forceinline__ void widen4(uint32_t v, uint32_t& lo, uint32_t& hi) {
     hi = *reinterpret_cast<const uint32_t*>(&y);
 }
 
+// Lets the tile kernel begin only once everything before this kernel is
+// done: its CTAs then read channels and scales while tokens are widened, and
+// wait for this grid where they need its output.
 __global__ void __launch_bounds__(kThreads) widen_kernel(const __grid_constant__ WidenParams p) {
-    pdl_enter();
+    pdl_wait();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int64_t stride = static_cast<int64_t>(gridDim.x) * kThreads;
     const int64_t first = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
     const int64_t av = (p.xp + 15) / 16;
@@ -292,7 +299,7 @@ struct TileParams {
     const float* sw;
     void* out;       // or the parts, float [splits][M][N]
     int64_t ldo;
-    int32_t M, N, halves, nt, m_tiles, n_tiles, group, splits, blocks_per_split, stages, a_stages, d_stages;
+    int32_t M, N, halves, nt, m_tiles, n_tiles, group, splits, blocks_per_split, stages, a_stages, d_stages, repacked;
 };
 
 struct TileShared {
@@ -505,13 +512,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
     fence_after();
     // all 512 columns are this pair's, from address 0 on
     const uint32_t a_col0 = (p.d_stages * p.nt + 31) / 32 * 32, xs_addr = smem_u32(xs);
-    pdl_enter();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int pieces = p.m_tiles * p.n_tiles * p.splits, first = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
     if (warp == 0 && lane == 0) {                       // token producer
         Ring r;
         int issued = 0;
         bool ok = true;
+        pdl_wait();
         for (int u = first; u < pieces && ok; u += pairs) {
             const Piece w = piece(p, u);
             for (int h = w.h0; h < w.h1; h += 2) {
@@ -534,6 +542,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
         Ring r;
         int issued = 0;
         bool ok = true;
+        if (p.repacked) pdl_wait();
         for (int u = first; u < pieces && ok; u += pairs) {
             const Piece w = piece(p, u);
             for (int h = w.h0; h < w.h1; h += 2) {
@@ -901,6 +910,7 @@ extern "C" int q8_matmul(const int8_t* a, int64_t lda, const float* a_scale, con
     p.blocks_per_split = t.per_split;
     p.halves = (K + kHalfK - 1) / kHalfK;
     p.group = 8;
+    p.repacked = repack;
     const int stage = p.nt * 128 + kWStageBytes;
     p.stages = kRingBytes / stage < kMaxStages ? kRingBytes / stage : kMaxStages;
     p.d_stages = p.nt <= kMaxNT / 2 ? 2 : 1;        // narrow tiles: two accumulators
@@ -918,8 +928,10 @@ extern "C" int q8_matmul(const int8_t* a, int64_t lda, const float* a_scale, con
                      CU_TENSOR_MAP_SWIZZLE_128B)) != DDP_OK)
         return st;
     const int64_t pairs = pieces < d.sm_count / 2 ? pieces : d.sm_count / 2;
+    size_t smem = static_cast<size_t>(p.stages) * stage + 1024;
+    if (smem < kMinTileSmem) smem = kMinTileSmem;
     st = launch_smem(t.splits > 1 ? tile_kernel<kTilePart> : bf16 ? tile_kernel<kTileBf16> : tile_kernel<kTileF32>,
-                     static_cast<unsigned>(2 * pairs), kTileThreads, static_cast<size_t>(p.stages) * stage + 1024, s, p, 2);
+                     static_cast<unsigned>(2 * pairs), kTileThreads, smem, s, p, 2);
     if (st != DDP_OK || t.splits == 1) return st;
     const CombineParams q{parts, a_scale, w_scale, out, ldo, M, N, t.splits};
     return launch_pdl(bf16 ? combine_kernel<true> : combine_kernel<false>,
