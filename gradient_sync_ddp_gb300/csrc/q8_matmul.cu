@@ -38,9 +38,10 @@
 // one (-> 620); the issuing warp converged, descriptors in uniform registers:
 // 130 -> 45 clocks to issue an MMA (-> 562).
 // Few tiles split K (the parts are fp32 in the workspace, combine_kernel adds
-// them in their order).  37 x 8192 x 4096: 16 us, bound by the steps of the
-// pipeline itself: launches and TMEM 6 us, then 16 stages at about 850 clocks of
-// barriers each (12.6 us are left without loads, conversions and MMAs).
+// them in their order).  37 x 8192 x 4096: 15.1 us, bound by the steps of the
+// pipeline itself: launches and TMEM 6 us, then a stage at about 850 clocks of
+// barriers (12.6 us of 16.3 were left without loads, conversions and MMAs, with
+// one block of K a stage; narrow tiles take two).
 // Every wait is bounded; a tile whose wait ran out is written as NaN.
 #include <cstdint>
 
@@ -56,11 +57,11 @@ constexpr int kMaxK = 131071;     // |Σ| < 2^31
 constexpr int kFewTokens = 8;
 constexpr int kCtaN = 128;        // channels per CTA; 256 per pair: the MMA's rows
 constexpr int kMaxNT = 256;       // tokens per tile: an accumulator of 256 columns + 4 channel stages of 64 = 512
-constexpr int kBlockK = 128;      // one stage of the rings
+constexpr int kBlockK = 128;      // a block of K; a stage of the rings is one, or two for narrow tiles
 constexpr int kHalfK = 64;        // a row of 128 bytes in fp16
-constexpr int kWStageBytes = kCtaN * kBlockK;
+constexpr int kWBlockBytes = kCtaN * kBlockK;
 constexpr int kMaxAStages = 4;      // stages of channels in TMEM, 64 columns each; at most the rings' stages
-constexpr int kMaxStages = 6;        // narrow tiles: 37 x 8192 x 4096 at 16.0 us with 6, 16.3 with 12
+constexpr int kMaxStages = 4;        // narrow tiles: more cost time (37 x 8192 x 4096, one block a stage: 15.9 us with 5, 16.3 with 12)
 constexpr int kRingBytes = 212 * 1024;
 // A tile CTA takes all of its SM's TMEM, so never two on one SM: each asks for more than half of the shared memory.
 constexpr size_t kMinTileSmem = 128 * 1024;
@@ -299,7 +300,7 @@ struct TileParams {
     const float* sw;
     void* out;       // or the parts, float [splits][M][N]
     int64_t ldo;
-    int32_t M, N, halves, nt, m_tiles, n_tiles, group, splits, blocks_per_split, stages, a_stages, d_stages, repacked;
+    int32_t M, N, halves, nt, m_tiles, n_tiles, group, splits, stages_per_split, stages, a_stages, d_stages, repacked, subs;   // subs: blocks per stage
 };
 
 struct TileShared {
@@ -331,7 +332,7 @@ __device__ __forceinline__ bool bar_poll(uint64_t* b, uint32_t parity) {
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 100000;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
         : "r"(smem_u32(b)), "r"(parity)
@@ -469,8 +470,8 @@ __device__ __forceinline__ Piece piece(const TileParams& p, int u) {
     const int wide = min(p.group, p.m_tiles - g * p.group);
     w.n0 = r / wide * 2 * kCtaN;
     w.m0 = (g * p.group + r % wide) * p.nt;
-    w.h0 = w.split * p.blocks_per_split * 2;
-    w.h1 = min(p.halves, w.h0 + p.blocks_per_split * 2);
+    w.h0 = w.split * p.stages_per_split * 2 * p.subs;
+    w.h1 = min(p.halves, w.h0 + p.stages_per_split * 2 * p.subs);
     return w;
 }
 
@@ -482,10 +483,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
     __shared__ TileShared s;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = blockIdx.x & 1;
-    const int nth = p.nt / 2, x_half = nth * 128, x_stage = 2 * x_half;
+    const int nth = p.nt / 2, x_half = nth * 128, x_stage = 2 * p.subs * x_half, w_stage = p.subs * kWBlockBytes, hstep = 2 * p.subs;
     const uint32_t pad = (1024u - (smem_u32(raw) & 1023u)) & 1023u;
-    unsigned char* xs = raw + pad;                                   // [stages][2][nt / 2][128]
-    unsigned char* wsm = xs + p.stages * x_stage;                    // [stages][128][128]
+    unsigned char* xs = raw + pad;                                   // [stages][subs][2][nt / 2][128]
+    unsigned char* wsm = xs + p.stages * x_stage;                    // [stages][subs][128][128]
     if (threadIdx.x == 0) {
         for (int i = 0; i < p.stages; ++i) {
             bar_init(&s.x_full[i], 1);
@@ -522,13 +523,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
         pdl_wait();
         for (int u = first; u < pieces && ok; u += pairs) {
             const Piece w = piece(p, u);
-            for (int h = w.h0; h < w.h1; h += 2) {
+            for (int h = w.h0; h < w.h1; h += hstep) {
                 if (!(ok = bar_wait(&s.done[r.i], r.ph ^ 1, s))) break;
-                const bool two = h + 1 < w.h1;
-                bar_expect(&s.x_full[r.i], two ? x_stage : x_half);
+                const int n = min(hstep, w.h1 - h);
+                bar_expect(&s.x_full[r.i], n * x_half);
                 unsigned char* d = xs + r.i * x_stage;
-                tma_load(d, &p.tx, h * kHalfK, w.m0 + rank * nth, &s.x_full[r.i]);
-                if (two) tma_load(d + x_half, &p.tx, (h + 1) * kHalfK, w.m0 + rank * nth, &s.x_full[r.i]);
+                for (int i = 0; i < n; ++i) tma_load(d + i * x_half, &p.tx, (h + i) * kHalfK, w.m0 + rank * nth, &s.x_full[r.i]);
                 r.next(p.stages);
                 ++issued;
             }
@@ -545,10 +545,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
         if (p.repacked) pdl_wait();
         for (int u = first; u < pieces && ok; u += pairs) {
             const Piece w = piece(p, u);
-            for (int h = w.h0; h < w.h1; h += 2) {
+            for (int h = w.h0; h < w.h1; h += hstep) {
                 if (!(ok = bar_wait(&s.w_empty[r.i], r.ph ^ 1, s))) break;
-                bar_expect(&s.w_full[r.i], kWStageBytes);
-                tma_load(wsm + r.i * kWStageBytes, &p.tw, h * kHalfK, w.n0 + rank * kCtaN, &s.w_full[r.i]);
+                const int n = (min(hstep, w.h1 - h) + 1) / 2;
+                bar_expect(&s.w_full[r.i], n * kWBlockBytes);
+                for (int i = 0; i < n; ++i)
+                    tma_load(wsm + r.i * w_stage + i * kWBlockBytes, &p.tw, (h + 2 * i) * kHalfK, w.n0 + rank * kCtaN, &s.w_full[r.i]);
                 r.next(p.stages);
                 ++issued;
             }
@@ -567,14 +569,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
             const Piece w = piece(p, u);
             if (!(ok = __all_sync(0xffffffffu, bar_wait(&s.d_empty[d.i], d.ph ^ 1, s)))) break;
             const uint32_t acc = d.i * p.nt;
-            for (int h = w.h0; h < w.h1; h += 2) {
+            for (int h = w.h0; h < w.h1; h += hstep) {
                 if (!there && !(ok = __all_sync(0xffffffffu, bar_wait(&s.ready[x.i], x.ph, s)))) break;
                 fence_after();
-                const uint64_t desc = smem_desc(xs_addr + x.i * x_stage);
-                const uint32_t at = a_col0 + a * 64;
+                const uint32_t bs = xs_addr + x.i * x_stage, at = a_col0 + a * 64 * p.subs;
+                const int n = min(hstep, w.h1 - h);
                 if (one) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) mma_ts(acc, at + 8 * k, desc + 2 * k, idesc, h > w.h0 || k > 0);
+                    for (int k = 0; k < 4; ++k) mma_ts(acc, at + 8 * k, smem_desc(bs) + 2 * k, idesc, h > w.h0 || k > 0);
                 }
                 // A look at the next stage while these four run: a barrier costs 120 to 300 clocks to look at even
                 // where it is ready, in which the tensor cores would run dry.
@@ -582,9 +584,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
                 y.next(p.stages);
                 there = __all_sync(0xffffffffu, bar_test(&s.ready[y.i], y.ph));
                 if (one) {
-                    if (h + 1 < w.h1) {
+                    for (int i = 1; i < n; ++i) {
+                        const uint64_t desc = smem_desc(bs + i * x_half);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) mma_ts(acc, at + 32 + 8 * k, desc + (x_half >> 4) + 2 * k, idesc, true);
+                        for (int k = 0; k < 4; ++k) mma_ts(acc, at + 32 * i + 8 * k, desc + 2 * k, idesc, true);
                     }
                     mma_commit(&s.done[x.i]);
                 }
@@ -604,7 +607,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
         bool ok = true;
         for (int u = first; u < pieces && ok; u += pairs) {
             const Piece w = piece(p, u);
-            for (int h = w.h0; h < w.h1; h += 2) {
+            for (int h = w.h0; h < w.h1; h += hstep) {
                 if (!(ok = bar_wait(&s.x_full[x.i], x.ph, s))) break;
                 bar_arrive_first(&s.ready[x.i]);
                 x.next(p.stages);
@@ -679,26 +682,29 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
         bool ok = true;
         for (int u = first; u < pieces && ok; u += pairs) {
             const Piece pc = piece(p, u);
-            for (int h = pc.h0; h < pc.h1; h += 2, ++block) {
+            for (int h = pc.h0; h < pc.h1; h += hstep, ++block) {
                 if (!(ok = __all_sync(0xffffffffu, bar_wait(&s.w_full[w.i], w.ph, s)))) break;
+                const unsigned char* src = wsm + w.i * w_stage + row * kBlockK;
                 uint32_t r[32];
-                const unsigned char* src = wsm + w.i * kWStageBytes + row * kBlockK;
+                for (int b = 0; b < p.subs; ++b, src += kWBlockBytes) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const int4 v = *reinterpret_cast<const int4*>(src + (((4 * half + c) ^ (row & 7)) << 4));
-                    widen4(v.x, r[8 * c], r[8 * c + 1]);
-                    widen4(v.y, r[8 * c + 2], r[8 * c + 3]);
-                    widen4(v.z, r[8 * c + 4], r[8 * c + 5]);
-                    widen4(v.w, r[8 * c + 6], r[8 * c + 7]);
+                    for (int c = 0; c < 4; ++c) {
+                        const int4 v = *reinterpret_cast<const int4*>(src + (((4 * half + c) ^ (row & 7)) << 4));
+                        widen4(v.x, r[8 * c], r[8 * c + 1]);
+                        widen4(v.y, r[8 * c + 2], r[8 * c + 3]);
+                        widen4(v.z, r[8 * c + 4], r[8 * c + 5]);
+                        widen4(v.w, r[8 * c + 6], r[8 * c + 7]);
+                    }
+                    if (b == 0 && block >= p.a_stages) {
+                        if (!(ok = __all_sync(0xffffffffu, bar_wait(&s.done[e.i], e.ph, s)))) break;
+                        e.next(p.stages);
+                    }
+                    fence_after();
+                    tmem_st32(a_col0 + (a * p.subs + b) * 64 + half * 32 + lane_base, r);
                 }
+                if (!ok) break;
                 __syncwarp();
                 if (lane == 0) bar_arrive(&s.w_empty[w.i]);
-                if (block >= p.a_stages) {
-                    if (!(ok = __all_sync(0xffffffffu, bar_wait(&s.done[e.i], e.ph, s)))) break;
-                    e.next(p.stages);
-                }
-                fence_after();
-                tmem_st32(a_col0 + a * 64 + half * 32 + lane_base, r);
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 fence_before();
                 __syncwarp();
@@ -802,7 +808,7 @@ constexpr int kMinBlocks = 4;
 constexpr int kMaxSplits = 16;
 constexpr int kPairs = 76;        // of a full GB300: what splits are made for
 struct Tiles {
-    int nt, m_tiles, n_tiles, blocks, splits, per_split;
+    int nt, m_tiles, n_tiles, subs, splits, per_split;   // blocks of K per stage, stages per split
 };
 Tiles plan_tiles(int64_t M, int64_t N, int32_t K) {
     Tiles t{};
@@ -810,13 +816,15 @@ Tiles plan_tiles(int64_t M, int64_t N, int32_t K) {
     t.nt = static_cast<int>(round_up((M + mt - 1) / mt, 16));
     t.m_tiles = static_cast<int>((M + t.nt - 1) / t.nt);
     t.n_tiles = static_cast<int>((N + 2 * kCtaN - 1) / (2 * kCtaN));
-    t.blocks = (K + kBlockK - 1) / kBlockK;
+    // the barriers of a stage take as long as the MMAs of a narrow one: two blocks a stage
+    t.subs = t.nt <= kMaxNT / 2 && K > kBlockK ? 2 : 1;
+    const int stages = (K + t.subs * kBlockK - 1) / (t.subs * kBlockK);
     int64_t s = kPairs / (static_cast<int64_t>(t.m_tiles) * t.n_tiles);
-    if (s > t.blocks / kMinBlocks) s = t.blocks / kMinBlocks;
+    if (s > stages / (kMinBlocks / t.subs)) s = stages / (kMinBlocks / t.subs);
     if (s > kMaxSplits) s = kMaxSplits;
     if (s < 1) s = 1;
-    t.per_split = static_cast<int>((t.blocks + s - 1) / s);
-    t.splits = (t.blocks + t.per_split - 1) / t.per_split;
+    t.per_split = static_cast<int>((stages + s - 1) / s);
+    t.splits = (stages + t.per_split - 1) / t.per_split;
     return t;
 }
 
@@ -907,14 +915,18 @@ extern "C" int q8_matmul(const int8_t* a, int64_t lda, const float* a_scale, con
     p.m_tiles = t.m_tiles;
     p.n_tiles = t.n_tiles;
     p.splits = t.splits;
-    p.blocks_per_split = t.per_split;
+    p.stages_per_split = t.per_split;
     p.halves = (K + kHalfK - 1) / kHalfK;
     p.group = 8;
     p.repacked = repack;
-    const int stage = p.nt * 128 + kWStageBytes;
+    p.subs = t.subs;
+    const int stage = t.subs * (p.nt * 128 + kWBlockBytes);
     p.stages = kRingBytes / stage < kMaxStages ? kRingBytes / stage : kMaxStages;
-    p.d_stages = p.nt <= kMaxNT / 2 ? 2 : 1;        // narrow tiles: two accumulators
-    p.a_stages = p.stages < kMaxAStages ? p.stages : kMaxAStages;
+    // TMEM: accumulators (two of up to 64 columns), then stages of channels
+    p.d_stages = p.nt <= kMaxNT / 4 ? 2 : 1;
+    const int a_room = (512 - (p.d_stages * p.nt + 31) / 32 * 32) / (64 * t.subs);
+    p.a_stages = a_room < kMaxAStages ? a_room : kMaxAStages;
+    if (p.a_stages > p.stages) p.a_stages = p.stages;
     p.M = static_cast<int32_t>(M);
     p.N = static_cast<int32_t>(N);
     p.sa = a_scale;
