@@ -20,9 +20,11 @@
 // thread (16384 x 4099 bf16 124 us, 0.65: γ's columns shift against the
 // vectors).  Matrices that lie differently, and rows wider than the registers
 // hold, take the element loop (two passes over the row).
-// Backward's unaligned rows go by elements (4099 x 2051 fp32 at 0.62, 5000 x
-// 4099 bf16 at 0.34 of the copy rate: requests of 64 bytes); blocks of fixed columns shifted
-// out of two aligned pieces were slower (4099 x 2051 fp32 86 us against 32).
+// Backward keeps a CTA's rows alike (its grid is a multiple of VEC), so that
+// the vectors' columns stay a thread's own there too (5000 x 4099 bf16 46 us,
+// 0.53; 4099 x 2051 fp32 30 us, 0.67; by elements 72 and 32, which matrices that
+// lie differently still take).  Tried: blocks of fixed columns shifted out of
+// two aligned pieces, 4099 x 2051 fp32 86 us.
 // dγ: every thread owns the same columns of all its rows, a CTA's part goes to
 // the workspace and a second kernel adds the parts in their order.
 #include <cstdint>
@@ -384,59 +386,87 @@ struct Packed {
 // Backward, aligned rows, grid-stride: a row's dy, h and dh are all on their
 // way before the first is used, and stay packed in registers.  A thread's
 // columns are the same for every row, so its part of dγ is in registers too.
-// AHEAD: the next row is fetched before this one is reduced.
+// AHEAD: the next row is fetched before this one is reduced.  EDGE: rows off
+// the 16-byte boundaries that lie alike; the grid is a multiple of VEC, so a
+// thread's columns still do not change from row to row.
 // Rows per CTA of the warp-per-row kernel: one CTA per SM, so that dγ has few
 // parts and a warp has 128 registers (8192 x 768 bf16: 13.9 us with 16 warps, 14.6 with 8 and two CTAs per SM, 16.0 with
 // 4 and four; three CTAs of 8 spill).
 constexpr int kGradRows = 16;
 
-template <bool BF16, bool DYBF16, int VPT, bool WARP, bool AHEAD>
+template <bool BF16, bool DYBF16, int VPT, bool WARP, bool AHEAD, bool EDGE>
 __global__ void __launch_bounds__(WARP ? 32 * kGradRows : AHEAD ? 512 : max_group(BF16, VPT))
     norm_grad_kernel(const __grid_constant__ NormGradParams a) {
     constexpr int ES = BF16 ? 2 : 4, VEC = 16 / ES, YS = DYBF16 ? 2 : 4;
     extern __shared__ float part_sh[];   // WARP and a.partial: [kGradRows][D]
     __shared__ float sh[32];
     pdl_enter();
-    const int G = WARP ? 32 : blockDim.x, nvec = a.D / VEC;
+    const int G = WARP ? 32 : blockDim.x;
     const int t = WARP ? threadIdx.x & 31 : threadIdx.x;
     const int w = WARP ? threadIdx.x >> 5 : 0;
     const bool want = a.partial != nullptr;
-    float acc[VPT][VEC] = {};
+    const int64_t row0 = static_cast<int64_t>(blockIdx.x) * (WARP ? kGradRows : 1) + w;
+    const RowShape s = row_shape<BF16, EDGE>(row_ptr<BF16>(a.h, row0, a.ldh), a.D);
+    const int te = G - 1 - t, de = EDGE ? edge_elem<VEC>(s, te) : 0;
+    const bool has_edge = EDGE && te < s.edges;
+    const float gme = has_edge && a.gamma ? __ldg(a.gamma + de) : 1.0f;
+    float acc[VPT][VEC] = {}, acc_e = 0.0f, ge = 0.0f, he = 0.0f, re = 0.0f, ge2 = 0.0f, he2 = 0.0f, re2 = 0.0f;
+    float gk[EDGE && !WARP ? VPT : 1][VEC];          // γ of the thread's columns, where there is room for it
+    auto gamma_of = [&](int i, int v, float (&gm)[VEC]) {
+        if constexpr (EDGE && !WARP) {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) gm[e] = gk[i][e];
+        } else {
+            load_gamma<EDGE, VEC>(a.gamma, a.D, s.lead + v * VEC, gm);
+        }
+    };
     const int64_t stride = static_cast<int64_t>(gridDim.x) * (WARP ? kGradRows : 1);
     Packed<DYBF16, VEC> g[VPT], g2[AHEAD ? VPT : 1];
     Packed<BF16, VEC> h[VPT], r[VPT], h2[AHEAD ? VPT : 1], r2[AHEAD ? VPT : 1];
     float rstd = 0.0f, rstd2 = 0.0f;
-    auto fetch = [&](int64_t row, Packed<DYBF16, VEC>* gg, Packed<BF16, VEC>* hh, Packed<BF16, VEC>* rr, float& rs) {
+    auto fetch = [&](int64_t row, Packed<DYBF16, VEC>* gg, Packed<BF16, VEC>* hh, Packed<BF16, VEC>* rr, float& rs, float& eg, float& eh, float& er) {
         const char* dy = row_ptr<DYBF16>(a.dy, row, a.lddy);
         const char* hp = row_ptr<BF16>(a.h, row, a.ldh);
         const char* dh = a.dh ? row_ptr<BF16>(a.dh, row, a.lddh) : nullptr;
         rs = a.rstd[row];
+        if (has_edge) {
+            eg = load_elem<DYBF16>(dy, de);
+            eh = load_elem<BF16>(hp, de);
+            if (dh) er = load_elem<BF16>(dh, de);
+        }
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int v = t + i * G;
-            if (v < nvec) {
-                gg[i].load(dy + v * VEC * YS);
-                hh[i].load(hp + v * VEC * ES);
-                if (dh) rr[i].load(dh + v * VEC * ES);
+            if (v < s.nvec) {
+                gg[i].load(dy + (s.lead + v * VEC) * YS);
+                hh[i].load(hp + (s.lead + v * VEC) * ES);
+                if (dh) rr[i].load(dh + (s.lead + v * VEC) * ES);
                 else rr[i].zero();
             }
         }
     };
-    int64_t row = static_cast<int64_t>(blockIdx.x) * (WARP ? kGradRows : 1) + w;
-    if (AHEAD && row < a.rows) fetch(row, g, h, r, rstd);
+    int64_t row = row0;
+    if (AHEAD && row < a.rows) fetch(row, g, h, r, rstd, ge, he, re);
     for (; row < a.rows; row += stride) {
         if constexpr (AHEAD) {
-            if (row + stride < a.rows) fetch(row + stride, g2, h2, r2, rstd2);
+            if (row + stride < a.rows) fetch(row + stride, g2, h2, r2, rstd2, ge2, he2, re2);
         } else {
-            fetch(row, g, h, r, rstd);
+            fetch(row, g, h, r, rstd, ge, he, re);
+        }
+        if constexpr (EDGE && !WARP) {
+            if (row == row0) {                       // behind the first row's loads
+#pragma unroll
+                for (int i = 0; i < VPT; ++i)
+                    if (t + i * G < s.nvec) load_gamma<true, VEC>(a.gamma, a.D, s.lead + (t + i * G) * VEC, gk[i]);
+            }
         }
         float sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int v = t + i * G;
-            if (v >= nvec) break;
+            if (v >= s.nvec) break;
             float gm[VEC];
-            load_gamma<false, VEC>(a.gamma, a.D, v * VEC, gm);
+            gamma_of(i, v, gm);
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
                 const float gn = g[i].at(e) * (h[i].at(e) * rstd);
@@ -444,18 +474,24 @@ __global__ void __launch_bounds__(WARP ? 32 * kGradRows : AHEAD ? 512 : max_grou
                 sum = fmaf(gn, gm[e], sum);
             }
         }
+        if constexpr (EDGE) {
+            const float gn = ge * (he * rstd);
+            acc_e += gn;
+            sum = fmaf(gn, gme, sum);
+        }
         const float c = (WARP ? warp_all<SumOp>(sum) : block_all<SumOp>(sum, sh)) / a.D;
         char* dx = row_ptr<BF16>(a.dx, row, a.lddx);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int v = t + i * G;
-            if (v >= nvec) break;
+            if (v >= s.nvec) break;
             float gm[VEC], o[VEC];
-            load_gamma<false, VEC>(a.gamma, a.D, v * VEC, gm);
+            gamma_of(i, v, gm);
 #pragma unroll
             for (int e = 0; e < VEC; ++e) o[e] = fmaf(rstd, g[i].at(e) * gm[e] - h[i].at(e) * rstd * c, r[i].at(e));
-            store_n<BF16, VEC>(dx + v * VEC * ES, o);
+            store_n<BF16, VEC>(dx + (s.lead + v * VEC) * ES, o);
         }
+        if (has_edge) store_elem<BF16>(dx, de, fmaf(rstd, ge * gme - he * rstd * c, re));
         if constexpr (AHEAD) {
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
@@ -464,6 +500,9 @@ __global__ void __launch_bounds__(WARP ? 32 * kGradRows : AHEAD ? 512 : max_grou
                 r[i] = r2[i];
             }
             rstd = rstd2;
+            ge = ge2;
+            he = he2;
+            re = re2;
         }
     }
     if (!want) return;
@@ -471,11 +510,18 @@ __global__ void __launch_bounds__(WARP ? 32 * kGradRows : AHEAD ? 512 : max_grou
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int v = t + i * G;
-        if (v >= nvec) break;
-        float4* d = reinterpret_cast<float4*>((WARP ? part_sh + w * a.D : out) + v * VEC);
+        if (v >= s.nvec) break;
+        float* d = (WARP ? part_sh + w * a.D : out) + s.lead + v * VEC;
+        if constexpr (EDGE) {
 #pragma unroll
-        for (int q = 0; q < VEC / 4; ++q) d[q] = make_float4(acc[i][4 * q], acc[i][4 * q + 1], acc[i][4 * q + 2], acc[i][4 * q + 3]);
+            for (int e = 0; e < VEC; ++e) d[e] = acc[i][e];
+        } else {
+#pragma unroll
+            for (int q = 0; q < VEC / 4; ++q)
+                reinterpret_cast<float4*>(d)[q] = make_float4(acc[i][4 * q], acc[i][4 * q + 1], acc[i][4 * q + 2], acc[i][4 * q + 3]);
+        }
     }
+    if (has_edge) ((WARP ? part_sh + w * a.D : out))[de] = acc_e;
     if constexpr (WARP) {
         __syncthreads();
         for (int d = threadIdx.x; d < a.D; d += 32 * kGradRows) {
@@ -609,13 +655,15 @@ void (*fwd_kernel(Lay lay, const Group& g))(NormParams) {
     if (lay == Lay::kDifferent || g.threads == 0) return norm_loop_kernel<BF16, OUT>;
     return lay == Lay::kAligned ? fwd_kernel<BF16, OUT, false>(g) : fwd_kernel<BF16, OUT, true>(g);
 }
-template <bool BF16, bool DYBF16>
+template <bool BF16, bool DYBF16, bool EDGE>
 void (*bwd_vec(const Group& g))(NormGradParams) {
-    if (g.warp) return g.vpt == 1 ? norm_grad_kernel<BF16, DYBF16, 1, true, false> : g.vpt == 2 ? norm_grad_kernel<BF16, DYBF16, 2, true, false> : g.vpt == 3 ? norm_grad_kernel<BF16, DYBF16, 3, true, false> : norm_grad_kernel<BF16, DYBF16, 4, true, false>;
-    // fetching ahead needs more than 64 registers: 8192 x 4096 bf16 at 52 us with it, 53 without
-    if (g.threads <= 512 && g.vpt <= 2) return g.vpt == 1 ? norm_grad_kernel<BF16, DYBF16, 1, false, true> : norm_grad_kernel<BF16, DYBF16, 2, false, true>;
-    return g.vpt == 1 ? norm_grad_kernel<BF16, DYBF16, 1, false, false> : g.vpt == 2 ? norm_grad_kernel<BF16, DYBF16, 2, false, false> : norm_grad_kernel<BF16, DYBF16, 4, false, false>;
+    if (g.warp) return g.vpt == 1 ? norm_grad_kernel<BF16, DYBF16, 1, true, false, EDGE> : g.vpt == 2 ? norm_grad_kernel<BF16, DYBF16, 2, true, false, EDGE> : g.vpt == 3 ? norm_grad_kernel<BF16, DYBF16, 3, true, false, EDGE> : norm_grad_kernel<BF16, DYBF16, 4, true, false, EDGE>;
+    // fetching ahead needs more than 64 registers: 8192 x 4096 bf16 at 52 us with it, 53 without; off the boundaries
+    // 5000 x 4099 bf16 71 with it, 46 without
+    if (g.threads <= 512 && g.vpt <= 2) return g.vpt == 1 ? norm_grad_kernel<BF16, DYBF16, 1, false, !EDGE, EDGE> : norm_grad_kernel<BF16, DYBF16, 2, false, !EDGE, EDGE>;
+    return g.vpt == 1 ? norm_grad_kernel<BF16, DYBF16, 1, false, false, EDGE> : g.vpt == 2 ? norm_grad_kernel<BF16, DYBF16, 2, false, false, EDGE> : norm_grad_kernel<BF16, DYBF16, 4, false, false, EDGE>;
 }
+
 // Element kernels by width: threads, kernel.
 template <bool BF16, bool DYBF16>
 int bwd_elem(int D, void (**k)(NormGradParams)) {
@@ -640,8 +688,9 @@ int grad_plan(Lay lay, int64_t rows, int D, bool want, int sms, GradPlan* p) {
     const Group g = pick_group(rows, D, BF16, sms);
     int64_t rows_per_cta = 1;
     p->smem = 0;
-    if (lay == Lay::kAligned && g.threads != 0) {
-        p->kernel = bwd_vec<BF16, DYBF16>(g);
+    const bool vec = lay != Lay::kDifferent && g.threads != 0;
+    if (vec) {
+        p->kernel = lay == Lay::kAligned ? bwd_vec<BF16, DYBF16, false>(g) : bwd_vec<BF16, DYBF16, true>(g);
         p->threads = g.warp ? 32 * kGradRows : g.threads;
         rows_per_cta = g.warp ? kGradRows : 1;
         p->smem = g.warp && want ? static_cast<size_t>(kGradRows) * D * 4 : 0;
@@ -652,6 +701,7 @@ int grad_plan(Lay lay, int64_t rows, int D, bool want, int sms, GradPlan* p) {
     const int64_t ctas = (rows + rows_per_cta - 1) / rows_per_cta;
     const int st = one_wave_grid(reinterpret_cast<const void*>(p->kernel), p->threads, ctas, &p->ctas);
     if (p->ctas > kGradCtas) p->ctas = kGradCtas;
+    if (vec && lay == Lay::kAlike && p->ctas < ctas) p->ctas = p->ctas / 8 * 8;   // rows of a CTA lie alike
     return st;
 }
 
