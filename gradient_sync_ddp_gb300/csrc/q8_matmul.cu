@@ -26,8 +26,8 @@
 //                    L2 and shared memory
 //     one issuer     (of the pair's first CTA) tcgen05.mma.cta_group::2, A
 //                    from TMEM, B from shared memory, fp32 accumulator in TMEM
-//     epilogue       two warpgroups: TMEM -> scales -> registers, which frees
-//                    the accumulator; stored under the next tile's contraction
+//     epilogue       two warpgroups: TMEM -> scales -> out, 64 columns at a
+//                    time; the accumulator is free before the last are stored
 // 8192 x 16384 x 4096: 549 us in bursts, 604 held (the clock falls): 2.0 and
 // 1.8 PFLOP/s, 1.05 and 0.96 of the 16-bit rate measured with cuBLAS.  What
 // that took, each by its measurement: 64-token-deep tiles of one CTA 870 us,
@@ -38,7 +38,7 @@
 // one (-> 620); the issuing warp converged, descriptors in uniform registers:
 // 130 -> 45 clocks to issue an MMA (-> 562).
 // Few tiles split K (the parts are fp32 in the workspace, combine_kernel adds
-// them in their order).  37 x 8192 x 4096: 15.1 us, bound by the steps of the
+// them in their order).  37 x 8192 x 4096: 14.7 us, bound by the steps of the
 // pipeline itself: launches and TMEM 6 us, then a stage at about 850 clocks of
 // barriers (12.6 us of 16.3 were left without loads, conversions and MMAs, with
 // one block of K a stage; narrow tiles take two).
@@ -619,7 +619,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
         float* sa = s.sa[warp - 4];
         const int64_t ld = OUT == kTilePart ? p.N : p.ldo;
         constexpr int ES = OUT == kTileBf16 ? 2 : 4;
-        constexpr int BATCH = OUT == kTileBf16 ? 8 : 4;   // chunks of 16 columns held in 64 registers
+        constexpr int BATCH = OUT == kTileBf16 ? 4 : 2;   // chunks of 16 columns held at a time: 32 registers (64 spill)
         for (int u = first; u < pieces; u += pairs) {
             const Piece w = piece(p, u);
             const int64_t n = w.n0 + rank * kCtaN + q * 32 + lane;
@@ -639,7 +639,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
             char* o = static_cast<char*>(p.out) + ((OUT == kTilePart ? static_cast<int64_t>(w.split) * p.M * p.N : 0) + (w.m0 + c0) * ld + n) * ES;
             const uint32_t acc = d.i * p.nt + (static_cast<uint32_t>(q * 32) << 16);
             if (c0 >= c1 && lane == 0) bar_arrive_first(&s.d_empty[d.i]);   // a tile of 16 tokens
-            // The accumulator is read into registers and given back before anything is stored: the next tile waits for it.
+            // The accumulator is given back before the last columns are stored: the next tile waits for it.
             for (int b = c0; b < c1; b += 16 * BATCH) {
                 uint32_t r[BATCH][ES == 2 ? 8 : 16];
 #pragma unroll
