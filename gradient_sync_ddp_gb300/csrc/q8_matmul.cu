@@ -304,7 +304,7 @@ struct TileParams {
 };
 
 struct TileShared {
-    uint64_t x_full[kMaxStages], w_full[kMaxStages], w_empty[kMaxStages];
+    uint64_t w_full[kMaxStages], w_empty[kMaxStages];
     uint64_t ready[kMaxStages];  // of the first CTA: both CTAs' tokens are in shared memory, their channels in TMEM
     uint64_t done[kMaxStages];   // a stage's MMAs: its tokens and its channels in TMEM may be overwritten
     uint64_t d_full[2], d_empty[2], idle;
@@ -319,11 +319,15 @@ __device__ __forceinline__ void bar_init(uint64_t* b, int count) {
 __device__ __forceinline__ void bar_arrive(uint64_t* b) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(b)) : "memory");
 }
-// Arrive on the barrier of the pair's first CTA.
-__device__ __forceinline__ void bar_arrive_first(uint64_t* b) {
+// The barrier of the pair's first CTA at the place of this CTA's.
+__device__ __forceinline__ uint32_t first_of_pair(uint64_t* b) {
     uint32_t r;
     asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(b)));
-    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(r) : "memory");
+    return r;
+}
+// Arrive on it.  Relaxed, so only for reads and writes of TMEM, which the tcgen05 fences about the arrival order.
+__device__ __forceinline__ void bar_arrive_first(uint64_t* b) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(first_of_pair(b)) : "memory");
 }
 __device__ __forceinline__ void bar_expect(uint64_t* b, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(b)), "r"(bytes) : "memory");
@@ -339,11 +343,34 @@ __device__ __forceinline__ bool bar_poll(uint64_t* b, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
-__device__ __forceinline__ bool bar_test(uint64_t* b, uint32_t parity) {   // does not wait
+// For what the other CTA of the pair announces.
+__device__ __forceinline__ bool bar_poll_pair(uint64_t* b, uint32_t parity) {
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(b)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool bar_wait_pair(uint64_t* b, uint32_t parity, TileShared& s) {
+    const long long t0 = clock64();
+    while (!bar_poll_pair(b, parity)) {
+        if (s.failed) return false;
+        if (clock64() - t0 > kWaitClocks) {
+            s.failed = 1;
+            return false;
+        }
+    }
+    return true;
+}
+__device__ __forceinline__ bool bar_test_pair(uint64_t* b, uint32_t parity) {   // does not wait
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
         : "r"(smem_u32(b)), "r"(parity)
@@ -388,6 +415,16 @@ __device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int 
         "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
             smem_u32(dst)),
         "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// Into this CTA's shared memory, told to a barrier of either CTA of the pair: the copy itself orders its bytes before
+// the arrival.  A thread that waits for the copy and arrives with a release takes 8192 x 16384 x 4096 from 553 to 729 us.
+__device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+        "[%4];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
         : "memory");
 }
 
@@ -489,8 +526,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
     unsigned char* wsm = xs + p.stages * x_stage;                    // [stages][subs][128][128]
     if (threadIdx.x == 0) {
         for (int i = 0; i < p.stages; ++i) {
-            bar_init(&s.x_full[i], 1);
-            bar_init(&s.ready[i], 18);                               // of either CTA: eight warps, and word of its tokens
+            bar_init(&s.ready[i], 17);                               // eight warps of either CTA, and the bytes of both's tokens
             bar_init(&s.done[i], 1);
             bar_init(&s.w_full[i], 1);
             bar_init(&s.w_empty[i], 8);
@@ -526,17 +562,19 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
             for (int h = w.h0; h < w.h1; h += hstep) {
                 if (!(ok = bar_wait(&s.done[r.i], r.ph ^ 1, s))) break;
                 const int n = min(hstep, w.h1 - h);
-                bar_expect(&s.x_full[r.i], n * x_half);
+                if (rank == 0) bar_expect(&s.ready[r.i], 2 * n * x_half);
+                const uint32_t bar = first_of_pair(&s.ready[r.i]);
                 unsigned char* d = xs + r.i * x_stage;
-                for (int i = 0; i < n; ++i) tma_load(d + i * x_half, &p.tx, (h + i) * kHalfK, w.m0 + rank * nth, &s.x_full[r.i]);
+                for (int i = 0; i < n; ++i) tma_load_pair(d + i * x_half, &p.tx, (h + i) * kHalfK, w.m0 + rank * nth, bar);
                 r.next(p.stages);
                 ++issued;
             }
         }
-        // every copy has landed before the CTA gives its shared memory back
+        // Every copy has landed before the CTA gives its shared memory back: what has been multiplied has, and where a
+        // wait ran out, this one's limit is far longer than a copy takes.
         for (int j = 0; j < p.stages && j < issued; ++j) {
             r.back(p.stages);
-            bar_drain(&s.x_full[r.i], r.ph, s);
+            bar_drain(&s.done[r.i], r.ph, s);
         }
     } else if (warp == 2 && lane == 0) {                // channel producer
         Ring r;
@@ -570,7 +608,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
             if (!(ok = __all_sync(0xffffffffu, bar_wait(&s.d_empty[d.i], d.ph ^ 1, s)))) break;
             const uint32_t acc = d.i * p.nt;
             for (int h = w.h0; h < w.h1; h += hstep) {
-                if (!there && !(ok = __all_sync(0xffffffffu, bar_wait(&s.ready[x.i], x.ph, s)))) break;
+                if (!there && !(ok = __all_sync(0xffffffffu, bar_wait_pair(&s.ready[x.i], x.ph, s)))) break;
                 fence_after();
                 const uint32_t bs = xs_addr + x.i * x_stage, at = a_col0 + a * 64 * p.subs;
                 const int n = min(hstep, w.h1 - h);
@@ -582,7 +620,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
                 // where it is ready, in which the tensor cores would run dry.
                 Ring y = x;
                 y.next(p.stages);
-                there = __all_sync(0xffffffffu, bar_test(&s.ready[y.i], y.ph));
+                there = __all_sync(0xffffffffu, bar_test_pair(&s.ready[y.i], y.ph));
                 if (one) {
                     for (int i = 1; i < n; ++i) {
                         const uint64_t desc = smem_desc(bs + i * x_half);
@@ -601,17 +639,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
         if (one) {
             mma_commit(&s.idle);
             bar_drain(&s.idle, 0, s);
-        }
-    } else if (warp == 3 && lane == 0) {                // this CTA's tokens are there: told to the first
-        Ring x;
-        bool ok = true;
-        for (int u = first; u < pieces && ok; u += pairs) {
-            const Piece w = piece(p, u);
-            for (int h = w.h0; h < w.h1; h += hstep) {
-                if (!(ok = bar_wait(&s.x_full[x.i], x.ph, s))) break;
-                bar_arrive_first(&s.ready[x.i]);
-                x.next(p.stages);
-            }
         }
     } else if (warp >= 4 && warp < 12) {                // epilogue: warp's channels, half of the tokens
         Ring d;
@@ -642,6 +669,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
             // The accumulator is given back before the last columns are stored: the next tile waits for it.
             for (int b = c0; b < c1; b += 16 * BATCH) {
                 uint32_t r[BATCH][ES == 2 ? 8 : 16];
+                __syncwarp();
 #pragma unroll
                 for (int i = 0; i < BATCH; ++i) {
                     const int c = b + 16 * i;
