@@ -477,7 +477,7 @@ int distill(const void* z, int64_t ldz, int32_t dtype, const void* index, int64_
         return DDP_ERR_INVALID_ARG;
     const float c = static_cast<float>(1.4426950408889634 / static_cast<double>(tau));
     if (!(c > 1.2e-38f) || !(c < 3.0e38f)) return DDP_ERR_INVALID_ARG;
-    if (k > kMaxTop) return DDP_ERR_UNSUPPORTED;
+    if (k > kMaxTop || V > kMaxWidth) return DDP_ERR_UNSUPPORTED;
     const int es = dsize(dtype);
     const Mat mz{z, T, V, ldz, es}, mi{index, T, k, ldi, index_bits / 8}, mt{teacher, T, k, ldt, dsize(t_dtype)},
         mli{lse_in, 1, T, T, 4}, mdl{dloss, 1, T, T, 4}, ml{loss, 1, T, T, 4}, mle{lse, 1, T, T, 4},

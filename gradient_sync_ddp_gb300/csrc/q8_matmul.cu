@@ -890,7 +890,7 @@ Tiles plan_tiles(int64_t M, int64_t N, int32_t K) {
 using namespace ddp;
 
 extern "C" size_t q8_matmul_workspace_bytes(int64_t M, int64_t N, int32_t K) {
-    if (M < 0 || N < 0 || K < 0 || K > kMaxK || M > INT32_MAX || N > INT32_MAX) return 0;
+    if (M < 0 || N < 0 || K < 0 || K > kMaxK || M > kMaxWidth || N > kMaxWidth) return 0;
     if (M <= kFewTokens || N == 0 || K == 0) return 16;
     const Tiles t = plan_tiles(M, N, K);
     return token_bytes(M, K) + channel_bytes(N, K) + (t.splits > 1 ? static_cast<size_t>(t.splits) * M * N * 4 : 0);
@@ -900,7 +900,7 @@ extern "C" int q8_matmul(const int8_t* a, int64_t lda, const float* a_scale, con
                          const float* w_scale, int64_t M, int64_t N, int32_t K, void* out, int64_t ldo,
                          int32_t out_dtype, void* workspace, size_t workspace_bytes, void* stream) {
     if ((out_dtype != DDP_F32 && out_dtype != DDP_BF16) || M < 0 || N < 0 || K < 0) return DDP_ERR_INVALID_ARG;
-    if (K > kMaxK || M > INT32_MAX || N > INT32_MAX) return DDP_ERR_UNSUPPORTED;
+    if (K > kMaxK || M > kMaxWidth || N > kMaxWidth) return DDP_ERR_UNSUPPORTED;
     const Mat ma{a, M, K, lda, 1}, mw{w, N, K, ldw, 1}, mo{out, M, N, ldo, out_dtype == DDP_BF16 ? 2 : 4},
         msa{a_scale, 1, M, M, 4}, msw{w_scale, 1, N, N, 4};
     if (!mat_valid(ma) || !mat_valid(mw) || !mat_valid(mo)) return DDP_ERR_INVALID_ARG;

@@ -709,6 +709,7 @@ int forward(const void* x, int64_t ldx, const void* residual, int64_t ldr, int32
             int64_t rows, int32_t D, float eps, void* h_out, int64_t ldh, void* y, int64_t ldy, int out,
             float* scale, float* rstd_out, void* stream) {
     if (!dtype_ok(in_dtype) || rows < 0 || D < 1 || !(eps >= 0.0f) || !(eps < 3.0e38f)) return DDP_ERR_INVALID_ARG;
+    if (D > kMaxWidth) return DDP_ERR_UNSUPPORTED;
     const int es = dsize(in_dtype), ys = out == kOutQ8 ? 1 : out == kOutBf16 ? 2 : 4;
     const Mat mx{x, rows, D, ldx, es}, mr{residual, rows, D, ldr, es}, mh{h_out, rows, D, ldh, es},
         my{y, rows, D, ldy, ys}, mg{gamma, 1, D, D, 4}, ms{scale, 1, rows, rows, 4}, mt{rstd_out, 1, rows, rows, 4};
@@ -767,7 +768,7 @@ extern "C" int rmsnorm_forward_q8(const void* x, int64_t ldx, const void* residu
 }
 
 extern "C" size_t rmsnorm_backward_workspace_bytes(int64_t rows, int32_t D) {
-    return rows < 0 || D < 1 ? 0 : static_cast<size_t>(grad_parts(rows)) * static_cast<size_t>(D) * 4;
+    return rows < 0 || D < 1 || D > kMaxWidth ? 0 : static_cast<size_t>(grad_parts(rows)) * static_cast<size_t>(D) * 4;
 }
 
 extern "C" int rmsnorm_backward(const void* dy, int64_t lddy, int32_t dy_dtype, const void* h, int64_t ldh,
@@ -775,6 +776,7 @@ extern "C" int rmsnorm_backward(const void* dy, int64_t lddy, int32_t dy_dtype, 
                                 int64_t rows, int32_t D, void* dx, int64_t lddx, float* dgamma, void* workspace,
                                 size_t workspace_bytes, void* stream) {
     if (!dtype_ok(dy_dtype) || !dtype_ok(h_dtype) || rows < 0 || D < 1) return DDP_ERR_INVALID_ARG;
+    if (D > kMaxWidth) return DDP_ERR_UNSUPPORTED;
     const int es = dsize(h_dtype);
     const size_t need = dgamma ? rmsnorm_backward_workspace_bytes(rows, D) : 0;
     const Mat my{dy, rows, D, lddy, dsize(dy_dtype)}, mh{h, rows, D, ldh, es}, md{dh, rows, D, lddh, es},

@@ -115,6 +115,9 @@ __device__ __forceinline__ void block_all2(float& a, float& b, float2* sh) {
 
 // ---- host: a matrix argument of a call --------------------------------
 
+// Columns of a row: their numbers, rounded up to what a CTA takes at a time, fit 32 bits.
+constexpr int64_t kMaxWidth = (1ll << 31) - 65536;
+
 struct Mat {
     const void* p;
     int64_t rows, cols, ld;   // ld in elements

@@ -613,7 +613,8 @@ int dist_sampler_indices_from(int64_t n_items, int32_t n_replicas, int32_t rank,
  *   y             device [rows, D], out_dtype; may be x or residual itself
  *                 when the dtypes match, not h_out
  *   rstd_out      device float[rows] or NULL (the backward pass reads it)
- * Sums are fp32.  rows == 0 enqueues nothing.
+ * Sums are fp32.  rows == 0 enqueues nothing.  D <= 2^31 - 65536 here and
+ * below (DDP_ERR_UNSUPPORTED beyond).
  */
 int rmsnorm_forward(const void* x, int64_t ldx, const void* residual, int64_t ldr, int32_t in_dtype,
                     const float* gamma, int64_t rows, int32_t D, float eps, void* h_out, int64_t ldh,
@@ -667,8 +668,10 @@ size_t q8_matmul_workspace_bytes(int64_t M, int64_t N, int32_t K);
  *   workspace    device buffer of q8_matmul_workspace_bytes(M, N, K), 16-byte
  *                aligned, contents ignored on entry; overlapping calls need
  *                different ones
- * K <= 131071, M and N < 2^31 (DDP_ERR_UNSUPPORTED beyond).  K == 0 gives
- * zeros (0*a_scale*w_scale).
+ * K <= 131071, M and N <= 2^31 - 65536 (DDP_ERR_UNSUPPORTED beyond).  K == 0
+ * gives zeros (0*a_scale*w_scale).  Sums are 32-bit integers (up to 8 tokens)
+ * or fp32, exact there while partial sums stay within 2^24: always for
+ * K <= 1024; past that a partial sum is rounded to fp32.
  */
 int q8_matmul(const int8_t* a, int64_t lda, const float* a_scale, const int8_t* w, int64_t ldw,
               const float* w_scale, int64_t M, int64_t N, int32_t K, void* out, int64_t ldo, int32_t out_dtype,
@@ -688,7 +691,8 @@ int q8_matmul(const int8_t* a, int64_t lda, const float* a_scale, const int8_t* 
  *                   an index outside [0, V) is no entry (pad lists with -1);
  *                   an index may occur more than once
  *   teacher         device [T, k], teacher_dtype
- *   k               0 .. DDP_DISTILL_MAX_TOP (DDP_ERR_UNSUPPORTED beyond)
+ *   k               0 .. DDP_DISTILL_MAX_TOP, V <= 2^31 - 65536
+ *                   (DDP_ERR_UNSUPPORTED beyond)
  *   temperature     > 0
  *   loss            device float[T]
  *   lse             device float[T] or NULL (the backward pass reads it)

@@ -167,3 +167,21 @@ def test_binding_checks_tensors(g):
                                 stream=0)
     with pytest.raises(g.DdpError):
         g.distill_topk_forward(z, torch.zeros(3, 2, dtype=torch.int32), t, torch.zeros(3), temperature=0.0, stream=0)
+
+
+def test_widths_that_32_bits_cannot_count(g):
+    """Column numbers, rounded up to what a CTA takes at a time, would pass 2^31."""
+    h, U, wide = g.lib_handle(), g.DDP_ERR_UNSUPPORTED, 2**31 - 65535
+    assert norm(g, rows=1, D=wide, ldx=wide, ldr=wide, ldh=wide, ldy=wide) == U
+    assert h.rmsnorm_forward_q8(at(0), wide, None, wide, 1, None, 1, wide, 1e-6, None, wide, at(4), wide, at(6), None,
+                                None) == U
+    assert h.rmsnorm_backward(at(0), wide, 1, at(1), wide, 1, at(2), None, None, wide, 1, wide, at(3), wide, None, None,
+                              0, None) == U
+    assert h.q8_matmul(at(0), 64, at(1), at(2), 64, at(3), 1, wide, 64, at(4), wide, 0, at(5), 1 << 20, None) == U
+    assert h.q8_matmul(at(0), 64, at(1), at(2), 64, at(3), wide, 1, 64, at(4), 1, 0, at(5), 1 << 20, None) == U
+    assert h.q8_matmul_workspace_bytes(wide, 64, 64) == h.q8_matmul_workspace_bytes(64, wide, 64) == 0
+    assert h.rmsnorm_backward_workspace_bytes(4, wide) == 0
+    t = (at(1), 8, 32, at(2), 8, 0, 1, wide, 8, 1.0)
+    assert h.distill_topk_forward(at(0), wide, 1, *t, at(3), None, None) == U
+    assert h.distill_topk_backward(at(0), wide, 1, *t, at(3), None, at(4), wide, None) == U
+    assert h.distill_topk_forward_backward(at(0), wide, 1, *t, None, at(3), None, at(4), wide, None) == U
