@@ -28,8 +28,8 @@
 //                    from TMEM, B from shared memory, fp32 accumulator in TMEM
 //     epilogue       two warpgroups: TMEM -> scales -> out, 64 columns at a
 //                    time; the accumulator is free before the last are stored
-// 8192 x 16384 x 4096: 549 us in bursts, 604 held (the clock falls): 2.0 and
-// 1.8 PFLOP/s, 1.05 and 0.96 of the 16-bit rate measured with cuBLAS.  What
+// 8192 x 16384 x 4096: 553 us in bursts, 609 held (the clock falls): 2.0 and
+// 1.8 PFLOP/s, 1.05 and 0.95 of the 16-bit rate measured with cuBLAS.  What
 // that took, each by its measurement: 64-token-deep tiles of one CTA 870 us,
 // held by L2 -> SM traffic (65 bytes per clock and SM); the pair halves what
 // tokens cost; arrivals across the pair without release (1438 -> 1063); one
@@ -38,7 +38,7 @@
 // one (-> 620); the issuing warp converged, descriptors in uniform registers:
 // 130 -> 45 clocks to issue an MMA (-> 562).
 // Few tiles split K (the parts are fp32 in the workspace, combine_kernel adds
-// them in their order).  37 x 8192 x 4096: 14.7 us, bound by the steps of the
+// them in their order).  37 x 8192 x 4096: 14.8 us, bound by the steps of the
 // pipeline itself: launches and TMEM 6 us, then a stage at about 850 clocks of
 // barriers (12.6 us of 16.3 were left without loads, conversions and MMAs, with
 // one block of K a stage; narrow tiles take two).
