@@ -441,12 +441,14 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
         "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
         : "memory");
 }
-// The barrier of both CTAs arrives when the MMAs issued so far are done.
+// The barrier arrives when the MMAs issued so far are done: that of the first CTA, and with BOTH that of the second at
+// the same place.  An arrival is under way until a thread of its CTA has seen it, so each is waited for there.
+template <bool BOTH = true>
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
             smem_u32(bar)),
-        "h"(static_cast<uint16_t>(3))
+        "h"(static_cast<uint16_t>(BOTH ? 3 : 1))
         : "memory");
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -637,7 +639,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
             d.next(p.d_stages);
         }
         if (one) {
-            mma_commit(&s.idle);
+            mma_commit<false>(&s.idle);                 // no one in the second CTA waits for it
             bar_drain(&s.idle, 0, s);
         }
     } else if (warp >= 4 && warp < 12) {                // epilogue: warp's channels, half of the tokens

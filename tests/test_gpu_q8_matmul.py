@@ -163,3 +163,26 @@ def test_offsets_past_32_bits(g):
     run(g, a, sa, w, sw, o)
     rows = torch.tensor([0, 1, 21399, M - 200, M - 2, M - 1], device="cuda")
     check(a[rows], sa[rows], w, sw, o[rows])
+
+
+def test_products_end_before_others_take_their_place(g):
+    """Tile kernels of different rings one behind the other and among row kernels, with no wait between them: whatever
+    a tile's CTAs still had under way when they end would land in the next one's shared memory and barriers."""
+    shapes = [(300, 512, 64), (16, 4096, 1024), (513, 640, 200), (64, 300, 4096), (9, 256, 128), (1000, 257, 48)]
+    calls = []
+    for i, (M, N, K) in enumerate(shapes):
+        a, w, sa, sw = ints(M, K, 40 + i), ints(N, K, 50 + i), scales(M, 60 + i), scales(N, 70 + i)
+        ws = torch.empty(g.q8_matmul_workspace_bytes(M, N, K), dtype=torch.uint8, device="cuda")
+        calls.append((a, sa, w, sw, torch.empty(M, N, device="cuda"), ws))
+    x = torch.ones(600, 768, device="cuda")
+    ys = [torch.empty_like(x) for _ in range(3)]
+    sync()
+    for r in range(12):
+        for i in range(len(calls)):
+            g.q8_matmul(*calls[(i * (1 + r % 2) + r) % len(calls)])
+            if (i + r) % 3 == 0:
+                g.rmsnorm_forward(x, None, ys[i % 3], 0.0)
+    sync()
+    for a, sa, w, sw, out, _ in calls:
+        check(a, sa, w, sw, out)
+    assert all(torch.equal(y, x) for y in ys)
