@@ -263,9 +263,8 @@ __device__ __forceinline__ void widen4(uint32_t v, uint32_t& lo, uint32_t& hi) {
     hi = *reinterpret_cast<const uint32_t*>(&y);
 }
 
-// Lets the tile kernel begin only once everything before this kernel is
-// done: its CTAs then read channels and scales while tokens are widened, and
-// wait for this grid where they need its output.
+// Lets the tile kernel begin once everything before this kernel is done: its
+// CTAs set up their barriers and TMEM while tokens are widened.
 __global__ void __launch_bounds__(kThreads) widen_kernel(const __grid_constant__ WidenParams p) {
     pdl_wait();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -300,7 +299,7 @@ struct TileParams {
     const float* sw;
     void* out;       // or the parts, float [splits][M][N]
     int64_t ldo;
-    int32_t M, N, halves, nt, m_tiles, n_tiles, group, splits, stages_per_split, stages, a_stages, d_stages, repacked, subs;   // subs: blocks per stage
+    int32_t M, N, halves, nt, m_tiles, n_tiles, group, splits, stages_per_split, stages, a_stages, d_stages, subs;   // subs: blocks per stage
 };
 
 struct TileShared {
@@ -552,13 +551,15 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
     // all 512 columns are this pair's, from address 0 on
     const uint32_t a_col0 = (p.d_stages * p.nt + 31) / 32 * 32, xs_addr = smem_u32(xs);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // Every thread waits for the tokens' grid itself, those that read none of its output too: what the calls before it
+    // wrote (scales, channels) is visible to a thread that has waited, and to no other.  No bounded wait begins before.
+    pdl_wait();
     const int pieces = p.m_tiles * p.n_tiles * p.splits, first = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
     if (warp == 0 && lane == 0) {                       // token producer
         Ring r;
         int issued = 0;
         bool ok = true;
-        pdl_wait();
         for (int u = first; u < pieces && ok; u += pairs) {
             const Piece w = piece(p, u);
             for (int h = w.h0; h < w.h1; h += hstep) {
@@ -582,7 +583,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
         Ring r;
         int issued = 0;
         bool ok = true;
-        if (p.repacked) pdl_wait();
         for (int u = first; u < pieces && ok; u += pairs) {
             const Piece w = piece(p, u);
             for (int h = w.h0; h < w.h1; h += hstep) {
@@ -976,7 +976,6 @@ extern "C" int q8_matmul(const int8_t* a, int64_t lda, const float* a_scale, con
     p.stages_per_split = t.per_split;
     p.halves = (K + kHalfK - 1) / kHalfK;
     p.group = 8;
-    p.repacked = repack;
     p.subs = t.subs;
     const int stage = t.subs * (p.nt * 128 + kWBlockBytes);
     p.stages = kRingBytes / stage < kMaxStages ? kRingBytes / stage : kMaxStages;

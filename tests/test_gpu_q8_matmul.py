@@ -186,3 +186,28 @@ def test_products_end_before_others_take_their_place(g):
     for a, sa, w, sw, out, _ in calls:
         check(a, sa, w, sw, out)
     assert all(torch.equal(y, x) for y in ys)
+
+
+@pytest.mark.parametrize("M,N,K", [(3, 640, 512), (24, 512, 1024), (40, 2048, 768), (700, 1000, 256)])
+def test_operands_written_just_before(g, M, N, K):
+    """Norm and product enqueued again and again into the same 8-bit rows and scales, the channels and their scales
+    rewritten on the way: every product reads what the calls right before it wrote."""
+    steps = 8
+    xs = [torch.randn(M, K, device="cuda") * 4.0 ** i for i in range(steps)]
+    ws_, sws = [ints(N, K, 80 + i) for i in range(2)], [scales(N, 82 + i) for i in range(2)]
+    a, sa = torch.empty(M, K, device="cuda", dtype=torch.int8), torch.empty(M, device="cuda")
+    w, sw = ws_[0].clone(), sws[0].clone()
+    outs = [torch.empty(M, N, device="cuda") for _ in range(steps)]
+    work = torch.empty(g.q8_matmul_workspace_bytes(M, N, K), dtype=torch.uint8, device="cuda")
+    sync()
+    for i in range(steps):
+        if i == steps // 2:
+            w.copy_(ws_[1])
+            sw.copy_(sws[1])
+        g.rmsnorm_forward_q8(xs[i], None, a, sa, float(i))           # another eps, another scale, every time
+        g.q8_matmul(a, sa, w, sw, outs[i], work)
+    sync()
+    for i in range(steps):
+        g.rmsnorm_forward_q8(xs[i], None, a, sa, float(i))
+        sync()
+        check(a, sa, ws_[i >= steps // 2], sws[i >= steps // 2], outs[i])
