@@ -39,7 +39,8 @@ constexpr int kScanTop = 32;          // up to this many entries repeats are fou
 constexpr float kLog2eLow = 1.9259629911e-8f;   // log2(e) − kLog2e
 constexpr int64_t kRowsInL2 = 90ll << 20;   // of the rows in hand, so that the second pass finds them there
 constexpr float kMasked = 1.0e4f;     // logits beyond this are no reference
-constexpr float kFar = 1.0e37f;       // beyond this, z·c may overflow: exponents from (z − max)·c instead
+constexpr float kFar = 1.0e37f;       // of m·c: beyond this the product may overflow
+constexpr float kNear = 4096.0f;      // of m·c: beyond this its spacing is felt beside ln V and ln|dloss|, and exponents are (z − m)·c
 
 struct DistillParams {
     const void* z;
@@ -383,10 +384,10 @@ __global__ void __launch_bounds__(kDistillThreads, 4) distill_kernel(const __gri
         }
     } else {
         M = lse_in * kLog2e;                             // with what the product rounds off, below
-        m = lse_in * a.tau;
+        m = fminf(fmaxf(lse_in * a.tau, -3.4e38f), 3.4e38f);
     }
-    // Logits whose product with c may overflow (a row that a mask of the type's lowest value leaves whole): differences first.
-    const bool far = !(fabsf(m) * fmaxf(a.c, 1.0f) < kFar) && fabsf(m) < INFINITY;
+    // Logits far from 0 beside the temperature (a row that a finite mask leaves whole): differences first.
+    const bool far = !(fabsf(m) * a.c <= kNear) && fabsf(FWD ? m : lse_in) < INFINITY;
     if constexpr (FWD) {
         if (far) {                                       // rare, and every CTA of the token sums the whole row itself
             float all = 0.0f, none = 0.0f;
@@ -396,8 +397,8 @@ __global__ void __launch_bounds__(kDistillThreads, 4) distill_kernel(const __gri
             if (BWD && a.cluster > 1) cluster_sync();    // every read of the row lies before any write
         }
     }
-    // q_v = 2^(z·c − M − ls)
-    const float ls = FWD ? log2f(sum) : far ? 0.0f : fmaf(lse_in, kLog2e, -M) + lse_in * kLog2eLow;
+    // q_v = 2^(z·c − M − ls), far: 2^((z − m)·c − ls); of a kept lse, ls is what rounding M or m left
+    const float ls = FWD ? log2f(sum) : far ? fmaf(lse_in, a.tau, -m) * a.c : fmaf(lse_in, kLog2e, -M) + lse_in * kLog2eLow;
     auto q2 = [&](float x) { return (far ? (x - m) * a.c : fmaf(x, a.c, -M)) - ls; };
     if constexpr (FWD) {
         if (rank == 0) {

@@ -144,6 +144,61 @@ def test_row_masked_whole(g, T, V, dt):
         check(z, index, t, up, tau, loss, lse, dz, rows=slice(0, 1))
 
 
+def shifted(T, V, dt, common, seed=3):
+    """Logits about a large common value, and what is left of them without it (exact: neighbours in the type)."""
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(seed)
+    z = (torch.randn(T, V, generator=gen, device="cuda") * 2.5 + common).to(DT[dt])
+    base = torch.tensor(float(common), device="cuda").to(DT[dt])
+    return z, (z.double() - base.double())
+
+
+@pytest.mark.parametrize("common", [2e3, 3e3, -3e3, 1e5, -1e5, 1e6, -1e9, 1e20])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("T,V", [(3, 515), (3, 4096), (2, 40000), (700, 1003)])
+def test_large_common_value(g, T, V, dt, common):
+    """A shift of all of a token's logits changes neither loss nor gradient, whatever |dloss|.  The logits' differences
+    are exact, so only they enter the bound."""
+    _, index, t, up = make(T, V, 7, dt)
+    z, rest = shifted(T, V, dt, common)
+    if rest.abs().amax() > 100:                # the type's spacing there: only rows of one value are left to compare
+        z = torch.full_like(z, common)
+        rest = torch.zeros_like(rest)
+    for tau, w in ((1.0, up), (2.5, up / 8192), (1.0, -up * 2.0 ** -30)):
+        loss, lse, dz = torch.empty(T, device="cuda"), torch.empty(T, device="cuda"), torch.empty_like(z)
+        g.distill_topk_forward_backward(z, index, t, w, loss, lse, dz, temperature=tau)
+        only = torch.empty_like(loss)
+        g.distill_topk_forward(z, index, t, only, temperature=tau)
+        sync()
+        check(rest, index, t, w, tau, loss, None, dz, rows=slice(0, 8))
+        assert torch.equal(only, loss)
+        want = torch.logsumexp(z.double() / tau, 1)
+        # m·c and its product with ln 2 round a few times; E of these sizes is below 1e-4
+        assert torch.all((lse.double() - want).abs() <= 8 * U * want.abs() + 1e-4)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("common", [3e3, -3e3, 2e4, -2e4])
+def test_kept_lse_of_large_logits(g, dt, common):
+    """The gradient from a kept fp32 lse is that of exp(z/τ − lse) with the lse as it was rounded."""
+    T, V, k = 5, 1003, 7
+    _, index, t, up = make(T, V, k, dt)
+    z, rest = shifted(T, V, dt, common)
+    for tau in (1.0, 2.5, 3.0):
+        exact = torch.logsumexp(z.double() / tau, 1)
+        dz = torch.empty_like(z)
+        g.distill_topk_backward(z, index, t, exact.float(), up, dz, temperature=tau)
+        sync()
+        q = torch.exp(z.double() / tau - exact.float().double()[:, None])
+        p = torch.zeros_like(q).scatter_add_(1, index, torch.softmax(t.double() / tau, 1))
+        gw = up.double()[:, None] * tau
+        # as in check, with the size of the exponents' own terms: lse·log2(e) and z·c are rounded as they are
+        E = (V / 128 + 64) * U + 16 * U * (float(rest.abs().amax() + t.abs().amax()) + abs(common)) / tau + 2.0 ** -20
+        rnd = 2.0 ** -8 if dt == "bf16" else U
+        want = gw * (q - p)
+        assert torch.all((dz.double() - want).abs() <= gw.abs() * 2 * E * (q + p) + rnd * want.abs() + 1e-37)
+
+
 def test_zero_weight_and_special_logits(g):
     z, index, t, up = make(5, 700, 8, "f32")
     up[0] = 0.0
