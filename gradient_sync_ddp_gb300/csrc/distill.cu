@@ -38,7 +38,7 @@ constexpr int kHash = 2 * kMaxTop;
 constexpr int kScanTop = 32;          // up to this many entries repeats are found by scanning all pairs
 constexpr float kLog2eLow = 1.9259629911e-8f;   // log2(e) − kLog2e
 constexpr int64_t kRowsInL2 = 90ll << 20;   // of the rows in hand, so that the second pass finds them there
-constexpr float kMasked = 1.0e4f;     // logits beyond this are no reference
+constexpr float kSlack = 100.0f;      // what lies 2^100 below the token's reference is nothing beside it
 constexpr float kFar = 1.0e37f;       // of m·c: beyond this the product may overflow
 constexpr float kNear = 4096.0f;      // of m·c: beyond this its spacing is felt beside ln V and ln|dloss|, and exponents are (z − m)·c
 
@@ -53,7 +53,7 @@ struct DistillParams {
     void* dz;
     int64_t ldz, ldi, ldt, lddz, T;
     int32_t V, k;
-    float tau, c;          // c = log2(e) / τ
+    float tau, c, top;     // c = log2(e) / τ; top·c a little below kNear
     int32_t t_bf16, i_64, cluster;
 };
 
@@ -270,24 +270,34 @@ __global__ void __launch_bounds__(kDistillThreads, 4) distill_kernel(const __gri
         if (tid == 0) s_twice = hash ? 0 : 1;
     }
 
-    // The sum takes no maximum: fp32 holds 2^±126 about any reference near the thread's logits, and its first vector
-    // gives one (0 where that is masked).  A token that a thread's sum leaves the middle of that range for (logits 40
-    // nats above the reference, or masked references and very low logits) is summed again with a running maximum.
+    // The sum takes no maximum: fp32 holds 2^±126 about any reference near the thread's logits, and the first of its
+    // vectors that is not masked (top·c > −kNear) gives one; its own top then makes the sum about 1 or more, so that
+    // what the join drops, under 2^-126 of at most 1e18, is nothing beside it.  Masked vectors before it add 0:
+    // the token's reference, once known, says whether they count.  A token that a thread's sum leaves that range for
+    // (logits 40 nats above the reference), or whose reference is itself near the masks, is summed again with a
+    // running maximum.
     Running run;
     bool out = false;
     if constexpr (FWD) {
         const uint64_t c2 = pair(a.c, a.c);
         uint64_t s2 = 0, n2 = 0;
         bool begun = false;
+        auto begin = [&](float top) {
+            if (top * a.c <= -kNear) {                   // not a NaN
+                run.m = fmaxf(run.m, top);
+                return false;
+            }
+            run.m = fminf(top, a.top);
+            run.mc = __fmul_rn(run.m, a.c);
+            n2 = pair(-run.mc, -run.mc);
+            return true;
+        };
         each_vector<BF16, true>(s, [&](int, const uint4& v) {
             if (!begun) {
-                begun = true;
                 float top = vec_elem<BF16>(v, 0);
 #pragma unroll
-                for (int e = 1; e < VEC; ++e) top = fmaxf(top, vec_elem<BF16>(v, e));
-                run.m = top > -kMasked ? fminf(top, kMasked) : 0.0f;
-                run.mc = run.m * a.c;
-                n2 = pair(-run.mc, -run.mc);
+                for (int e = 1; e < VEC; ++e) top = max_nan(top, vec_elem<BF16>(v, e));
+                begun = begin(top);                      // else n2 is 0, and 2^(z·c) as well
             }
             uint64_t part = pow2_pair(fma2(vec_pair<BF16>(v, 0), c2, n2));
 #pragma unroll
@@ -297,11 +307,8 @@ __global__ void __launch_bounds__(kDistillThreads, 4) distill_kernel(const __gri
         float s_lo, s_hi;
         unpair(s2, s_lo, s_hi);
         run.s = s_lo + s_hi;
-        out = begun && !(run.s > 1.0e-18f && run.s < 1.0e18f);
-        if (has_edge) {
-            run.raise(xe, a.c);
-            run.s += pow2(fmaf(xe, a.c, -run.mc));
-        }
+        if (has_edge && (begun || (begun = begin(xe)))) run.s += pow2(fmaf(xe, a.c, -run.mc));
+        out = begun && !(run.s > 0.5f && run.s < 1.0e18f);
     }
 
     // what the entries are, and the logits at those that this CTA writes or sums (another's slice may hold gradients)
@@ -321,7 +328,7 @@ __global__ void __launch_bounds__(kDistillThreads, 4) distill_kernel(const __gri
     float m = out ? INFINITY : run.m;
     once_all2<MaxOp, MaxNanOp>(m, tm, sh[0]);
     if constexpr (FWD) {
-        if (m == INFINITY) {                             // again, with a running maximum (or a logit is infinite)
+        if (m == INFINITY || (m * a.c <= kSlack - kNear && m > -INFINITY)) {   // again, with a running maximum
             run = Running();
             each_vector<BF16, true>(s, [&](int, const uint4& v) {
                 float top = -INFINITY;
@@ -507,7 +514,7 @@ int distill(const void* z, int64_t ldz, int32_t dtype, const void* index, int64_
            (T * cluster < 2ll * d.sm_count || (fwd && bwd && 4ll * d.sm_count / cluster * V * es > kRowsInL2)))
         cluster *= 2;
     if (T * cluster > INT32_MAX) return DDP_ERR_UNSUPPORTED;
-    const DistillParams p{z, index, teacher, lse_in, dloss, loss, lse, dz, ldz, ldi, ldt, lddz, T, V, k, tau, c,
+    const DistillParams p{z, index, teacher, lse_in, dloss, loss, lse, dz, ldz, ldi, ldt, lddz, T, V, k, tau, c, fminf(0.999f * kNear / c, 3.4e38f),
                           t_dtype == DDP_BF16, index_bits == 64, cluster};
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(T * cluster));

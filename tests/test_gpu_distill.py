@@ -199,6 +199,44 @@ def test_kept_lse_of_large_logits(g, dt, common):
         assert torch.all((dz.double() - want).abs() <= gw.abs() * 2 * E * (q + p) + rnd * want.abs() + 1e-37)
 
 
+def low_rows(T, V, dt, mask, slices, seed=5):
+    """Rows of low logits: at the start of every slice a masked 16-byte vector and a stretch of -88 on the first vectors
+    of a CTA's other threads, then -46 on what the masked one's thread reads and -52 elsewhere; rows of random levels
+    and random masked vectors; rows of which a long stretch is masked."""
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(seed)
+    vec = 8 if dt == "bf16" else 4
+    per = -(-(-(-V // slices)) // 128) * 128
+    i = torch.arange(V, device="cuda") % per // vec
+    z = torch.full((T, V), -52.0, device="cuda")
+    z[:, i % 256 == 0] = -46.0
+    z[:, (i > 0) & (i < 256)] = -88.0
+    z[:, i == 0] = mask
+    levels = torch.tensor([-88.0, -52.0, -46.0, -10.0, 0.0, 9.0], device="cuda")
+    z[1::4] = levels[torch.randint(0, 6, (V // vec + 1,), generator=gen, device="cuda")].repeat_interleave(vec)[:V]
+    z[2::4] = levels[torch.randint(0, 2, (V // vec + 1,), generator=gen, device="cuda")].repeat_interleave(vec)[:V]
+    off = torch.rand(V // vec + 1, generator=gen, device="cuda").repeat_interleave(vec)[:V] < 0.3
+    z[1:2, off] = mask
+    z[2:3, off] = mask
+    z[3::4] = torch.randn(V, generator=gen, device="cuda") * 2.5 - 20
+    z[3::4, V // 8:V - V // 16] = mask
+    return z.to(DT[dt])
+
+
+@pytest.mark.parametrize("mask", [float("-inf"), -1e4])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("T,V,slices", [(320, 50176, 1), (4, 50176, 8), (4, 16384, 4), (320, 2051, 1)])
+def test_masked_vectors_among_low_logits(g, T, V, slices, dt, mask):
+    _, index, t, up = make(T, V, 5, dt)
+    z = low_rows(T, V, dt, mask, slices)
+    index = torch.arange(V - 5, V, device="cuda").repeat(T, 1)         # not masked: the loss is finite
+    z[:, V - 5:] = -52.0
+    for tau in (1.0, 2.0):
+        for got in all_three(g, z, index, t, up, tau):
+            finite = z.masked_fill(z <= -9e3, -1e3)                    # as far as any mask: R is of the logits that count
+            check(finite, index, t, up, tau, *got, rows=slice(0, 4))
+
+
 def test_zero_weight_and_special_logits(g):
     z, index, t, up = make(5, 700, 8, "f32")
     up[0] = 0.0
