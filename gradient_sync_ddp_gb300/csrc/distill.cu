@@ -39,7 +39,7 @@ constexpr int kScanTop = 32;          // up to this many entries repeats are fou
 constexpr float kLog2eLow = 1.9259629911e-8f;   // log2(e) − kLog2e
 constexpr int64_t kRowsInL2 = 90ll << 20;   // of the rows in hand, so that the second pass finds them there
 constexpr float kSlack = 100.0f;      // what lies 2^100 below the token's reference is nothing beside it
-constexpr float kFar = 1.0e37f;       // of m·c: beyond this the product may overflow
+constexpr float kHuge = 3.4028235e38f;   // the largest finite number
 constexpr float kNear = 4096.0f;      // of m·c: beyond this its spacing is felt beside ln V and ln|dloss|, and exponents are (z − m)·c
 
 struct DistillParams {
@@ -86,15 +86,14 @@ __device__ __forceinline__ float cluster_read(const float* p, uint32_t rank) {
     return v;
 }
 
-// Largest m of z and Σ 2^(z·c − mc), mc = m·c kept within ±kFar.
+// Largest m of z, kept finite, and Σ 2^((z − m)·c): of differences, for m·c itself may round by more than any exponent.
 struct Running {
-    float m = -INFINITY, mc = 0.0f, s = 0.0f;
+    float m = -kHuge, s = 0.0f;
     __device__ __forceinline__ void raise(float to, float c) {
         if (to > m) {
+            to = fminf(to, kHuge);
+            s *= pow2((m - to) * c);
             m = to;
-            const float n = fminf(fmaxf(to * c, -kFar), kFar);
-            s = s == 0.0f ? 0.0f : s * pow2(mc - n);
-            mc = n;
         }
     }
 };
@@ -227,7 +226,7 @@ __device__ __forceinline__ void once_all2(float& a, float& b, float2* sh) {
 template <bool BF16, bool FWD, bool BWD>
 __global__ void __launch_bounds__(kDistillThreads, 4) distill_kernel(const __grid_constant__ DistillParams a) {
     constexpr int VEC = BF16 ? 8 : 4;
-    __shared__ float2 sh[3][kDistillThreads / 32];
+    __shared__ float2 sh[2][kDistillThreads / 32];
     __shared__ float s_part[2];                      // this CTA's (m, s), read by its cluster
     __shared__ float s_loss[kDistillThreads / 32];
     __shared__ int s_idx[BWD ? kMaxTop : 1];
@@ -276,7 +275,7 @@ __global__ void __launch_bounds__(kDistillThreads, 4) distill_kernel(const __gri
     // the token's reference, once known, says whether they count.  A token that a thread's sum leaves that range for
     // (logits 40 nats above the reference), or whose reference is itself near the masks, is summed again with a
     // running maximum.
-    Running run;
+    float ref = -INFINITY, mc = 0.0f, part = 0.0f;      // reference (without one the largest masked logit), ref·c, sum
     bool out = false;
     if constexpr (FWD) {
         const uint64_t c2 = pair(a.c, a.c);
@@ -284,12 +283,12 @@ __global__ void __launch_bounds__(kDistillThreads, 4) distill_kernel(const __gri
         bool begun = false;
         auto begin = [&](float top) {
             if (top * a.c <= -kNear) {                   // not a NaN
-                run.m = fmaxf(run.m, top);
+                ref = fmaxf(ref, top);
                 return false;
             }
-            run.m = fminf(top, a.top);
-            run.mc = __fmul_rn(run.m, a.c);
-            n2 = pair(-run.mc, -run.mc);
+            ref = fminf(top, a.top);
+            mc = __fmul_rn(ref, a.c);
+            n2 = pair(-mc, -mc);
             return true;
         };
         each_vector<BF16, true>(s, [&](int, const uint4& v) {
@@ -299,16 +298,16 @@ __global__ void __launch_bounds__(kDistillThreads, 4) distill_kernel(const __gri
                 for (int e = 1; e < VEC; ++e) top = max_nan(top, vec_elem<BF16>(v, e));
                 begun = begin(top);                      // else n2 is 0, and 2^(z·c) as well
             }
-            uint64_t part = pow2_pair(fma2(vec_pair<BF16>(v, 0), c2, n2));
+            uint64_t v2 = pow2_pair(fma2(vec_pair<BF16>(v, 0), c2, n2));
 #pragma unroll
-            for (int e = 1; e < VEC / 2; ++e) part = add2(part, pow2_pair(fma2(vec_pair<BF16>(v, e), c2, n2)));
-            s2 = add2(s2, part);
+            for (int e = 1; e < VEC / 2; ++e) v2 = add2(v2, pow2_pair(fma2(vec_pair<BF16>(v, e), c2, n2)));
+            s2 = add2(s2, v2);
         });
         float s_lo, s_hi;
         unpair(s2, s_lo, s_hi);
-        run.s = s_lo + s_hi;
-        if (has_edge && (begun || (begun = begin(xe)))) run.s += pow2(fmaf(xe, a.c, -run.mc));
-        out = begun && !(run.s > 0.5f && run.s < 1.0e18f);
+        part = s_lo + s_hi;
+        if (has_edge && (begun || (begun = begin(xe)))) part += pow2(fmaf(xe, a.c, -mc));
+        out = begun && !(part > 0.5f && part < 1.0e18f);
     }
 
     // what the entries are, and the logits at those that this CTA writes or sums (another's slice may hold gradients)
@@ -325,27 +324,33 @@ __global__ void __launch_bounds__(kDistillThreads, 4) distill_kernel(const __gri
     }
 
     // maxima of the logits and of the entries, then their sums
-    float m = out ? INFINITY : run.m;
+    float m = out ? INFINITY : ref;
     once_all2<MaxOp, MaxNanOp>(m, tm, sh[0]);
+    bool diff = false;                                   // sums are of 2^((z − m)·c), not of 2^(z·c − M)
     if constexpr (FWD) {
-        if (m == INFINITY || (m * a.c <= kSlack - kNear && m > -INFINITY)) {   // again, with a running maximum
-            run = Running();
+        diff = m == INFINITY || (m * a.c <= kSlack - kNear && m > -INFINITY);
+        if (diff) {                                      // again, with a running maximum
+            Running run;
             each_vector<BF16, true>(s, [&](int, const uint4& v) {
                 float top = -INFINITY;
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) top = fmaxf(top, vec_elem<BF16>(v, e));
                 run.raise(top, a.c);
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) run.s += pow2(fmaf(vec_elem<BF16>(v, e), a.c, -run.mc));
+                for (int e = 0; e < VEC; ++e) run.s += pow2((vec_elem<BF16>(v, e) - run.m) * a.c);
             });
             if (has_edge) {
                 run.raise(xe, a.c);
-                run.s += pow2(fmaf(xe, a.c, -run.mc));
+                run.s += pow2((xe - run.m) * a.c);
             }
             m = run.m;
             float none = 0.0f;
             __syncthreads();
             once_all2<MaxOp, SumOp>(m, none, sh[0]);
+            part = run.s * pow2((run.m - m) * a.c);
+        } else {
+            m = fmaxf(m, -kHuge);
+            part = part == 0.0f ? 0.0f : part * pow2(mc - __fmul_rn(m, a.c));
         }
     }
     const bool some = !(tm == -INFINITY);
@@ -365,47 +370,39 @@ __global__ void __launch_bounds__(kDistillThreads, 4) distill_kernel(const __gri
             }
         }
     }
-    float M = fminf(fmaxf(m * a.c, -kFar), kFar);
-    float sum = run.s == 0.0f ? 0.0f : run.s * pow2(run.mc - M);
+    float sum = part;
     once_all2<SumOp, SumOp>(sum, ts, sh[1]);
+    float M = __fmul_rn(m, a.c);
     if constexpr (FWD) {
         if (a.cluster > 1) {
             if (tid == 0) {
                 s_part[0] = m;
-                s_part[1] = sum;
+                s_part[1] = diff || sum == 0.0f ? sum : sum * pow2(-fmaf(m, a.c, -M));
             }
             cluster_sync();
             float pm[kMaxCluster], ps[kMaxCluster];
-            m = -INFINITY;
+            m = -kHuge;
 #pragma unroll
             for (int r = 0; r < kMaxCluster; ++r) {
-                pm[r] = r < a.cluster ? cluster_read(&s_part[0], r) : -INFINITY;
+                pm[r] = r < a.cluster ? cluster_read(&s_part[0], r) : -kHuge;
                 ps[r] = r < a.cluster ? cluster_read(&s_part[1], r) : 0.0f;
                 m = fmaxf(m, pm[r]);
             }
-            M = fminf(fmaxf(m * a.c, -kFar), kFar);
             sum = 0.0f;
 #pragma unroll
-            for (int r = 0; r < kMaxCluster; ++r)
-                sum += ps[r] == 0.0f ? 0.0f : ps[r] * pow2(fminf(fmaxf(pm[r] * a.c, -kFar), kFar) - M);
+            for (int r = 0; r < kMaxCluster; ++r) sum += ps[r] * pow2((pm[r] - m) * a.c);
+            M = __fmul_rn(m, a.c);
+            diff = true;
         }
     } else {
         M = lse_in * kLog2e;                             // with what the product rounds off, below
-        m = fminf(fmaxf(lse_in * a.tau, -3.4e38f), 3.4e38f);
+        m = fminf(fmaxf(lse_in * a.tau, -kHuge), kHuge);
     }
     // Logits far from 0 beside the temperature (a row that a finite mask leaves whole): differences first.
-    const bool far = !(fabsf(m) * a.c <= kNear) && fabsf(FWD ? m : lse_in) < INFINITY;
-    if constexpr (FWD) {
-        if (far) {                                       // rare, and every CTA of the token sums the whole row itself
-            float all = 0.0f, none = 0.0f;
-            for (int v = tid; v < a.V; v += kDistillThreads) all += pow2((load_elem<BF16>(z, v) - m) * a.c);
-            once_all2<SumOp, SumOp>(all, none, sh[2]);
-            sum = all;
-            if (BWD && a.cluster > 1) cluster_sync();    // every read of the row lies before any write
-        }
-    }
+    const bool far = !(fabsf(M) <= kNear) && (FWD || fabsf(lse_in) < INFINITY);
     // q_v = 2^(z·c − M − ls), far: 2^((z − m)·c − ls); of a kept lse, ls is what rounding M or m left
-    const float ls = FWD ? log2f(sum) : far ? fmaf(lse_in, a.tau, -m) * a.c : fmaf(lse_in, kLog2e, -M) + lse_in * kLog2eLow;
+    const float ls = FWD ? log2f(sum) + (diff && !far ? fmaf(m, a.c, -M) : 0.0f)
+                         : far ? fmaf(lse_in, a.tau, -m) * a.c : fmaf(lse_in, kLog2e, -M) + lse_in * kLog2eLow;
     auto q2 = [&](float x) { return (far ? (x - m) * a.c : fmaf(x, a.c, -M)) - ls; };
     if constexpr (FWD) {
         if (rank == 0) {
@@ -514,7 +511,7 @@ int distill(const void* z, int64_t ldz, int32_t dtype, const void* index, int64_
            (T * cluster < 2ll * d.sm_count || (fwd && bwd && 4ll * d.sm_count / cluster * V * es > kRowsInL2)))
         cluster *= 2;
     if (T * cluster > INT32_MAX) return DDP_ERR_UNSUPPORTED;
-    const DistillParams p{z, index, teacher, lse_in, dloss, loss, lse, dz, ldz, ldi, ldt, lddz, T, V, k, tau, c, fminf(0.999f * kNear / c, 3.4e38f),
+    const DistillParams p{z, index, teacher, lse_in, dloss, loss, lse, dz, ldz, ldi, ldt, lddz, T, V, k, tau, c, fminf(0.999f * kNear / c, kHuge),
                           t_dtype == DDP_BF16, index_bits == 64, cluster};
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(T * cluster));

@@ -237,6 +237,44 @@ def test_masked_vectors_among_low_logits(g, T, V, slices, dt, mask):
             check(finite, index, t, up, tau, *got, rows=slice(0, 4))
 
 
+@pytest.mark.parametrize("mask", [-1e4, -1e9, -1e10, -1e15, -1e20, -1e30])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("T,V", [(8, 2051), (8, 40000), (700, 2048), (320, 9000)])
+def test_finite_masks(g, T, V, dt, mask):
+    """Masks that are neither -infinity nor the type's lowest value: over one vector, a thread's or a cluster's whole
+    share of the row, all but one logit, the whole row, and over none."""
+    _, index, t, up = make(T, V, 4, dt)
+    z = (torch.randn(T, V, device="cuda", generator=torch.Generator("cuda").manual_seed(7)) * 2.5).to(DT[dt])
+    z[1, 8:16] = mask
+    z[2, :V // 2] = mask
+    z[3, V // 2:] = mask
+    z[4, torch.arange(V, device="cuda") != int(index[4, 1])] = mask
+    z[5] = mask
+    z[6, torch.arange(V, device="cuda") // 8 % 256 == 3] = mask
+    z[7] = mask
+    z[7, ::3] = 2 * mask
+    index[4] = index[4, 1].clone()
+    index[2] = torch.where(index[2] < V // 2, -1, index[2])
+    index[3] = torch.where(index[3] < V // 2, index[3], -1)
+    index[6] = V - 1 - torch.arange(4, device="cuda") * 8
+    index[7] = torch.arange(4, device="cuda") * 3 + 1
+    flat = z.masked_fill(z <= -5e3, -1e3)                 # nothing beside the others, where there are others
+    flat[5] = 0.0
+    flat[7] = 0.0
+    flat[7, ::3] = -1e3
+    flat[6, index[6]], z[6, index[6]] = 1.0, 1.0
+    for tau in (1.0, 2.0):
+        (loss, lse, dz), (loss2, lse2, dz2) = all_three(g, z, index, t, up, tau)
+        check(flat, index, t, up, tau, loss, None, dz, rows=slice(0, 8))
+        check(flat, index, t, up, tau, loss2, None, None, rows=slice(0, 8))
+        usual = torch.tensor([0, 1, 2, 3, 4, 6], device="cuda")
+        check(flat, index, t, up, tau, loss2, lse2, dz2, rows=usual)
+        check(flat, index, t, up, tau, None, lse, None, rows=usual)
+        want = torch.logsumexp(z[[5, 7]].double() / tau, 1)
+        for got in (lse, lse2):
+            assert torch.all((got[[5, 7]].double() - want).abs() <= 8 * U * want.abs() + 1e-4)
+
+
 def test_zero_weight_and_special_logits(g):
     z, index, t, up = make(5, 700, 8, "f32")
     up[0] = 0.0
