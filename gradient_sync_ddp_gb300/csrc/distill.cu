@@ -398,8 +398,9 @@ __global__ void __launch_bounds__(kDistillThreads, 4) distill_kernel(const __gri
         M = lse_in * kLog2e;                             // with what the product rounds off, below
         m = fminf(fmaxf(lse_in * a.tau, -kHuge), kHuge);
     }
-    // Logits far from 0 beside the temperature (a row that a finite mask leaves whole): differences first.
-    const bool far = !(fabsf(M) <= kNear) && (FWD || fabsf(lse_in) < INFINITY);
+    // Logits far from 0 beside the temperature (a row that a finite mask leaves whole): differences first.  m is finite,
+    // so that an lse of ±infinity lies in ls: q is 0 at every finite logit, and NaN at one that is infinite as it is.
+    const bool far = !(fabsf(M) <= kNear);
     // q_v = 2^(z·c − M − ls), far: 2^((z − m)·c − ls); of a kept lse, ls is what rounding M or m left
     const float ls = FWD ? log2f(sum) + (diff && !far ? fmaf(m, a.c, -M) : 0.0f)
                          : far ? fmaf(lse_in, a.tau, -m) * a.c : fmaf(lse_in, kLog2e, -M) + lse_in * kLog2eLow;

@@ -697,7 +697,10 @@ int q8_matmul(const int8_t* a, int64_t lda, const float* a_scale, const int8_t* 
  *   loss            device float[T]
  *   lse             device float[T] or NULL (the backward pass reads it)
  * A token without entries, or whose entries are all -infinity, has loss 0.
- * Entries and logits of -infinity have probability 0.
+ * Entries and logits of -infinity have probability 0.  A logit of +infinity
+ * gives lse +infinity: q is 0 at the finite logits, NaN there.  A token with
+ * entries whose logits are all -infinity has no q: lse -infinity, loss and
+ * gradient NaN.
  */
 int distill_topk_forward(const void* logits, int64_t ldz, int32_t dtype, const void* index, int64_t ldi,
                          int32_t index_bits, const void* teacher, int64_t ldt, int32_t teacher_dtype, int64_t T,

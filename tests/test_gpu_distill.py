@@ -297,6 +297,34 @@ def test_zero_weight_and_special_logits(g):
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("T,V", [(6, 515), (6, 40000), (700, 1001)])
+def test_infinite_logits(g, T, V, dt):
+    """+infinity at a word that is no entry, at an entry, at two words; -infinity throughout: one call and two agree on
+    what the formulas leave, q = 0 at finite logits and NaN at the infinite one."""
+    z, index, t, up = make(T, V, 4, dt)
+    inf = float("inf")
+    hit = torch.zeros(T, V, dtype=torch.bool, device="cuda").scatter_(1, index, True)
+    word = int((~hit[0]).nonzero()[0])
+    z[0, word] = inf
+    z[1, int(index[1, 2])] = inf
+    z[2, int((~hit[2]).nonzero()[5])], z[2, V - 1] = inf, inf
+    z[3], z[4], index[4] = -inf, -inf, -1
+    for tau in (1.0, 2.5):
+        for loss, lse, dz in all_three(g, z, index, t, up, tau):
+            assert torch.all(lse[:3] == inf) and torch.all(lse[3:5] == -inf)
+            assert loss[0] == inf and torch.isnan(loss[1]) and torch.isnan(loss[3]) and loss[4] == 0
+            p = torch.zeros(T, V, dtype=torch.float64, device="cuda").scatter_(1, index.clamp(0), torch.softmax(t.double() / tau, 1))
+            for r in range(3):
+                at = z[r] == inf
+                want = -(up[r].double() * tau) * p[r]
+                # a softmax of four terms; the type's rounding
+                tol = (2.0 ** -18 + (2.0 ** -8 if dt == "bf16" else U)) * want.abs()
+                assert torch.isnan(dz[r][at]).all() and torch.all(((dz[r].double() - want).abs() <= tol)[~at])
+            assert torch.isnan(dz[3]).all() and not dz[4].any()
+            check(z, index, t, up, tau, loss, lse, dz, rows=slice(5, 6))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
 @pytest.mark.parametrize("T,V", [(7, 515), (3, 50257), (300, 1001)])
 def test_strides_offsets_and_in_place(g, T, V, dt):
     k = 6
