@@ -161,17 +161,24 @@ __device__ __forceinline__ void store_vec_anywhere(char* d, const uint4& w) {
     }
 }
 
+// A probability's exponent: a kept lse of far logits, rounded by more than ln V, would allow any number.
+__device__ __forceinline__ float at_most_one(float x) { return x > 0.0f ? 0.0f : x; }   // NaN stays
+
 // dz = g·q over a slice; the exponent of q as FAR says.  A bf16 dz has |g| in the exponent and its sign set
 // afterwards; an fp32 dz keeps them apart, for the larger exponent would round more.
 template <bool BF16, bool FAR, bool KEEP>
 __device__ __forceinline__ void write_grad(const Slice& s, char* dz, float c, float M, float m, float ls, float g, bool has_edge, int ve, float xe) {
     constexpr int ES = BF16 ? 2 : 4, VEC = 16 / ES;
-    const float off = (FAR ? ls : M + ls) - log2f(fabsf(g));
+    const float lg = log2f(fabsf(g)), off = M + ls - lg;
     const uint32_t sign = BF16 && g < 0.0f ? 0x80008000u : 0u;
     const uint64_t c2 = pair(c, c), n2 = pair(-off, -off);
     auto f = [&](float z) {
-        if constexpr (BF16) return pow2(FAR ? fmaf(z - m, c, -off) : fmaf(z, c, -off));
-        else return g * pow2((FAR ? (z - m) * c : fmaf(z, c, -M)) - ls);
+        if constexpr (FAR) {
+            const float x = at_most_one((z - m) * c - ls);
+            return BF16 ? pow2(x + lg) : g * pow2(x);
+        } else {
+            return BF16 ? pow2(fmaf(z, c, -off)) : g * pow2(fmaf(z, c, -M) - ls);
+        }
     };
     char* dv = dz + static_cast<int64_t>(s.v0 + s.lead) * ES;
     const bool whole = (reinterpret_cast<uintptr_t>(dv) & 15) == 0;
@@ -404,7 +411,7 @@ __global__ void __launch_bounds__(kDistillThreads, 4) distill_kernel(const __gri
     // q_v = 2^(z·c − M − ls), far: 2^((z − m)·c − ls); of a kept lse, ls is what rounding M or m left
     const float ls = FWD ? log2f(sum) + (diff && !far ? fmaf(m, a.c, -M) : 0.0f)
                          : far ? fmaf(lse_in, a.tau, -m) * a.c : fmaf(lse_in, kLog2e, -M) + lse_in * kLog2eLow;
-    auto q2 = [&](float x) { return (far ? (x - m) * a.c : fmaf(x, a.c, -M)) - ls; };
+    auto q2 = [&](float x) { return far ? at_most_one((x - m) * a.c - ls) : fmaf(x, a.c, -M) - ls; };
     if constexpr (FWD) {
         if (rank == 0) {
             const float lts = log2f(ts);

@@ -711,8 +711,8 @@ int distill_topk_forward(const void* logits, int64_t ldz, int32_t dtype, const v
  *     dlogits[v] = dloss*t*(q_v - sum_{j: index_j = v} p_j)
  *   lse       what the forward pass wrote, in fp32: off by up to |lse|*2^-24.
  *             Of a token whose logits are far from 0 (all of them masked with
- *             -1e9, say) it cannot carry the logarithm of a sum, and q is off
- *             by that much; distill_topk_forward_backward needs no lse and
+ *             -1e9, say) it cannot carry the logarithm of a sum, and q, at
+ *             most 1, is off by that factor; distill_topk_forward_backward needs no lse and
  *             depends on the logits' differences only
  *   dloss     device float[T] or NULL (1): the gradient of each token's loss;
  *             a token of dloss 0 (or without entries) has gradient 0,

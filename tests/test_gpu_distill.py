@@ -199,6 +199,21 @@ def test_kept_lse_of_large_logits(g, dt, common):
         assert torch.all((dz.double() - want).abs() <= gw.abs() * 2 * E * (q + p) + rnd * want.abs() + 1e-37)
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("T,V", [(64, 515), (64, 40000), (700, 515)])
+def test_kept_lse_that_cannot_carry_the_sum(g, T, V, dt):
+    """Rows of one value near -1e9: whatever the fp32 lse rounds to, q stays a probability."""
+    _, index, t, up = make(T, V, 5, dt)
+    z = (-1e9 - 448.0 * torch.arange(T, device="cuda") * (1 if dt == "f32" else 2.0 ** 14))[:, None].expand(T, V).to(DT[dt]).contiguous()
+    loss, lse, dz = torch.empty(T, device="cuda"), torch.empty(T, device="cuda"), torch.empty_like(z)
+    for tau in (1.0, 1.5, 3.0):
+        g.distill_topk_forward(z, index, t, loss, lse, temperature=tau)
+        g.distill_topk_backward(z, index, t, lse, up, dz, temperature=tau)
+        sync()
+        # g·(q − p) with 0 <= q, p <= 1 lies within |g|, and a rounding
+        assert torch.all(dz.double().abs() <= up.double().abs()[:, None] * tau * (1 + 2.0 ** -8))
+
+
 def low_rows(T, V, dt, mask, slices, seed=5):
     """Rows of low logits: at the start of every slice a masked 16-byte vector and a stretch of -88 on the first vectors
     of a CTA's other threads, then -46 on what the masked one's thread reads and -52 elsewhere; rows of random levels
