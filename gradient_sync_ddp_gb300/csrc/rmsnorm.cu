@@ -29,6 +29,7 @@
 // the workspace and a second kernel adds the parts in their order.
 #include <cstdint>
 
+#include "row_grid.h"
 #include "rows.cuh"
 
 namespace ddp {
@@ -701,7 +702,7 @@ int grad_plan(Lay lay, int64_t rows, int D, bool want, int sms, GradPlan* p) {
     const int64_t ctas = (rows + rows_per_cta - 1) / rows_per_cta;
     const int st = one_wave_grid(reinterpret_cast<const void*>(p->kernel), p->threads, ctas, &p->ctas);
     if (p->ctas > kGradCtas) p->ctas = kGradCtas;
-    if (vec && lay == Lay::kAlike && p->ctas < ctas) p->ctas = p->ctas / 8 * 8;   // rows of a CTA lie alike
+    if (vec && lay == Lay::kAlike) p->ctas = alike_grid(p->ctas, ctas);
     return st;
 }
 
