@@ -118,6 +118,29 @@ def test_backward(g, rows, D, dt, dyt):
         assert torch.equal(only, dx)
 
 
+@pytest.mark.parametrize("rows,D,ld,at", [
+    (1500, 4099, 4099, 0), (5000, 515, 515, 0), (5000, 255, 255, 0), (700, 8195, 8195, 0),      # odd rows, packed
+    (1500, 2051, 2056, 3), (1500, 2048, 2051, 0), (5000, 512, 515, 0), (5000, 500, 509, 5), (2500, 16, 17, 0)])
+@pytest.mark.parametrize("dt,dyt", [("bf16", "bf16"), ("f32", "f32"), ("f32", "bf16"), ("bf16", "f32")])
+def test_backward_of_many_unaligned_rows(g, rows, D, ld, at, dt, dyt):
+    """Several rows to a CTA or warp, off the 16-byte boundaries, all matrices alike: odd widths, odd pitches with even
+    widths, odd bases with aligned pitches."""
+    def cut(seed, std, t):
+        return rand((rows * ld + 16,), seed, std, DT[t])[at:at + rows * ld].view(rows, ld)[:, :D]
+    h, dy, dh = cut(80, 2.0, dt), cut(81, 0.5, dyt), cut(82, 0.5, dt)
+    gamma = 1 + rand((D,), 83, 0.1)
+    rstd = torch.rsqrt((h.double() ** 2).mean(1) + 1e-5).float()
+    flat = torch.full((rows * ld + 16,), 3.0, device="cuda", dtype=DT[dt])
+    dx, dgamma = flat[at:at + rows * ld].view(rows, ld)[:, :D], torch.full((D,), float("nan"), device="cuda")
+    ws = torch.empty(g.rmsnorm_backward_workspace_bytes(rows, D), dtype=torch.uint8, device="cuda")
+    ws.fill_(255)
+    g.rmsnorm_backward(dy, h, rstd, gamma, dx, dgamma, ws, dh=dh)
+    sync()
+    check_backward(dy, h, rstd, gamma, dh, dx, dgamma)
+    assert torch.all(flat[at:at + rows * ld].view(rows, ld)[:, D:] == 3)
+    assert torch.all(flat[:at] == 3) and torch.all(flat[at + rows * ld:] == 3)
+
+
 def check_backward(dy, h, rstd, gamma, dh, dx, dgamma):
     rows, D = h.shape
     dyw, n = f64(dy), f64(h) * f64(rstd)[:, None]
