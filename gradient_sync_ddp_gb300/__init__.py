@@ -552,7 +552,6 @@ class _Torch:
     @classmethod
     def load(cls):
         import torch
-        cls.codes = {torch.float32: F32, torch.bfloat16: BF16}
         cls.f32, cls.bf16, cls.i8, cls.i32, cls.i64 = (torch.float32, torch.bfloat16, torch.int8, torch.int32,
                                                        torch.int64)
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -560,6 +559,7 @@ class _Torch:
             cls.stream = staticmethod(lambda: torch.cuda.current_stream().cuda_stream)
         else:
             cls.stream = staticmethod(lambda: raw(torch.cuda.current_device()))
+        cls.codes = {torch.float32: F32, torch.bfloat16: BF16}      # last: another thread that finds it goes on
 
 
 def _launch_stream(stream) -> int:
