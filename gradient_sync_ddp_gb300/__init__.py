@@ -603,6 +603,12 @@ def _vec(t, name: str, n: int):
     return t.data_ptr()
 
 
+def _n32(n: int) -> int:
+    """A size for a 32-bit argument (ctypes would keep its low bits): what does not fit becomes the largest number, which
+    every call refuses."""
+    return n if -2**31 <= n < 2**31 else 2**31 - 1
+
+
 def _bytes(ws) -> int:
     return 0 if ws is None else ws.numel() * ws.element_size()
 
@@ -615,7 +621,7 @@ def rmsnorm_forward(x, gamma, y, eps: float = 1e-6, residual=None, h_out=None, r
     pr, ldr = _mat(residual, "residual", x.shape, x.dtype)
     ph, ldh = _mat(h_out, "h_out", x.shape, x.dtype)
     py, ldy = _mat(y, "y", x.shape)
-    _check(_lib.rmsnorm_forward(px, ldx, pr, ldr, code, _vec(gamma, "gamma", D), rows, D, eps, ph, ldh,
+    _check(_lib.rmsnorm_forward(px, ldx, pr, ldr, code, _vec(gamma, "gamma", D), rows, _n32(D), eps, ph, ldh,
                                 py, ldy, _code(y), _vec(rstd_out, "rstd_out", rows), _launch_stream(stream)),
            "rmsnorm_forward")
 
@@ -628,14 +634,14 @@ def rmsnorm_forward_q8(x, gamma, q, scale, eps: float = 1e-6, residual=None, h_o
     pr, ldr = _mat(residual, "residual", x.shape, x.dtype)
     ph, ldh = _mat(h_out, "h_out", x.shape, x.dtype)
     pq, ldq = _mat(q, "q", x.shape, _Torch.i8)
-    _check(_lib.rmsnorm_forward_q8(px, ldx, pr, ldr, code, _vec(gamma, "gamma", D), rows, D, eps, ph, ldh,
+    _check(_lib.rmsnorm_forward_q8(px, ldx, pr, ldr, code, _vec(gamma, "gamma", D), rows, _n32(D), eps, ph, ldh,
                                    pq, ldq, _vec(scale, "scale", rows), _vec(rstd_out, "rstd_out", rows),
                                    _launch_stream(stream)),
            "rmsnorm_forward_q8")
 
 
 def rmsnorm_backward_workspace_bytes(rows: int, D: int) -> int:
-    return int(_lib.rmsnorm_backward_workspace_bytes(rows, D))
+    return int(_lib.rmsnorm_backward_workspace_bytes(rows, _n32(D)))
 
 
 def rmsnorm_backward(dy, h, rstd, gamma, dx, dgamma=None, workspace=None, dh=None, stream=None) -> None:
@@ -647,13 +653,13 @@ def rmsnorm_backward(dy, h, rstd, gamma, dx, dgamma=None, workspace=None, dh=Non
     pd, ldd = _mat(dh, "dh", h.shape, h.dtype)
     po, ldo = _mat(dx, "dx", h.shape, h.dtype)
     _check(_lib.rmsnorm_backward(py, ldy, _code(dy), ph, ldh, code, _vec(rstd, "rstd", rows),
-                                 _vec(gamma, "gamma", D), pd, ldd, rows, D, po, ldo, _vec(dgamma, "dgamma", D),
+                                 _vec(gamma, "gamma", D), pd, ldd, rows, _n32(D), po, ldo, _vec(dgamma, "dgamma", D),
                                  _ptr(workspace), _bytes(workspace), _launch_stream(stream)),
            "rmsnorm_backward")
 
 
 def q8_matmul_workspace_bytes(M: int, N: int, K: int) -> int:
-    return int(_lib.q8_matmul_workspace_bytes(M, N, K))
+    return int(_lib.q8_matmul_workspace_bytes(M, N, _n32(K)))
 
 
 def q8_matmul(a, a_scale, w, w_scale, out, workspace, stream=None) -> None:
@@ -666,7 +672,7 @@ def q8_matmul(a, a_scale, w, w_scale, out, workspace, stream=None) -> None:
         raise ValueError(f"w: shape {tuple(w.shape)}, need [N, {K}]")
     N = w.shape[0]
     po, ldo = _mat(out, "out", (M, N))
-    _check(_lib.q8_matmul(pa, lda, _vec(a_scale, "a_scale", M), pw, ldw, _vec(w_scale, "w_scale", N), M, N, K, po, ldo,
+    _check(_lib.q8_matmul(pa, lda, _vec(a_scale, "a_scale", M), pw, ldw, _vec(w_scale, "w_scale", N), M, N, _n32(K), po, ldo,
                           code, _ptr(workspace), _bytes(workspace), _launch_stream(stream)),
            "q8_matmul")
 
@@ -681,8 +687,8 @@ def _distill_args(logits, index, teacher, temperature):
     if index.shape[0] != T:
         raise ValueError(f"index: shape {tuple(index.shape)}, need [{T}, k]")
     pt, ldt = _mat(teacher, "teacher", index.shape)
-    return T, (pz, ldz, code, pi, ldi, 8 * index.element_size(), pt, ldt, _code(teacher), T, V, k,
-               temperature)
+    return T, (pz, ldz, code, pi, ldi, 8 * index.element_size(), pt, ldt, _code(teacher), T, _n32(V),
+               _n32(k), temperature)
 
 
 def distill_topk_forward(logits, index, teacher, loss, lse=None, temperature: float = 1.0, stream=None) -> None:
