@@ -692,16 +692,18 @@ def _distill_args(logits, index, teacher, temperature):
 
 
 def distill_topk_forward(logits, index, teacher, loss, lse=None, temperature: float = 1.0, stream=None) -> None:
-    """loss[t] = temperature^2 * KL(p || q): p the softmax of the teacher's entries teacher [T, k] at index [T, k]
-    (an index outside the vocabulary is no entry), q that of logits [T, V], both at the temperature; loss and lse
-    are float32 [T]."""
+    """loss[t] = temperature^2 * sum_j p_j (ln p_j - ln q[index_j]): p the softmax of the teacher's entries teacher [T, k]
+    at index [T, k] (an index outside the vocabulary is no entry), q that of logits [T, V], both at the temperature;
+    loss and lse are float32 [T].  KL(p || q) where no index is repeated; entries of one index count one by one, which
+    shifts the loss by a constant of the teacher's."""
     T, args = _distill_args(logits, index, teacher, temperature)
     _check(_lib.distill_topk_forward(*args, _vec(loss, "loss", T), _vec(lse, "lse", T), _launch_stream(stream)),
            "distill_topk_forward")
 
 
 def distill_topk_backward(logits, index, teacher, lse, dloss, dlogits, temperature: float = 1.0, stream=None) -> None:
-    """Gradient of distill_topk_forward's loss (dloss float32 [T], or None for 1) into dlogits (may be logits)."""
+    """Gradient of distill_topk_forward's loss (dloss float32 [T], or None for 1) into dlogits (may be logits).  An fp32
+    lse of logits far from 0 is off by |lse|·2^-24, and the gradient with it; distill_topk_forward_backward needs none."""
     T, args = _distill_args(logits, index, teacher, temperature)
     pd, ldd = _mat(dlogits, "dlogits", logits.shape, logits.dtype)
     _check(_lib.distill_topk_backward(*args, _vec(lse, "lse", T), _vec(dloss, "dloss", T), pd, ldd,

@@ -20,9 +20,9 @@
 // 2049 x 32003 46 us, 0.86; loss alone 129 x 50257 fp32 7.4 us.  What bounds it
 // is the time a token's dependent steps take (loads, two sums over the CTA,
 // loads from L2) with four tokens in hand per SM: more of them miss L2, and rows
-// kept in shared memory instead (two per SM) took 373 us.  Rows need not start on 16-byte boundaries
-// (an odd vocabulary): a row is its 16-byte vectors and up to 2·(VEC − 1)
-// elements at its ends.
+// kept in shared memory instead (two per SM) took 373 us.  Rows need not start
+// on 16-byte boundaries (an odd vocabulary): a row is its 16-byte vectors and up
+// to 2·(VEC − 1) elements at its ends.
 #include <cstdint>
 
 #include "rows.cuh"
@@ -40,7 +40,7 @@ constexpr float kLog2eLow = 1.9259629911e-8f;   // log2(e) − kLog2e
 constexpr int64_t kRowsInL2 = 90ll << 20;   // of the rows in hand, so that the second pass finds them there
 constexpr float kSlack = 100.0f;      // what lies 2^100 below the token's reference is nothing beside it
 constexpr float kHuge = 3.4028235e38f;   // the largest finite number
-constexpr float kNear = 4096.0f;      // of m·c: beyond this its spacing is felt beside ln V and ln|dloss|, and exponents are (z − m)·c
+constexpr float kNear = 4096.0f;      // of m·c: beyond, its spacing is felt beside ln V and ln|dloss|: (z − m)·c then
 
 struct DistillParams {
     const void* z;
@@ -519,8 +519,8 @@ int distill(const void* z, int64_t ldz, int32_t dtype, const void* index, int64_
            (T * cluster < 2ll * d.sm_count || (fwd && bwd && 4ll * d.sm_count / cluster * V * es > kRowsInL2)))
         cluster *= 2;
     if (T * cluster > INT32_MAX) return DDP_ERR_UNSUPPORTED;
-    const DistillParams p{z, index, teacher, lse_in, dloss, loss, lse, dz, ldz, ldi, ldt, lddz, T, V, k, tau, c, fminf(0.999f * kNear / c, kHuge),
-                          t_dtype == DDP_BF16, index_bits == 64, cluster};
+    const DistillParams p{z, index, teacher, lse_in, dloss, loss, lse, dz, ldz, ldi, ldt, lddz, T, V, k, tau, c,
+                          fminf(0.999f * kNear / c, kHuge), t_dtype == DDP_BF16, index_bits == 64, cluster};
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(T * cluster));
     cfg.blockDim = dim3(kDistillThreads);

@@ -4,8 +4,10 @@
 // Up to kFewTokens tokens: the channels are streamed once and multiplied into
 // exact 32-bit integers, with dp4a (few_kernel) or, from 3 tokens on, the
 // warp-wide 8-bit tensor instruction (few_mma_kernel).  Bound by HBM (1 token,
-// 8192 x 4096: 33.6 MB in 6.2 us; 16384 x 8192: 22 us, 0.90 of the copy rate)
-// or that instruction's low rate (8 tokens, 8192 x 4096: 10.2 us).
+// 8192 x 4096: 33.6 MB in 6.4 us; 16384 x 8192: 22 us, 0.91 of the copy rate;
+// of 50257 x 768 8.2 us, 0.71: its 1571 groups of channels are 2.07 rounds of
+// the 760 CTAs that are resident, so a third one is nearly empty), or by loads and that instruction taking turns (8
+// tokens, 8192 x 4096: 9.9 us, where bytes need 5.0 and the instruction 6.0).
 //
 // More tokens: GB300's tensor cores run 8-bit integers far below their 16-bit
 // rate, and an 8-bit integer is exact in fp16, as is a product of two in
@@ -28,8 +30,8 @@
 //                    from TMEM, B from shared memory, fp32 accumulator in TMEM
 //     epilogue       two warpgroups: TMEM -> scales -> out, 64 columns at a
 //                    time; the accumulator is free before the last are stored
-// 8192 x 16384 x 4096: 553 us in bursts, 609 held (the clock falls): 2.0 and
-// 1.8 PFLOP/s, 1.05 and 0.95 of the 16-bit rate measured with cuBLAS.  What
+// 8192 x 16384 x 4096: 545-564 us in bursts, 609-615 held (the clock falls): 2.0
+// and 1.8 PFLOP/s, 1.05 and 0.94 of the 16-bit rate measured with cuBLAS.  What
 // that took, each by its measurement: 64-token-deep tiles of one CTA 870 us,
 // held by L2 -> SM traffic (65 bytes per clock and SM); the pair halves what
 // tokens cost; arrivals across the pair without release (1438 -> 1063); one
@@ -38,11 +40,13 @@
 // one (-> 620); the issuing warp converged, descriptors in uniform registers:
 // 130 -> 45 clocks to issue an MMA (-> 562).
 // Few tiles split K (the parts are fp32 in the workspace, combine_kernel adds
-// them in their order).  37 x 8192 x 4096: 14.8 us, bound by the steps of the
+// them in their order).  37 x 8192 x 4096: 16.0 us, bound by the steps of the
 // pipeline itself: launches and TMEM 6 us, then a stage at about 850 clocks of
 // barriers (12.6 us of 16.3 were left without loads, conversions and MMAs, with
-// one block of K a stage; narrow tiles take two).
-// Every wait is bounded; a tile whose wait ran out is written as NaN.
+// one block of K a stage; narrow tiles take two).  1.2 us of it are the wait of
+// all threads for the tokens' grid, without which channels and scales could be
+// read before an earlier call's writes are visible.
+// Every wait on a barrier is bounded; a tile whose wait ran out is written as NaN.
 #include <cstdint>
 
 #include <cuda.h>
@@ -825,7 +829,7 @@ int encode(CUtensorMap* map, CUtensorMapDataType type, const void* base, int64_t
 
 // dp4a for up to kDotTokens.  Lanes per row, rows at a time and vectors in flight by K (us): 50257 x 768 at 8.3 with
 // (16, 2, 3), 13.2 with (32, 1, 8); 8192 x 4096 at 8.0 and 6.2.  From 3 tokens on the 8-bit tensor instruction is ahead:
-// 8 tokens of 8192 x 4096 17.7 by dp4a, 10.3; of 50257 x 768 19.3, 12.0 (1 token there 11.7).
+// 8 tokens of 8192 x 4096 17.7 by dp4a, 9.9; of 50257 x 768 19.3, 12.0 (1 token there 11.7).
 constexpr int kDotTokens = 2;
 struct DotPlan {
     void (*kernel)(FewParams);

@@ -613,7 +613,10 @@ int dist_sampler_indices_from(int64_t n_items, int32_t n_replicas, int32_t rank,
  *   y             device [rows, D], out_dtype; may be x or residual itself
  *                 when the dtypes match, not h_out
  *   rstd_out      device float[rows] or NULL (the backward pass reads it)
- * Sums are fp32.  rows == 0 enqueues nothing.  D <= 2^31 - 65536 here and
+ * Sums are fp32, of squares too: a row whose sum of squares passes 3.4e38
+ * (values beyond about 1.8e19/sqrt(D)) has rstd 0 and y 0, and the squares of
+ * values below about 1e-19 vanish (beside any eps that is not about as small,
+ * they do not matter).  rows == 0 enqueues nothing.  D <= 2^31 - 65536 here and
  * below (DDP_ERR_UNSUPPORTED beyond).
  */
 int rmsnorm_forward(const void* x, int64_t ldx, const void* residual, int64_t ldr, int32_t in_dtype,
@@ -671,7 +674,13 @@ size_t q8_matmul_workspace_bytes(int64_t M, int64_t N, int32_t K);
  * K <= 131071, M and N <= 2^31 - 65536 (DDP_ERR_UNSUPPORTED beyond).  K == 0
  * gives zeros (0*a_scale*w_scale).  Sums are 32-bit integers (up to 8 tokens)
  * or fp32, exact there while partial sums stay within 2^24: always for
- * K <= 1024; past that a partial sum is rounded to fp32.
+ * K <= 1024; past that a partial sum is rounded to fp32, so that a token's
+ * result can differ in its last bits with the number of tokens beside it.
+ * The workspace is that of the sizes alone: with more than 8 tokens it has
+ * room for a copy of all channels, used where their rows do not lie on 16
+ * bytes.  The tiles' waits on their own copies and products are bounded (about
+ * a second of GPU clocks): a tile whose wait ran out is written as NaN, and the
+ * call, which has returned by then, reports nothing.
  */
 int q8_matmul(const int8_t* a, int64_t lda, const float* a_scale, const int8_t* w, int64_t ldw,
               const float* w_scale, int64_t M, int64_t N, int32_t K, void* out, int64_t ldo, int32_t out_dtype,
