@@ -30,8 +30,8 @@
 //                    from TMEM, B from shared memory, fp32 accumulator in TMEM
 //     epilogue       two warpgroups: TMEM -> scales -> out, 64 columns at a
 //                    time; the accumulator is free before the last are stored
-// 8192 x 16384 x 4096: 545-564 us in bursts, 609-615 held (the clock falls): 2.0
-// and 1.8 PFLOP/s, 1.05 and 0.94 of the 16-bit rate measured with cuBLAS.  What
+// 8192 x 16384 x 4096: 545-564 us in bursts, 609-622 held (the clock falls): 2.0
+// and 1.8 PFLOP/s, 1.05 and 0.93 of the 16-bit rate measured with cuBLAS.  What
 // that took, each by its measurement: 64-token-deep tiles of one CTA 870 us,
 // held by L2 -> SM traffic (65 bytes per clock and SM); the pair halves what
 // tokens cost; arrivals across the pair without release (1438 -> 1063); one
