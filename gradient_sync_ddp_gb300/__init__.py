@@ -724,3 +724,53 @@ def distill_topk_forward_backward(logits, index, teacher, dloss, loss, lse, dlog
 __all__ += ["rmsnorm_forward", "rmsnorm_forward_q8", "rmsnorm_backward_workspace_bytes", "rmsnorm_backward",
             "q8_matmul_workspace_bytes", "q8_matmul", "distill_topk_forward", "distill_topk_backward",
             "distill_topk_forward_backward", "DISTILL_MAX_TOP"]
+
+
+# ---------------------------------------------------------------- operators of a transformer's training step
+
+_lib.layernorm_forward.argtypes = [_P, _i64, _P, _i64, _i32, _P, _P, _i64, _i32, _f32, _P, _i64, _P, _i64, _i32, _P, _P,
+                                   _P]
+_lib.layernorm_forward.restype = _c.c_int
+_lib.layernorm_backward_workspace_bytes.argtypes = [_i64, _i32]
+_lib.layernorm_backward_workspace_bytes.restype = _c.c_size_t
+_lib.layernorm_backward.argtypes = [_P, _i64, _i32, _P, _i64, _i32, _P, _P, _P, _P, _i64, _i64, _i32, _P, _i64, _P, _P,
+                                    _P, _c.c_size_t, _P]
+_lib.layernorm_backward.restype = _c.c_int
+
+
+def layernorm_forward(x, gamma, beta, y, eps: float = 1e-5, residual=None, h_out=None, mean_out=None, rstd_out=None,
+                      stream=None) -> None:
+    """y = (h - mean) * rstd * gamma + beta with h = x + residual and the mean and 1/sqrt(variance + eps) of every row
+    of [rows, D] matrices (fp32 or bf16, row strides as they are); h_out receives the sum, mean_out and rstd_out
+    (float32 [rows]) the statistics."""
+    code, (rows, D) = _code(x), x.shape
+    px, ldx = _mat(x, "x")
+    pr, ldr = _mat(residual, "residual", x.shape, x.dtype)
+    ph, ldh = _mat(h_out, "h_out", x.shape, x.dtype)
+    py, ldy = _mat(y, "y", x.shape)
+    _check(_lib.layernorm_forward(px, ldx, pr, ldr, code, _vec(gamma, "gamma", D), _vec(beta, "beta", D), rows, _n32(D),
+                                  eps, ph, ldh, py, ldy, _code(y), _vec(mean_out, "mean_out", rows),
+                                  _vec(rstd_out, "rstd_out", rows), _launch_stream(stream)),
+           "layernorm_forward")
+
+
+def layernorm_backward_workspace_bytes(rows: int, D: int) -> int:
+    return int(_lib.layernorm_backward_workspace_bytes(rows, _n32(D)))
+
+
+def layernorm_backward(dy, h, mean, rstd, gamma, dx, dgamma=None, dbeta=None, workspace=None, dh=None,
+                       stream=None) -> None:
+    """Gradient of layernorm_forward: dx (of x and of residual alike; dh is what reaches h by other ways), dgamma and
+    dbeta (float32 [D]; they need a workspace of layernorm_backward_workspace_bytes(rows, D) bytes)."""
+    code, (rows, D) = _code(h), h.shape
+    ph, ldh = _mat(h, "h")
+    py, ldy = _mat(dy, "dy", h.shape)
+    pd, ldd = _mat(dh, "dh", h.shape, h.dtype)
+    po, ldo = _mat(dx, "dx", h.shape, h.dtype)
+    _check(_lib.layernorm_backward(py, ldy, _code(dy), ph, ldh, code, _vec(mean, "mean", rows), _vec(rstd, "rstd", rows),
+                                   _vec(gamma, "gamma", D), pd, ldd, rows, _n32(D), po, ldo, _vec(dgamma, "dgamma", D),
+                                   _vec(dbeta, "dbeta", D), _ptr(workspace), _bytes(workspace), _launch_stream(stream)),
+           "layernorm_backward")
+
+
+__all__ += ["layernorm_forward", "layernorm_backward_workspace_bytes", "layernorm_backward"]

@@ -25,21 +25,18 @@
 // to 2·(VEC − 1) elements at its ends.
 #include <cstdint>
 
-#include "rows.cuh"
+#include "vocab.cuh"
 
 namespace ddp {
 namespace {
 
-constexpr int kDistillThreads = 256;
+constexpr int kDistillThreads = kVocabThreads;
 constexpr int kMaxTop = DDP_DISTILL_MAX_TOP;
 constexpr int kTopPerThread = kMaxTop / kDistillThreads;
-constexpr int kMaxCluster = 8;
 constexpr int kHash = 2 * kMaxTop;
 constexpr int kScanTop = 32;          // up to this many entries repeats are found by scanning all pairs
-constexpr float kLog2eLow = 1.9259629911e-8f;   // log2(e) − kLog2e
 constexpr int64_t kRowsInL2 = 90ll << 20;   // of the rows in hand, so that the second pass finds them there
 constexpr float kSlack = 100.0f;      // what lies 2^100 below the token's reference is nothing beside it
-constexpr float kHuge = 3.4028235e38f;   // the largest finite number
 constexpr float kNear = 4096.0f;      // of m·c: beyond, its spacing is felt beside ln V and ln|dloss|: (z − m)·c then
 
 struct DistillParams {
@@ -57,35 +54,6 @@ struct DistillParams {
     int32_t t_bf16, i_64, cluster;
 };
 
-// 2^x; results under 2^-126 are 0.
-__device__ __forceinline__ float pow2(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-
-__device__ __forceinline__ uint64_t pow2_pair(uint64_t x) {
-    float lo, hi;
-    unpair(x, lo, hi);
-    return pair(pow2(lo), pow2(hi));
-}
-// The e-th pair of a vector's values.
-template <bool BF16>
-__device__ __forceinline__ uint64_t vec_pair(const uint4& v, int e) {
-    return pair(vec_elem<BF16>(v, 2 * e), vec_elem<BF16>(v, 2 * e + 1));
-}
-
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ float cluster_read(const float* p, uint32_t rank) {
-    uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(p)), r;
-    float v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(r) : "memory");
-    return v;
-}
-
 // Largest m of z, kept finite, and Σ 2^((z − m)·c): of differences, for m·c itself may round by more than any exponent.
 struct Running {
     float m = -kHuge, s = 0.0f;
@@ -97,69 +65,6 @@ struct Running {
         }
     }
 };
-
-// The slice [v0, v1) of a row, v1 > v0: `lead` elements before its first
-// 16-byte boundary, `nvec` whole vectors, `tail` elements after them.
-struct Slice {
-    const char* base;   // of the row
-    int v0, lead, nvec, tail;
-};
-template <bool BF16>
-__device__ __forceinline__ Slice make_slice(const char* row, int v0, int v1) {
-    constexpr int ES = BF16 ? 2 : 4, VEC = 16 / ES;
-    const uintptr_t a = reinterpret_cast<uintptr_t>(row) + static_cast<uintptr_t>(v0) * ES;
-    Slice s;
-    s.base = row;
-    s.v0 = v0;
-    s.lead = min(static_cast<int>(((16 - (a & 15)) & 15) / ES), v1 - v0);
-    s.nvec = (v1 - v0 - s.lead) / VEC;
-    s.tail = v1 - v0 - s.lead - s.nvec * VEC;
-    return s;
-}
-// Index of the slice's e-th element outside its vectors (e < lead + tail).
-template <bool BF16>
-__device__ __forceinline__ int edge(const Slice& s, int e) {
-    return s.v0 + (e < s.lead ? e : e + s.nvec * (BF16 ? 8 : 4));
-}
-
-// body(vector index, values) for every 16-byte vector of the slice that is this thread's, U loads in flight.
-template <bool BF16, bool KEEP, class F>
-__device__ __forceinline__ void each_vector(const Slice& s, F body) {
-    constexpr int U = 6;
-    const char* zv = s.base + static_cast<int64_t>(s.v0 + s.lead) * (BF16 ? 2 : 4);
-    int i = threadIdx.x;
-    for (; i + (U - 1) * kDistillThreads < s.nvec; i += U * kDistillThreads) {
-        uint4 v[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const char* p = zv + static_cast<int64_t>(i + u * kDistillThreads) * 16;
-            v[u] = KEEP ? ld16_keep(p) : ld16<false>(p);
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) body(i + u * kDistillThreads, v[u]);
-    }
-    uint4 v[U - 1];
-#pragma unroll
-    for (int u = 0; u < U - 1; ++u) {
-        const char* p = zv + static_cast<int64_t>(i + u * kDistillThreads) * 16;
-        if (i + u * kDistillThreads < s.nvec) v[u] = KEEP ? ld16_keep(p) : ld16<false>(p);
-    }
-#pragma unroll
-    for (int u = 0; u < U - 1; ++u)
-        if (i + u * kDistillThreads < s.nvec) body(i + u * kDistillThreads, v[u]);
-}
-
-// A vector of dz to an address that is not on 16 bytes.
-template <bool BF16>
-__device__ __forceinline__ void store_vec_anywhere(char* d, const uint4& w) {
-#pragma unroll
-    for (int e = 0; e < (BF16 ? 8 : 4); ++e) {
-        const int q = BF16 ? e / 2 : e;
-        const uint32_t x = q == 0 ? w.x : q == 1 ? w.y : q == 2 ? w.z : w.w;
-        if constexpr (BF16) reinterpret_cast<unsigned short*>(d)[e] = static_cast<unsigned short>(x >> (16 * (e & 1)));
-        else reinterpret_cast<uint32_t*>(d)[e] = x;
-    }
-}
 
 // A probability's exponent: a kept lse of far logits, rounded by more than ln V, would allow any number.
 __device__ __forceinline__ float at_most_one(float x) { return x > 0.0f ? 0.0f : x; }   // NaN stays
@@ -201,33 +106,6 @@ __device__ __forceinline__ void write_grad(const Slice& s, char* dz, float c, fl
         const float o = f(xe);
         store_elem<BF16>(dz, ve, BF16 && g < 0.0f ? -o : o);
     }
-}
-
-template <bool BF16>
-__device__ __forceinline__ void write_zero(const Slice& s, char* dz) {
-    constexpr int ES = BF16 ? 2 : 4, VEC = 16 / ES;
-    char* dv = dz + static_cast<int64_t>(s.v0 + s.lead) * ES;
-    const bool whole = (reinterpret_cast<uintptr_t>(dv) & 15) == 0;
-    for (int i = threadIdx.x; i < s.nvec; i += kDistillThreads) {
-        if (whole) {
-            st16(dv + static_cast<int64_t>(i) * 16, make_uint4(0, 0, 0, 0));
-        } else {
-            for (int e = 0; e < VEC; ++e) store_elem<BF16>(dv, static_cast<int64_t>(i) * VEC + e, 0.0f);
-        }
-    }
-    if (threadIdx.x < s.lead + s.tail) store_elem<BF16>(dz, edge<BF16>(s, threadIdx.x), 0.0f);
-}
-
-// Two values over the CTA, in every thread, with one barrier: `sh` is not used again before another.
-template <class OpA, class OpB>
-__device__ __forceinline__ void once_all2(float& a, float& b, float2* sh) {
-    a = warp_all<OpA>(a);
-    b = warp_all<OpB>(b);
-    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = make_float2(a, b);
-    __syncthreads();
-    const float2 v = (threadIdx.x & 31) < kDistillThreads / 32 ? sh[threadIdx.x & 31] : make_float2(OpA::id(), OpB::id());
-    a = warp_all<OpA>(v.x);
-    b = warp_all<OpB>(v.y);
 }
 
 template <bool BF16, bool FWD, bool BWD>
@@ -472,9 +350,6 @@ __global__ void __launch_bounds__(kDistillThreads, 4) distill_kernel(const __gri
         if (a.cluster > 1) cluster_sync();               // no CTA ends while another reads its part
     }
 }
-
-bool dtype_ok(int32_t t) { return t == DDP_F32 || t == DDP_BF16; }
-int dsize(int32_t t) { return t == DDP_BF16 ? 2 : 4; }
 
 template <bool BF16>
 void (*pick(bool fwd, bool bwd))(DistillParams) {

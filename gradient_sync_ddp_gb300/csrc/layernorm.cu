@@ -1,0 +1,640 @@
+// Layer norm with the residual's addition, forward and backward.
+//
+//   h = x + residual,  mean = mean(h),  rstd = 1/sqrt(mean((h − mean)²) + eps),
+//   y = (h − mean)·rstd·γ + β
+//   backward: n = (h − mean)·rstd, c1 = mean(dy·γ), c2 = mean(dy·γ·n),
+//             dx = rstd·(dy·γ − c1 − n·c2) + dh,  dγ = Σ_rows dy·n,  dβ = Σ_rows dy
+//
+// Sums and statistics are fp32; h is rounded to its type only where it is
+// stored, the statistics and y use the unrounded sum.  The variance is taken
+// about the mean in a second pass over the row's registers: a row far from 0
+// (mean² >> variance) loses nothing that its own rounding had not lost.
+//
+// Bound by HBM: forward reads x and residual and writes h and y once, backward
+// reads dy, h and dh and writes dx once.  Rows are held as the RMS norm's are:
+// a warp per row (narrow ones) or a CTA per row, 16-byte vectors, all loads of
+// a row in flight at once; rows off the 16-byte boundaries that lie alike take
+// the vectors of the aligned grid and one element per thread at their ends;
+// matrices that lie differently, and rows wider than the registers hold, go by
+// elements.
+// dγ and dβ: every thread owns the same columns of all its rows; a CTA's part
+// goes to the workspace and a second kernel adds the parts in their order.
+#include <cstdint>
+
+#include "norm_rows.cuh"
+
+namespace ddp {
+namespace {
+
+constexpr int kNormThreads = 256;
+
+struct LayerNormParams {
+    const void* x;
+    const void* res;
+    const float* gamma;
+    const float* beta;
+    void* h;
+    void* y;
+    float* mean;
+    float* rstd;
+    int64_t ldx, ldr, ldh, ldy, rows;
+    int32_t D;
+    float eps;
+};
+
+// Sum over the CTA in every thread with one barrier: `sh` is not written again before every thread has passed another.
+__device__ __forceinline__ float sum_once(float v, float* sh) {
+    v = warp_all<SumOp>(v);
+    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
+    __syncthreads();
+    const int nw = (blockDim.x + 31) >> 5;
+    return warp_all<SumOp>((threadIdx.x & 31) < nw ? sh[threadIdx.x & 31] : 0.0f);
+}
+__device__ __forceinline__ void sum_once2(float& a, float& b, float2* sh) {
+    a = warp_all<SumOp>(a);
+    b = warp_all<SumOp>(b);
+    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = make_float2(a, b);
+    __syncthreads();
+    const int nw = (blockDim.x + 31) >> 5;
+    const float2 v = (threadIdx.x & 31) < nw ? sh[threadIdx.x & 31] : make_float2(0.0f, 0.0f);
+    a = warp_all<SumOp>(v.x);
+    b = warp_all<SumOp>(v.y);
+}
+
+// A CTA per row (grid-stride), three passes over the row; every element is
+// read and written by the same thread, so y and h may lie on x or residual.
+template <bool BF16, bool YBF16>
+__global__ void __launch_bounds__(kNormThreads) ln_loop_kernel(const __grid_constant__ LayerNormParams a) {
+    __shared__ float sh[32];
+    pdl_enter();
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        const void* x = row_ptr<BF16>(a.x, row, a.ldx);
+        const void* r = a.res ? row_ptr<BF16>(a.res, row, a.ldr) : nullptr;
+        auto value = [&](int d) { return load_elem<BF16>(x, d) + (r ? load_elem<BF16>(r, d) : 0.0f); };
+        float s = 0.0f, ss = 0.0f;
+        for (int d = threadIdx.x; d < a.D; d += kNormThreads) s += value(d);
+        const float mean = block_all<SumOp>(s, sh) / a.D;
+        for (int d = threadIdx.x; d < a.D; d += kNormThreads) {
+            const float c = value(d) - mean;
+            ss = fmaf(c, c, ss);
+        }
+        const float rstd = 1.0f / sqrtf(block_all<SumOp>(ss, sh) / a.D + a.eps);
+        if (threadIdx.x == 0) {
+            if (a.mean) a.mean[row] = mean;
+            if (a.rstd) a.rstd[row] = rstd;
+        }
+        for (int d = threadIdx.x; d < a.D; d += kNormThreads) {
+            const float h = value(d), n = (h - mean) * rstd;
+            if (a.h) store_elem<BF16>(row_ptr<BF16>(a.h, row, a.ldh), d, h);
+            store_elem<YBF16>(row_ptr<YBF16>(a.y, row, a.ldy), d, fmaf(n, a.gamma ? a.gamma[d] : 1.0f, a.beta ? a.beta[d] : 0.0f));
+        }
+    }
+}
+
+// VPT vectors per thread.  WARP: a warp per row, kWarpRows per CTA; else a CTA per row.
+template <bool BF16, bool YBF16, int VPT, bool EDGE, bool WARP>
+__global__ void __launch_bounds__(WARP ? 32 * kWarpRows : max_group(BF16, VPT))
+    ln_kernel(const __grid_constant__ LayerNormParams a) {
+    constexpr int ES = BF16 ? 2 : 4, VEC = 16 / ES, YS = YBF16 ? 2 : 4;
+    __shared__ float sh[2][32];
+    pdl_enter();
+    const int G = WARP ? 32 : blockDim.x;
+    const int t = WARP ? threadIdx.x & 31 : threadIdx.x;
+    const int64_t row = WARP ? static_cast<int64_t>(blockIdx.x) * kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
+    if (row >= a.rows) return;       // whole warps
+    const char* x = row_ptr<BF16>(a.x, row, a.ldx);
+    const char* r = a.res ? row_ptr<BF16>(a.res, row, a.ldr) : nullptr;
+    const RowShape s = row_shape<BF16, EDGE>(x, a.D);
+    float h[VPT][VEC], he = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int v = t + i * G;
+        if (v < s.nvec) load_n<BF16, VEC>(x + (s.lead + v * VEC) * ES, h[i]);
+        else
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) h[i][e] = 0.0f;
+    }
+    if (r != nullptr) {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int v = t + i * G;
+            if (v >= s.nvec) break;
+            float rr[VEC];
+            load_n<BF16, VEC>(r + (s.lead + v * VEC) * ES, rr);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) h[i][e] += rr[e];
+        }
+    }
+    // the last warp has the fewest vectors: it takes the row's ends
+    const int te = G - 1 - t;
+    const bool has_edge = EDGE && te < s.edges;
+    const int de = EDGE ? edge_elem<VEC>(s, te) : 0;
+    if (has_edge) he = load_elem<BF16>(x, de) + (r ? load_elem<BF16>(r, de) : 0.0f);
+    float sum = he;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) sum += h[i][e];
+    if (a.h != nullptr) {
+        char* ho = row_ptr<BF16>(a.h, row, a.ldh);
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int v = t + i * G;
+            if (v < s.nvec) store_n<BF16, VEC>(ho + (s.lead + v * VEC) * ES, h[i]);
+        }
+        if (has_edge) store_elem<BF16>(ho, de, he);
+    }
+    const float mean = (WARP ? warp_all<SumOp>(sum) : sum_once(sum, sh[0])) / a.D;
+    he -= mean;
+    float ss = has_edge ? he * he : 0.0f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        if (t + i * G >= s.nvec) break;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            h[i][e] -= mean;
+            ss = fmaf(h[i][e], h[i][e], ss);
+        }
+    }
+    const float rstd = 1.0f / sqrtf((WARP ? warp_all<SumOp>(ss) : sum_once(ss, sh[1])) / a.D + a.eps);
+    if (t == 0) {
+        if (a.mean) a.mean[row] = mean;
+        if (a.rstd) a.rstd[row] = rstd;
+    }
+    char* y = row_ptr<YBF16>(a.y, row, a.ldy);
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int v = t + i * G;
+        if (v >= s.nvec) break;
+        float g[VEC], b[VEC];
+        load_cols<EDGE, VEC>(a.gamma, 1.0f, a.D, s.lead + v * VEC, g);
+        load_cols<EDGE, VEC>(a.beta, 0.0f, a.D, s.lead + v * VEC, b);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) h[i][e] = fmaf(h[i][e] * rstd, g[e], b[e]);
+        store_n<YBF16, VEC>(y + (s.lead + v * VEC) * YS, h[i]);
+    }
+    if (has_edge) store_elem<YBF16>(y, de, fmaf(he * rstd, a.gamma ? a.gamma[de] : 1.0f, a.beta ? a.beta[de] : 0.0f));
+}
+
+struct LayerNormGradParams {
+    const void* dy;
+    const void* h;
+    const float* mean;
+    const float* rstd;
+    const float* gamma;
+    const void* dh;
+    void* dx;
+    float* partial;   // [gridDim.x][2][D]: dγ, dβ; or NULL
+    int64_t lddy, ldh, lddh, lddx, rows;
+    int32_t D;
+};
+
+// A CTA per row (grid-stride); each thread owns the same columns of every
+// row, so its CTA's part of dγ and dβ needs no atomics: it is kept in the workspace.
+template <bool BF16, bool DYBF16>
+__global__ void __launch_bounds__(kNormThreads) ln_grad_loop_kernel(const __grid_constant__ LayerNormGradParams a) {
+    __shared__ float2 sh[32];
+    pdl_enter();
+    float* pg = a.partial ? a.partial + static_cast<int64_t>(blockIdx.x) * 2 * a.D : nullptr;
+    float* pb = a.partial ? pg + a.D : nullptr;
+    bool first = true;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, first = false) {
+        const void* dy = row_ptr<DYBF16>(a.dy, row, a.lddy);
+        const void* hp = row_ptr<BF16>(a.h, row, a.ldh);
+        const void* dh = a.dh ? row_ptr<BF16>(a.dh, row, a.lddh) : nullptr;
+        void* dx = row_ptr<BF16>(a.dx, row, a.lddx);
+        const float rstd = a.rstd[row], mean = a.mean[row];
+        float c1 = 0.0f, c2 = 0.0f;
+        for (int d = threadIdx.x; d < a.D; d += kNormThreads) {
+            const float g = load_elem<DYBF16>(dy, d) * (a.gamma ? a.gamma[d] : 1.0f), n = (load_elem<BF16>(hp, d) - mean) * rstd;
+            c1 += g;
+            c2 = fmaf(g, n, c2);
+        }
+        block_all2<SumOp, SumOp>(c1, c2, sh);
+        c1 /= a.D;
+        c2 /= a.D;
+        for (int d = threadIdx.x; d < a.D; d += kNormThreads) {
+            const float g = load_elem<DYBF16>(dy, d), n = (load_elem<BF16>(hp, d) - mean) * rstd;
+            float v = rstd * ((a.gamma ? g * a.gamma[d] : g) - c1 - n * c2);
+            if (dh) v += load_elem<BF16>(dh, d);
+            store_elem<BF16>(dx, d, v);
+            if (pg) {
+                pg[d] = first ? g * n : fmaf(g, n, pg[d]);
+                pb[d] = first ? g : g + pb[d];
+            }
+        }
+    }
+}
+
+// Rows per CTA of the warp-per-row kernel: one CTA per SM, so that dγ and dβ have few parts.
+constexpr int kGradRows = 16;
+// Threads of a CTA per row: four vectors of dγ and dβ need more registers than 1024 threads have.
+constexpr int max_grad_group(bool bf16, int vpt) { return vpt == 4 ? 512 : max_group(bf16, vpt); }
+
+// A row's dy, h and dh are all on their way before the first is used, and stay
+// packed in registers; a thread's columns are the same for every row, so its
+// part of dγ and dβ is in registers too.  AHEAD: the next row is fetched before
+// this one is reduced.  EDGE: rows off the 16-byte boundaries that lie alike;
+// the grid is a multiple of VEC, so a thread's columns still do not change from
+// row to row.
+template <bool BF16, bool DYBF16, int VPT, bool WARP, bool AHEAD, bool EDGE>
+__global__ void __launch_bounds__(WARP ? 32 * kGradRows : AHEAD ? 512 : max_grad_group(BF16, VPT))
+    ln_grad_kernel(const __grid_constant__ LayerNormGradParams a) {
+    constexpr int ES = BF16 ? 2 : 4, VEC = 16 / ES, YS = DYBF16 ? 2 : 4;
+    extern __shared__ float part_sh[];   // WARP and a.partial: [kGradRows][D]
+    __shared__ float2 sh[2][32];
+    pdl_enter();
+    const int G = WARP ? 32 : blockDim.x;
+    const int t = WARP ? threadIdx.x & 31 : threadIdx.x;
+    const int w = WARP ? threadIdx.x >> 5 : 0;
+    const bool want = a.partial != nullptr;
+    const int64_t row0 = static_cast<int64_t>(blockIdx.x) * (WARP ? kGradRows : 1) + w;
+    const RowShape s = row_shape<BF16, EDGE>(row_ptr<BF16>(a.h, row0, a.ldh), a.D);
+    const int te = G - 1 - t, de = EDGE ? edge_elem<VEC>(s, te) : 0;
+    const bool has_edge = EDGE && te < s.edges;
+    const float gme = has_edge && a.gamma ? __ldg(a.gamma + de) : 1.0f;
+    float ag[VPT][VEC] = {}, ab[VPT][VEC] = {}, age = 0.0f, abe = 0.0f;
+    float ge = 0.0f, he = 0.0f, re = 0.0f, ge2 = 0.0f, he2 = 0.0f, re2 = 0.0f;
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * (WARP ? kGradRows : 1);
+    Packed<DYBF16, VEC> g[VPT], g2[AHEAD ? VPT : 1];
+    Packed<BF16, VEC> h[VPT], r[VPT], h2[AHEAD ? VPT : 1], r2[AHEAD ? VPT : 1];
+    float rstd = 0.0f, rstd2 = 0.0f, mean = 0.0f, mean2 = 0.0f;
+    auto fetch = [&](int64_t row, Packed<DYBF16, VEC>* gg, Packed<BF16, VEC>* hh, Packed<BF16, VEC>* rr, float& rs, float& mn, float& eg, float& eh, float& er) {
+        const char* dy = row_ptr<DYBF16>(a.dy, row, a.lddy);
+        const char* hp = row_ptr<BF16>(a.h, row, a.ldh);
+        const char* dh = a.dh ? row_ptr<BF16>(a.dh, row, a.lddh) : nullptr;
+        rs = a.rstd[row];
+        mn = a.mean[row];
+        if (has_edge) {
+            eg = load_elem<DYBF16>(dy, de);
+            eh = load_elem<BF16>(hp, de);
+            if (dh) er = load_elem<BF16>(dh, de);
+        }
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int v = t + i * G;
+            if (v < s.nvec) {
+                gg[i].load(dy + (s.lead + v * VEC) * YS);
+                hh[i].load(hp + (s.lead + v * VEC) * ES);
+                if (dh) rr[i].load(dh + (s.lead + v * VEC) * ES);
+                else rr[i].zero();
+            }
+        }
+    };
+    int64_t row = row0;
+    int turn = 0;
+    if (AHEAD && row < a.rows) fetch(row, g, h, r, rstd, mean, ge, he, re);
+    for (; row < a.rows; row += stride) {
+        if constexpr (AHEAD) {
+            if (row + stride < a.rows) fetch(row + stride, g2, h2, r2, rstd2, mean2, ge2, he2, re2);
+        } else {
+            fetch(row, g, h, r, rstd, mean, ge, he, re);
+        }
+        float c1 = 0.0f, c2 = 0.0f;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int v = t + i * G;
+            if (v >= s.nvec) break;
+            float gm[VEC];
+            load_cols<EDGE, VEC>(a.gamma, 1.0f, a.D, s.lead + v * VEC, gm);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                const float gy = g[i].at(e), n = (h[i].at(e) - mean) * rstd, dn = gy * gm[e];
+                ag[i][e] = fmaf(gy, n, ag[i][e]);
+                ab[i][e] += gy;
+                c1 += dn;
+                c2 = fmaf(dn, n, c2);
+            }
+        }
+        if constexpr (EDGE) {
+            if (has_edge) {
+                const float n = (he - mean) * rstd, dn = ge * gme;
+                age = fmaf(ge, n, age);
+                abe += ge;
+                c1 += dn;
+                c2 = fmaf(dn, n, c2);
+            }
+        }
+        if constexpr (WARP) {
+            c1 = warp_all<SumOp>(c1);
+            c2 = warp_all<SumOp>(c2);
+        } else {
+            sum_once2(c1, c2, sh[turn]);
+            turn ^= 1;
+        }
+        c1 /= a.D;
+        c2 /= a.D;
+        char* dx = row_ptr<BF16>(a.dx, row, a.lddx);
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int v = t + i * G;
+            if (v >= s.nvec) break;
+            float gm[VEC], o[VEC];
+            load_cols<EDGE, VEC>(a.gamma, 1.0f, a.D, s.lead + v * VEC, gm);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+                o[e] = fmaf(rstd, fmaf(g[i].at(e), gm[e], -c1) - (h[i].at(e) - mean) * rstd * c2, r[i].at(e));
+            store_n<BF16, VEC>(dx + (s.lead + v * VEC) * ES, o);
+        }
+        if (has_edge) store_elem<BF16>(dx, de, fmaf(rstd, fmaf(ge, gme, -c1) - (he - mean) * rstd * c2, re));
+        if constexpr (AHEAD) {
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                g[i] = g2[i];
+                h[i] = h2[i];
+                r[i] = r2[i];
+            }
+            rstd = rstd2;
+            mean = mean2;
+            ge = ge2;
+            he = he2;
+            re = re2;
+        }
+    }
+    if (!want) return;
+    float* out = a.partial + static_cast<int64_t>(blockIdx.x) * 2 * a.D;
+    // dγ, then dβ: the warps' parts share one place in shared memory
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        float* to = WARP ? part_sh + w * a.D : out + k * a.D;
+        if (WARP && k == 1) __syncthreads();
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int v = t + i * G;
+            if (v >= s.nvec) break;
+            float* d = to + s.lead + v * VEC;
+            const float(&acc)[VEC] = k == 0 ? ag[i] : ab[i];
+            if constexpr (EDGE) {
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) d[e] = acc[e];
+            } else {
+#pragma unroll
+                for (int q = 0; q < VEC / 4; ++q)
+                    reinterpret_cast<float4*>(d)[q] = make_float4(acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]);
+            }
+        }
+        if (has_edge) to[de] = k == 0 ? age : abe;
+        if constexpr (WARP) {
+            __syncthreads();
+            for (int d = threadIdx.x; d < a.D; d += 32 * kGradRows) {
+                float v = part_sh[d];
+#pragma unroll
+                for (int i = 1; i < kGradRows; ++i) v += part_sh[i * a.D + d];
+                out[k * a.D + d] = v;
+            }
+        }
+    }
+}
+
+// Backward, rows that lie anywhere: an element at a time, each thread the
+// same EPT columns of every row (γ and its part of dγ and dβ in registers), G threads.
+template <bool BF16, bool DYBF16, int G, int EPT>
+__global__ void __launch_bounds__(G, G * EPT <= 512 ? 1024 / G : G <= 512 && EPT <= 4 ? 2 : 1)
+    ln_grad_elem_kernel(const __grid_constant__ LayerNormGradParams a) {
+    constexpr int ES = BF16 ? 2 : 4, YS = DYBF16 ? 2 : 4;
+    __shared__ float2 sh[2][32];
+    pdl_enter();
+    const int t = threadIdx.x;
+    float ag[EPT] = {}, ab[EPT] = {}, gm[EPT];
+    int turn = 0;
+#pragma unroll
+    for (int i = 0; i < EPT; ++i) gm[i] = t + i * G < a.D && a.gamma ? __ldg(a.gamma + t + i * G) : 1.0f;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        const char* dy = row_ptr<DYBF16>(a.dy, row, a.lddy) + t * YS;
+        const char* hp = row_ptr<BF16>(a.h, row, a.ldh) + t * ES;
+        const char* dh = row_ptr<BF16>(a.dh, row, a.lddh) + t * ES;
+        float g[EPT], n[EPT], r[EPT];
+        const float rstd = a.rstd[row], mean = a.mean[row];
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) {
+            const bool in = t + i * G < a.D;
+            g[i] = in ? load_elem<DYBF16>(dy + i * G * YS, 0) : 0.0f;
+            n[i] = in ? load_elem<BF16>(hp + i * G * ES, 0) : mean;
+            r[i] = in && a.dh ? load_elem<BF16>(dh + i * G * ES, 0) : 0.0f;
+        }
+        float c1 = 0.0f, c2 = 0.0f;
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) {
+            if (t + i * G >= a.D) break;
+            n[i] = (n[i] - mean) * rstd;
+            ag[i] = fmaf(g[i], n[i], ag[i]);
+            ab[i] += g[i];
+            g[i] *= gm[i];
+            c1 += g[i];
+            c2 = fmaf(g[i], n[i], c2);
+        }
+        sum_once2(c1, c2, sh[turn]);
+        turn ^= 1;
+        c1 /= a.D;
+        c2 /= a.D;
+        char* dx = row_ptr<BF16>(a.dx, row, a.lddx) + t * ES;
+#pragma unroll
+        for (int i = 0; i < EPT; ++i)
+            if (t + i * G < a.D) store_elem<BF16>(dx + i * G * ES, 0, fmaf(rstd, g[i] - c1 - n[i] * c2, r[i]));
+    }
+    if (a.partial == nullptr) return;
+    float* out = a.partial + static_cast<int64_t>(blockIdx.x) * 2 * a.D;
+#pragma unroll
+    for (int i = 0; i < EPT; ++i) {
+        if (t + i * G >= a.D) break;
+        out[t + i * G] = ag[i];
+        out[a.D + t + i * G] = ab[i];
+    }
+}
+
+struct ColumnParams {
+    const float* partial;   // [n][2][D]
+    float* out[2];          // dγ, dβ; either may be NULL
+    int32_t n, D;
+};
+
+// out[d] = Σ over the CTAs' parts, in a fixed order: 16 columns per CTA, 64
+// threads per column over interleaved parts, then those 64 by halves.
+__global__ void __launch_bounds__(1024) ln_columns_kernel(const __grid_constant__ ColumnParams a) {
+    __shared__ float sh[64][17];
+    pdl_enter();
+    const int c = threadIdx.x & 15, w = threadIdx.x >> 4;
+    const int d = blockIdx.x * 16 + c;
+    float* out = a.out[blockIdx.y];
+    if (out == nullptr) return;
+    const float* part = a.partial + static_cast<int64_t>(blockIdx.y) * a.D;
+    float s = 0.0f;
+    if (d < a.D) {
+#pragma unroll 10
+        for (int i = w; i < a.n; i += 64) s += part[static_cast<int64_t>(i) * 2 * a.D + d];
+    }
+    sh[w][c] = s;
+    __syncthreads();
+    if (threadIdx.x >= 512) return;
+    const int col = threadIdx.x >> 5, l = threadIdx.x & 31;      // a warp per column
+    s = warp_all<SumOp>(sh[l][col] + sh[l + 32][col]);
+    if (l == 0 && blockIdx.x * 16 + col < a.D) out[blockIdx.x * 16 + col] = s;
+}
+
+// ---- host ----------------------------------------------------------------
+
+template <bool BF16, bool YBF16, bool EDGE>
+void (*fwd_kernel(const Group& g))(LayerNormParams) {
+    if (g.warp) return g.vpt == 1 ? ln_kernel<BF16, YBF16, 1, EDGE, true> : g.vpt == 2 ? ln_kernel<BF16, YBF16, 2, EDGE, true> : g.vpt == 3 ? ln_kernel<BF16, YBF16, 3, EDGE, true> : ln_kernel<BF16, YBF16, 4, EDGE, true>;
+    return g.vpt == 1 ? ln_kernel<BF16, YBF16, 1, EDGE, false> : g.vpt == 2 ? ln_kernel<BF16, YBF16, 2, EDGE, false> : ln_kernel<BF16, YBF16, 4, EDGE, false>;
+}
+template <bool BF16, bool YBF16>
+void (*fwd_kernel(Lay lay, const Group& g))(LayerNormParams) {
+    if (lay == Lay::kDifferent || g.threads == 0) return ln_loop_kernel<BF16, YBF16>;
+    return lay == Lay::kAligned ? fwd_kernel<BF16, YBF16, false>(g) : fwd_kernel<BF16, YBF16, true>(g);
+}
+template <bool BF16, bool DYBF16, bool EDGE>
+void (*bwd_vec(const Group& g))(LayerNormGradParams) {
+    if (g.warp) return g.vpt == 1 ? ln_grad_kernel<BF16, DYBF16, 1, true, false, EDGE> : g.vpt == 2 ? ln_grad_kernel<BF16, DYBF16, 2, true, false, EDGE> : g.vpt == 3 ? ln_grad_kernel<BF16, DYBF16, 3, true, false, EDGE> : ln_grad_kernel<BF16, DYBF16, 4, true, false, EDGE>;
+    if (g.threads <= 512 && g.vpt <= 2) return g.vpt == 1 ? ln_grad_kernel<BF16, DYBF16, 1, false, !EDGE, EDGE> : ln_grad_kernel<BF16, DYBF16, 2, false, !EDGE, EDGE>;
+    return g.vpt == 1 ? ln_grad_kernel<BF16, DYBF16, 1, false, false, EDGE> : g.vpt == 2 ? ln_grad_kernel<BF16, DYBF16, 2, false, false, EDGE> : ln_grad_kernel<BF16, DYBF16, 4, false, false, EDGE>;
+}
+
+// Element kernels by width: threads, kernel.
+template <bool BF16, bool DYBF16>
+int bwd_elem(int D, void (**k)(LayerNormGradParams)) {
+    if (D <= 128) return *k = ln_grad_elem_kernel<BF16, DYBF16, 128, 1>, 128;
+    if (D <= 512) return *k = ln_grad_elem_kernel<BF16, DYBF16, 128, 4>, 128;
+    if (D <= 1024) return *k = ln_grad_elem_kernel<BF16, DYBF16, 256, 4>, 256;
+    if (D <= 2048) return *k = ln_grad_elem_kernel<BF16, DYBF16, 512, 4>, 512;
+    if (D <= 4096) return *k = ln_grad_elem_kernel<BF16, DYBF16, 512, 8>, 512;
+    if (D <= 8192) return *k = ln_grad_elem_kernel<BF16, DYBF16, 1024, 8>, 1024;
+    return *k = ln_grad_loop_kernel<BF16, DYBF16>, kNormThreads;
+}
+
+// How layernorm_backward runs: kernel, threads, CTAs, shared memory.
+struct GradPlan {
+    void (*kernel)(LayerNormGradParams);
+    int threads, ctas;
+    size_t smem;
+};
+template <bool BF16, bool DYBF16>
+int grad_plan(Lay lay, int64_t rows, int D, bool want, int sms, GradPlan* p) {
+    const Group g = pick_group(rows, D, BF16, sms);
+    int64_t rows_per_cta = 1;
+    p->smem = 0;
+    const bool vec = lay != Lay::kDifferent && g.threads != 0 && (g.warp || g.threads <= max_grad_group(BF16, g.vpt));
+    if (vec) {
+        p->kernel = lay == Lay::kAligned ? bwd_vec<BF16, DYBF16, false>(g) : bwd_vec<BF16, DYBF16, true>(g);
+        p->threads = g.warp ? 32 * kGradRows : g.threads;
+        rows_per_cta = g.warp ? kGradRows : 1;
+        p->smem = g.warp && want ? static_cast<size_t>(kGradRows) * D * 4 : 0;
+    } else {
+        p->threads = bwd_elem<BF16, DYBF16>(D, &p->kernel);
+    }
+    // one wave, and few enough parts of dγ and dβ
+    const int64_t ctas = (rows + rows_per_cta - 1) / rows_per_cta;
+    const int st = one_wave_grid(reinterpret_cast<const void*>(p->kernel), p->threads, ctas, &p->ctas);
+    if (p->ctas > kGradCtas) p->ctas = kGradCtas;
+    if (vec && lay == Lay::kAlike) p->ctas = alike_grid(p->ctas, ctas);
+    return st;
+}
+
+}  // namespace
+}  // namespace ddp
+
+using namespace ddp;
+
+extern "C" int layernorm_forward(const void* x, int64_t ldx, const void* residual, int64_t ldr, int32_t in_dtype,
+                                 const float* gamma, const float* beta, int64_t rows, int32_t D, float eps,
+                                 void* h_out, int64_t ldh, void* y, int64_t ldy, int32_t out_dtype, float* mean_out,
+                                 float* rstd_out, void* stream) {
+    if (!dtype_ok(in_dtype) || !dtype_ok(out_dtype) || rows < 0 || D < 1 || !(eps >= 0.0f) || !(eps < 3.0e38f))
+        return DDP_ERR_INVALID_ARG;
+    if (D > kMaxWidth) return DDP_ERR_UNSUPPORTED;
+    const int es = dsize(in_dtype);
+    const Mat mx{x, rows, D, ldx, es}, mr{residual, rows, D, ldr, es}, mh{h_out, rows, D, ldh, es},
+        my{y, rows, D, ldy, dsize(out_dtype)}, mg{gamma, 1, D, D, 4}, mb{beta, 1, D, D, 4},
+        mm{mean_out, 1, rows, rows, 4}, mt{rstd_out, 1, rows, rows, 4};
+    if (!mat_valid(mx) || !mat_valid(my) || (residual && !mat_valid(mr)) || (h_out && !mat_valid(mh)))
+        return DDP_ERR_INVALID_ARG;
+    if (rows > 0 && (x == nullptr || y == nullptr)) return DDP_ERR_INVALID_ARG;
+    for (const Mat* m : {&mx, &mr, &mh, &my, &mg, &mb, &mm, &mt})
+        if (!mat_aligned(*m)) return DDP_ERR_ALIGNMENT;
+    for (const Mat* o : {&my, &mh}) {
+        for (const Mat* i : {&mx, &mr})
+            if (!mats_same(*o, *i) && mats_overlap(*o, *i)) return DDP_ERR_INVALID_ARG;
+        for (const Mat* i : {&mg, &mb, &mm, &mt})
+            if (mats_overlap(*o, *i)) return DDP_ERR_INVALID_ARG;
+    }
+    if (mats_overlap(my, mh) || mats_overlap(mm, mt)) return DDP_ERR_INVALID_ARG;
+    for (const Mat* o : {&mm, &mt})
+        for (const Mat* i : {&mx, &mr, &mg, &mb})
+            if (mats_overlap(*o, *i)) return DDP_ERR_INVALID_ARG;
+    if (rows == 0) return DDP_OK;
+    const LayerNormParams p{x, residual, gamma, beta, h_out, y, mean_out, rstd_out, ldx, ldr, ldh, ldy, rows, D, eps};
+    DeviceInfo d;
+    const int st = current_device_info(&d);
+    if (st != DDP_OK) return st;
+    const bool b = in_dtype == DDP_BF16, c = out_dtype == DDP_BF16;
+    const Mat* const mats[4] = {&mx, &mr, &mh, &my};
+    Lay lay = layout(mats, 4, D, b ? 8 : 4, gamma);
+    if (lay == Lay::kAligned && !aligned16(beta)) lay = Lay::kAlike;
+    const Group g = pick_group(rows, D, b, d.sm_count);
+    void (*kernel)(LayerNormParams) = b ? (c ? fwd_kernel<true, true>(lay, g) : fwd_kernel<true, false>(lay, g))
+                                        : (c ? fwd_kernel<false, true>(lay, g) : fwd_kernel<false, false>(lay, g));
+    const bool loop = lay == Lay::kDifferent || g.threads == 0;
+    const int64_t ctas = loop ? (rows < (1 << 16) ? rows : 1 << 16) : g.warp ? (rows + kWarpRows - 1) / kWarpRows : rows;
+    if (ctas > INT32_MAX) return DDP_ERR_UNSUPPORTED;
+    return launch_pdl(kernel, dim3(static_cast<unsigned>(ctas)), loop ? kNormThreads : g.warp ? 32 * kWarpRows : g.threads,
+                      static_cast<cudaStream_t>(stream), p);
+}
+
+extern "C" size_t layernorm_backward_workspace_bytes(int64_t rows, int32_t D) {
+    return rows < 0 || D < 1 || D > kMaxWidth ? 0 : static_cast<size_t>(grad_parts(rows)) * static_cast<size_t>(D) * 8;
+}
+
+extern "C" int layernorm_backward(const void* dy, int64_t lddy, int32_t dy_dtype, const void* h, int64_t ldh,
+                                  int32_t h_dtype, const float* mean, const float* rstd, const float* gamma,
+                                  const void* dh, int64_t lddh, int64_t rows, int32_t D, void* dx, int64_t lddx,
+                                  float* dgamma, float* dbeta, void* workspace, size_t workspace_bytes, void* stream) {
+    if (!dtype_ok(dy_dtype) || !dtype_ok(h_dtype) || rows < 0 || D < 1) return DDP_ERR_INVALID_ARG;
+    if (D > kMaxWidth) return DDP_ERR_UNSUPPORTED;
+    const int es = dsize(h_dtype);
+    const bool want = dgamma != nullptr || dbeta != nullptr;
+    const size_t need = want ? layernorm_backward_workspace_bytes(rows, D) : 0;
+    const Mat my{dy, rows, D, lddy, dsize(dy_dtype)}, mh{h, rows, D, ldh, es}, md{dh, rows, D, lddh, es},
+        mo{dx, rows, D, lddx, es}, mm{mean, 1, rows, rows, 4}, mr{rstd, 1, rows, rows, 4}, mg{gamma, 1, D, D, 4},
+        mw{dgamma, 1, D, D, 4}, mb{dbeta, 1, D, D, 4},
+        ws{want ? workspace : nullptr, 1, static_cast<int64_t>(need / 4), static_cast<int64_t>(need / 4), 4};
+    if (!mat_valid(my) || !mat_valid(mh) || !mat_valid(mo) || (dh && !mat_valid(md))) return DDP_ERR_INVALID_ARG;
+    if (rows > 0 && (dy == nullptr || h == nullptr || mean == nullptr || rstd == nullptr || dx == nullptr))
+        return DDP_ERR_INVALID_ARG;
+    if (want && workspace == nullptr) return DDP_ERR_INVALID_ARG;
+    for (const Mat* m : {&my, &mh, &md, &mo, &mm, &mr, &mg, &mw, &mb})
+        if (!mat_aligned(*m)) return DDP_ERR_ALIGNMENT;
+    if (!aligned16(ws.p)) return DDP_ERR_ALIGNMENT;
+    if (want && workspace_bytes < need) return DDP_ERR_CAPACITY;
+    for (const Mat* i : {&my, &mh, &md})
+        if (!mats_same(mo, *i) && mats_overlap(mo, *i)) return DDP_ERR_INVALID_ARG;
+    for (const Mat* o : {&mo, &mw, &mb, &ws})
+        for (const Mat* i : {&mm, &mr, &mg})
+            if (mats_overlap(*o, *i)) return DDP_ERR_INVALID_ARG;
+    for (const Mat* o : {&mw, &mb, &ws})
+        for (const Mat* i : {&my, &mh, &md, &mo})
+            if (mats_overlap(*o, *i)) return DDP_ERR_INVALID_ARG;
+    if (mats_overlap(mw, ws) || mats_overlap(mb, ws) || mats_overlap(mw, mb)) return DDP_ERR_INVALID_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    int parts = 0;
+    if (rows > 0) {
+        const LayerNormGradParams p{dy, h, mean, rstd, gamma, dh, dx, want ? static_cast<float*>(workspace) : nullptr,
+                                    lddy, ldh, lddh, lddx, rows, D};
+        DeviceInfo d;
+        int st = current_device_info(&d);
+        if (st != DDP_OK) return st;
+        const bool b = h_dtype == DDP_BF16, c = dy_dtype == DDP_BF16;
+        const Mat* const mats[4] = {&mh, &my, &md, &mo};
+        const Lay lay = layout(mats, 4, D, b ? 8 : 4, gamma);
+        GradPlan g;
+        st = b ? (c ? grad_plan<true, true>(lay, rows, D, want, d.sm_count, &g) : grad_plan<true, false>(lay, rows, D, want, d.sm_count, &g))
+               : (c ? grad_plan<false, true>(lay, rows, D, want, d.sm_count, &g) : grad_plan<false, false>(lay, rows, D, want, d.sm_count, &g));
+        if (st != DDP_OK) return st;
+        parts = g.ctas;
+        if ((st = launch_smem(g.kernel, static_cast<unsigned>(g.ctas), g.threads, g.smem, s, p)) != DDP_OK) return st;
+    }
+    if (want) {
+        const ColumnParams q{static_cast<const float*>(workspace), {dgamma, dbeta}, parts, D};
+        return launch_pdl(ln_columns_kernel, dim3(static_cast<unsigned>((D + 15) / 16), 2), 1024, s, q);
+    }
+    return DDP_OK;
+}

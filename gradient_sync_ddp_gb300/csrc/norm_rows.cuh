@@ -1,0 +1,174 @@
+// Shared by the row norms (RMS norm, layer norm): what a thread holds of a row
+// of a strided matrix, column vectors (gamma, beta), and the host's choice of a
+// kernel by how the rows lie and how wide they are.
+#pragma once
+
+#include <cstdint>
+
+#include "row_grid.h"
+#include "rows.cuh"
+
+namespace ddp {
+
+// What one thread holds of a row: vectors threadIdx-strided, one element at the row's ends.
+struct RowShape {
+    int lead, nvec, edges;
+};
+template <bool BF16, bool EDGE>
+__device__ __forceinline__ RowShape row_shape(const char* p, int D) {
+    constexpr int ES = BF16 ? 2 : 4, VEC = 16 / ES;
+    RowShape s{0, D / VEC, 0};
+    if constexpr (EDGE) {
+        s.lead = min(static_cast<int>((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / ES, D);
+        s.nvec = (D - s.lead) / VEC;
+        s.edges = D - s.nvec * VEC;
+    }
+    return s;
+}
+template <int VEC>
+__device__ __forceinline__ int edge_elem(const RowShape& s, int e) {
+    return e < s.lead ? e : e + s.nvec * VEC;
+}
+
+// N consecutive values of a matrix, N·size a power of two up to 32 bytes and p aligned to it (or to 16).
+template <bool BF16, int N>
+__device__ __forceinline__ void load_n(const char* p, float (&o)[N]) {
+    if constexpr (!BF16) {
+#pragma unroll
+        for (int q = 0; q < N / 4; ++q) {
+            const uint4 v = ld16<false>(p + 16 * q);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[4 * q + e] = vec_elem<false>(v, e);
+        }
+    } else if constexpr (N == 8) {
+        const uint4 v = ld16<false>(p);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = vec_elem<true>(v, e);
+    } else {
+        uint2 v;
+        asm volatile("ld.global.cs.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p) : "memory");
+        o[0] = bf16_lo(v.x);
+        o[1] = bf16_hi(v.x);
+        o[2] = bf16_lo(v.y);
+        o[3] = bf16_hi(v.y);
+    }
+}
+template <bool BF16, int N>
+__device__ __forceinline__ void store_n(char* p, const float (&o)[N]) {
+    if constexpr (!BF16) {
+#pragma unroll
+        for (int q = 0; q < N / 4; ++q) *reinterpret_cast<float4*>(p + 16 * q) = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+    } else if constexpr (N == 8) {
+        *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7]));
+    } else {
+        *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+    }
+}
+// VEC columns from d on of γ or β (`none` without one).  EDGE: d is any column, the same
+// modulo 4 for a row's vectors; the 16-byte pieces that cover them, shifted
+// (one 4-byte load per column instead cost 8 passes of 32 sectors per warp).
+template <bool EDGE, int VEC>
+__device__ __forceinline__ void load_cols(const float* cols, float none, int D, int d, float (&o)[VEC]) {
+    if (cols == nullptr) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) o[e] = none;
+        return;
+    }
+    const int s = EDGE ? (d + static_cast<int>(reinterpret_cast<uintptr_t>(cols) / 4)) & 3 : 0, b = d - s;
+    if (EDGE && (b < 0 || b + VEC + 4 > D)) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) o[e] = __ldg(cols + d + e);
+        return;
+    }
+    float f[VEC + 4];
+#pragma unroll
+    for (int q = 0; q < VEC / 4 + (EDGE ? 1 : 0); ++q) {
+        const float4 v = __ldg(reinterpret_cast<const float4*>(cols + b) + q);
+        f[4 * q] = v.x;
+        f[4 * q + 1] = v.y;
+        f[4 * q + 2] = v.z;
+        f[4 * q + 3] = v.w;
+    }
+    if constexpr (EDGE) {
+#pragma unroll
+        for (int e = 0; e < VEC + 3; ++e) f[e] = s & 1 ? f[e + 1] : f[e];
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) f[e] = s & 2 ? f[e + 2] : f[e];
+    }
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) o[e] = f[e];
+}
+
+constexpr int kWarpRows = 8;      // rows per CTA of the warp-per-row forward kernels
+constexpr int max_group(bool bf16, int vpt) { return vpt * (bf16 ? 8 : 4) > 16 ? 512 : 1024; }
+
+// N values of a matrix as they lie in memory.
+template <bool BF16, int N>
+struct Packed {
+    static constexpr int W = N * (BF16 ? 2 : 4) / 4;
+    uint32_t w[W];
+    __device__ __forceinline__ void load(const char* p) {
+        if constexpr (W == 2) {
+            asm volatile("ld.global.cs.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p) : "memory");
+        } else {
+#pragma unroll
+            for (int q = 0; q < W / 4; ++q) {
+                const uint4 v = ld16<false>(p + 16 * q);
+                w[4 * q] = v.x;
+                w[4 * q + 1] = v.y;
+                w[4 * q + 2] = v.z;
+                w[4 * q + 3] = v.w;
+            }
+        }
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < W; ++i) w[i] = 0;
+    }
+    __device__ __forceinline__ float at(int e) const {
+        if constexpr (BF16) return e & 1 ? bf16_hi(w[e >> 1]) : bf16_lo(w[e >> 1]);
+        else return __uint_as_float(w[e]);
+    }
+};
+
+// ---- host ----------------------------------------------------------------
+
+constexpr int kGradCtas = 608;   // at most this many parts of dγ
+
+inline int grad_parts(int64_t rows) { return static_cast<int>(rows < kGradCtas ? (rows < 1 ? 1 : rows) : kGradCtas); }
+
+// How the rows of a call's matrices lie on the grid of VEC elements (16 bytes of x's type).
+enum class Lay { kAligned, kAlike, kDifferent };
+inline Lay layout(const Mat* const* mats, int n, int D, int vec, const float* gamma) {
+    bool aligned = D % vec == 0 && aligned16(gamma), alike = true;
+    for (int i = 0; i < n; ++i) {
+        const Mat &m = *mats[i], &f = *mats[0];
+        if (m.p == nullptr) continue;
+        const uintptr_t e = reinterpret_cast<uintptr_t>(m.p) / m.esz, e0 = reinterpret_cast<uintptr_t>(f.p) / f.esz;
+        const bool one = m.rows <= 1;
+        alike &= e % vec == e0 % vec && (one || m.ld % vec == f.ld % vec);
+        aligned &= e % vec == 0 && (one || m.ld % vec == 0);
+    }
+    return aligned ? Lay::kAligned : alike ? Lay::kAlike : Lay::kDifferent;
+}
+
+// Vectors per thread and threads per row.  Many rows: a warp per row up to 128
+// vectors, then two vectors per thread; few rows (they do not fill the GPU):
+// as many threads as the row has vectors.  0 threads: the row does not fit.
+struct Group {
+    int vpt, threads;
+    bool warp;
+};
+inline Group pick_group(int64_t rows, int D, bool bf16, int sms) {
+    const int vec = bf16 ? 8 : 4, nv = (D + vec - 1) / vec;
+    if (nv <= 32) return {1, 32, true};
+    const bool few = rows < 2ll * sms;
+    if (!few && nv <= 128) return {(nv + 31) / 32, 32, true};
+    for (int vpt = few ? 1 : 2; vpt <= 4; vpt *= 2) {
+        const int t = ((nv + vpt - 1) / vpt + 31) / 32 * 32;
+        if (t <= max_group(bf16, vpt)) return {vpt, t, false};
+    }
+    return {0, 0, false};
+}
+
+}  // namespace ddp

@@ -115,6 +115,9 @@ __device__ __forceinline__ void block_all2(float& a, float& b, float2* sh) {
 
 // ---- host: a matrix argument of a call --------------------------------
 
+inline bool dtype_ok(int32_t t) { return t == DDP_F32 || t == DDP_BF16; }
+inline int dsize(int32_t t) { return t == DDP_BF16 ? 2 : 4; }
+
 // Columns of a row: their numbers, rounded up to what a CTA takes at a time, fit 32 bits.
 constexpr int64_t kMaxWidth = (1ll << 31) - 65536;
 

@@ -742,6 +742,67 @@ int distill_topk_forward_backward(const void* logits, int64_t ldz, int32_t dtype
                                   int64_t T, int32_t V, int32_t k, float temperature, const float* dloss,
                                   float* loss, float* lse, void* dlogits, int64_t lddz, void* stream);
 
+/*
+ * ---- Operators of a transformer's training step -------------------------
+ *
+ * What the replicas of a GPT-2-like model run around the average beside the
+ * operators above: layer norm forward and backward, the log probabilities of
+ * a batch's tokens with their gradient, and the optimizer step of its matrices
+ * (the pages name no such operators).  Matrices, alignment and summation orders
+ * as above.
+ */
+
+/*
+ * layernorm_forward — h = x + residual; mean = mean(h);
+ * rstd = 1/sqrt(mean((h - mean)^2) + eps); y = (h - mean)*rstd*gamma + beta,
+ * per row.
+ *   x, residual   device [rows, D], in_dtype; residual may be NULL (h = x)
+ *   gamma, beta   device float[D] or NULL (1, 0)
+ *   eps           >= 0; with eps 0 a row of equal values has y NaN
+ *   h_out         device [rows, D], in_dtype, or NULL: the sum, rounded to
+ *                 in_dtype (statistics and y use it unrounded); may be x or
+ *                 residual itself (same pointer and ld)
+ *   y             device [rows, D], out_dtype; may be x or residual itself
+ *                 when the dtypes match, not h_out
+ *   mean_out, rstd_out   device float[rows] each or NULL (the backward pass
+ *                 reads them)
+ * Sums are fp32, the variance is taken about the mean; a row whose sum, or
+ * whose sum of squared differences, passes 3.4e38 has statistics that are not
+ * finite, or rstd 0.  rows == 0 enqueues nothing.  D <= 2^31 - 65536
+ * (DDP_ERR_UNSUPPORTED beyond).
+ */
+int layernorm_forward(const void* x, int64_t ldx, const void* residual, int64_t ldr, int32_t in_dtype,
+                      const float* gamma, const float* beta, int64_t rows, int32_t D, float eps, void* h_out,
+                      int64_t ldh, void* y, int64_t ldy, int32_t out_dtype, float* mean_out, float* rstd_out,
+                      void* stream);
+
+/* Workspace of layernorm_backward (0 for invalid sizes). */
+size_t layernorm_backward_workspace_bytes(int64_t rows, int32_t D);
+
+/*
+ * layernorm_backward — the gradient of layernorm_forward.  With
+ * n = (h - mean)*rstd, c1 = mean(dy*gamma) and c2 = mean(dy*gamma*n):
+ *     dx = rstd*(dy*gamma - c1 - n*c2) + dh   (x and residual have this gradient)
+ *     dgamma = sum over the rows of dy*n,  dbeta = sum over the rows of dy
+ *   dy               device [rows, D], dy_dtype: the gradient of y
+ *   h, mean, rstd    what the forward pass wrote (h in h_dtype)
+ *   dh               device [rows, D], h_dtype, or NULL: the gradient that
+ *                    reaches h by other ways (the residual stream)
+ *   dx               device [rows, D], h_dtype; may be dy, h or dh itself
+ *                    when the dtypes match
+ *   dgamma, dbeta    device float[D] each, or NULL (not wanted); written, not
+ *                    added to
+ *   workspace        device buffer of layernorm_backward_workspace_bytes(rows,
+ *                    D), 16-byte aligned, contents ignored on entry (NULL
+ *                    without dgamma and dbeta); overlapping calls need
+ *                    different ones
+ * rows == 0 writes a dgamma and a dbeta of zeros.
+ */
+int layernorm_backward(const void* dy, int64_t lddy, int32_t dy_dtype, const void* h, int64_t ldh, int32_t h_dtype,
+                       const float* mean, const float* rstd, const float* gamma, const void* dh, int64_t lddh,
+                       int64_t rows, int32_t D, void* dx, int64_t lddx, float* dgamma, float* dbeta, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
 /* Human-readable name of a ddp_status value (static string). */
 const char* ddp_status_string(int status);
 

@@ -1,0 +1,109 @@
+"""Definitions in fp64 of the operators of a transformer's training step: layer
+norm with the residual's addition and its gradient, the log probabilities of
+given tokens (with entropy and the most probable entries) and their gradient,
+the Newton-Schulz steps on a matrix and the optimizer step that takes them.
+Test infrastructure: plain numpy, no code shared with the CUDA path.
+"""
+from __future__ import annotations
+
+import numpy as np
+
+
+def layernorm(x, residual, gamma, beta, eps):
+    """(h, mean, rstd, y): h = x + residual, y = (h − mean)·rstd·γ + β per row, rstd = 1/sqrt(var + eps)."""
+    h = np.asarray(x, np.float64)
+    if residual is not None:
+        h = h + np.asarray(residual, np.float64)
+    mean = np.mean(h, axis=1)
+    c = h - mean[:, None]
+    rstd = 1.0 / np.sqrt(np.mean(c * c, axis=1) + eps)
+    y = c * rstd[:, None]
+    if gamma is not None:
+        y = y * np.asarray(gamma, np.float64)
+    if beta is not None:
+        y = y + np.asarray(beta, np.float64)
+    return h, mean, rstd, y
+
+
+def layernorm_grad(dy, h, mean, rstd, gamma, dh):
+    """(dx, dγ, dβ) with n = (h − mean)·rstd: dx = rstd·(dy·γ − mean(dy·γ) − n·mean(dy·γ·n)) + dh."""
+    dy, rstd = np.asarray(dy, np.float64), np.asarray(rstd, np.float64)[:, None]
+    n = (np.asarray(h, np.float64) - np.asarray(mean, np.float64)[:, None]) * rstd
+    dn = dy if gamma is None else dy * np.asarray(gamma, np.float64)
+    dx = rstd * (dn - np.mean(dn, axis=1, keepdims=True) - n * np.mean(dn * n, axis=1, keepdims=True))
+    if dh is not None:
+        dx = dx + np.asarray(dh, np.float64)
+    return dx, np.sum(dy * n, axis=0), np.sum(dy, axis=0)
+
+
+def token_logprobs(logits, target, temperature, k=0):
+    """(logprob, entropy, lse, top_index, top_logprob) per token, one token at a time: p = softmax(z/τ); a target
+    outside the vocabulary has log probability 0; the k largest logits in descending order, the lower index first
+    among equals (0 and −0 are equal); entries beyond the vocabulary have index −1 and log probability −infinity.
+    A token whose logits are all −infinity has lse −infinity, entropy 0 and log probabilities −infinity."""
+    T, V = logits.shape
+    logp, entropy, lse = np.zeros(T), np.zeros(T), np.zeros(T)
+    ti, tl = np.full((T, k), -1, np.int64), np.full((T, k), -np.inf)
+    for t in range(T):
+        z = np.asarray(logits[t], np.float64) / temperature
+        m = np.max(z)
+        if m == -np.inf:
+            lse[t] = -np.inf
+            lp = np.full(V, -np.inf)
+        else:
+            lse[t] = m + np.log(np.sum(np.exp(z - m)))
+            lp = z - lse[t]
+            p = np.exp(lp)
+            entropy[t] = -np.sum(p[p > 0] * lp[p > 0])
+        y = int(target[t])
+        logp[t] = lp[y] if 0 <= y < V else 0.0
+        order = np.lexsort((np.arange(V), -np.asarray(logits[t], np.float64)))[:k]
+        ti[t, :len(order)], tl[t, :len(order)] = order, lp[order]
+    return logp, entropy, lse, ti, tl
+
+
+def token_logprobs_grad(logits, target, temperature, dlogprob, dentropy):
+    """dz_v = (dlogprob·([v = target] − p_v) − dentropy·p_v·(ln p_v + H)) / τ; a target outside the vocabulary takes
+    no dlogprob, a token whose logits are all −infinity has gradient 0."""
+    T, V = logits.shape
+    dz = np.zeros((T, V))
+    for t in range(T):
+        z = np.asarray(logits[t], np.float64) / temperature
+        if np.max(z) == -np.inf:
+            continue
+        lp = z - (np.max(z) + np.log(np.sum(np.exp(z - np.max(z)))))
+        p = np.exp(lp)
+        plogp = np.where(p > 0, p * np.where(p > 0, lp, 0.0), 0.0)
+        y = int(target[t])
+        if dlogprob is not None and 0 <= y < V:
+            dz[t] -= float(dlogprob[t]) * p
+            dz[t, y] += float(dlogprob[t])
+        if dentropy is not None:
+            dz[t] -= float(dentropy[t]) * (plogp - p * np.sum(plogp))
+    return dz / temperature
+
+
+NS = (3.4445, -4.7750, 2.0315)
+
+
+def newton_schulz(x, steps=5, eps=1e-7):
+    """X / (‖X‖ + eps), then `steps` times X ← aX + (bA + cA²)X with A = X·Xᵀ (of the shorter side: Xᵀ for a tall X)."""
+    a, b, c = NS
+    x = np.asarray(x, np.float64)
+    tall = x.shape[0] > x.shape[1]
+    x = x.T if tall else x
+    x = x / (np.sqrt(np.sum(x * x)) + eps)
+    for _ in range(steps):
+        g = x @ x.T
+        x = a * x + (b * g + c * (g @ g)) @ x
+    return x.T if tall else x
+
+
+def muon_step(grads, theta, buf, lr, momentum, weight_decay, scale, nesterov=True, steps=5, eps=1e-7):
+    """(theta, buf) after one step on a matrix: g = mean of the replicas, buf ← μ·buf + g, u = g + μ·buf (or buf),
+    θ ← θ·(1 − lr·wd) − lr·scale·NS(u)."""
+    g = np.mean([np.asarray(x, np.float64) for x in grads], axis=0)
+    buf = momentum * np.asarray(buf, np.float64) + g
+    u = g + momentum * buf if nesterov else buf
+    theta = np.asarray(theta, np.float64) * (1.0 - lr * weight_decay) - lr * scale * newton_schulz(u, steps, eps)
+    return theta, buf

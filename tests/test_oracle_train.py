@@ -1,0 +1,97 @@
+"""Pins of the fp64 definitions of the training step's operators: gradients
+against central differences, closed forms, and torch's own operators."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import train_oracle as O
+
+
+def _gen(seed):
+    return np.random.Generator(np.random.PCG64(seed))
+
+
+def test_layernorm_against_torch_and_differences():
+    gen = _gen(1)
+    x, r, g, b, w, v = (gen.standard_normal(s) for s in ((3, 7), (3, 7), 7, 7, (3, 7), (3, 7)))
+    h, mean, rstd, y = O.layernorm(x, r, g, b, 1e-3)
+    want = torch.nn.functional.layer_norm(torch.from_numpy(x + r), (7,), torch.from_numpy(g), torch.from_numpy(b), 1e-3)
+    assert np.allclose(y, want.numpy(), rtol=1e-12, atol=1e-13) and np.array_equal(h, x + r)
+    dx, dg, db = O.layernorm_grad(w, h, mean, rstd, g, v)
+
+    def f(x, g, b):                       # v reaches h by another way
+        h, _, _, y = O.layernorm(x, r, g, b, 1e-3)
+        return np.sum(w * y) + np.sum(v * h)
+    e = 1e-6
+    for k, got in enumerate((dx, dg, db)):
+        for i in np.ndindex(got.shape):
+            up, down = [x.copy(), g.copy(), b.copy()], [x.copy(), g.copy(), b.copy()]
+            up[k][i] += e
+            down[k][i] -= e
+            assert abs((f(*up) - f(*down)) / (2 * e) - got[i]) < 1e-8
+
+
+@pytest.mark.parametrize("tau", [1.0, 2.5])
+def test_token_logprobs_against_torch_and_differences(tau):
+    gen = _gen(2)
+    z = gen.standard_normal((4, 9)) * 2
+    z[1, 3] = z[1, 5] = z[1].max() + 1            # a tie: the lower index first
+    z[2, ::2] = -np.inf
+    target = np.array([2, 5, 1, -100])
+    logp, entropy, lse, ti, tl = O.token_logprobs(z, target, tau, 11)
+    want = torch.log_softmax(torch.from_numpy(z) / tau, 1)
+    assert np.allclose(logp[:3], want.numpy()[np.arange(3), target[:3]], rtol=1e-12) and logp[3] == 0
+    assert np.allclose(lse, torch.logsumexp(torch.from_numpy(z) / tau, 1).numpy(), rtol=1e-13)
+    assert np.allclose(entropy, torch.special.entr(want.exp()).sum(1).numpy(), rtol=1e-12)
+    assert ti[1, :2].tolist() == [3, 5] and np.all(ti[:, 9:] == -1) and np.all(tl[:, 9:] == -np.inf)
+    for t in range(4):
+        assert sorted(ti[t, :9]) == list(range(9)) and np.array_equal(tl[t, :9], want[t].numpy()[ti[t, :9]]) or \
+            np.allclose(tl[t, :9], want[t].numpy()[ti[t, :9]], rtol=1e-12)
+    assert ti[2, 4:9].tolist() == [0, 2, 4, 6, 8]
+    up, ue = gen.standard_normal(4), gen.standard_normal(4)
+    dz = O.token_logprobs_grad(z, target, tau, up, ue)
+
+    def f(z):
+        lp, en, _, _, _ = O.token_logprobs(z, target, tau)
+        return lp * up + en * ue
+    e = 1e-6
+    for i in np.ndindex(4, 9):
+        if z[i] == -np.inf:
+            assert dz[i] == 0
+            continue
+        d = np.zeros((4, 9))
+        d[i] = e
+        assert abs((f(z + d) - f(z - d))[i[0]] / (2 * e) - dz[i]) < 1e-7
+
+
+def test_token_logprobs_of_nothing():
+    z = np.full((1, 3), -np.inf)
+    logp, entropy, lse, ti, tl = O.token_logprobs(z, np.array([1]), 1.0, 2)
+    assert logp[0] == -np.inf == lse[0] and entropy[0] == 0 and ti[0].tolist() == [0, 1] and np.all(tl == -np.inf)
+    assert not O.token_logprobs_grad(z, np.array([1]), 1.0, np.ones(1), np.ones(1)).any()
+
+
+@pytest.mark.parametrize("shape", [(6, 6), (5, 12), (12, 5), (1, 7)])
+def test_newton_schulz_acts_on_singular_values(shape):
+    """U·diag(s)·Vᵀ becomes U·diag(p(p(...s/‖s‖)))·Vᵀ with p(s) = as + bs³ + cs⁵."""
+    gen = _gen(3)
+    x = gen.standard_normal(shape)
+    u, s, v = np.linalg.svd(x, full_matrices=False)
+    s = s / (np.linalg.norm(s) + 1e-7)
+    a, b, c = O.NS
+    for _ in range(5):
+        s = a * s + b * s ** 3 + c * s ** 5
+    assert np.allclose(O.newton_schulz(x), u @ np.diag(s) @ v, atol=1e-11)
+    assert not O.newton_schulz(np.zeros(shape)).any()
+
+
+def test_muon_step():
+    gen = _gen(4)
+    grads = [gen.standard_normal((3, 4)) for _ in range(2)]
+    theta, buf = gen.standard_normal((3, 4)), gen.standard_normal((3, 4))
+    g = (grads[0] + grads[1]) / 2
+    t, b = O.muon_step(grads, theta, buf, 0.1, 0.9, 0.01, 2.0)
+    assert np.allclose(b, 0.9 * buf + g)
+    assert np.allclose(t, theta * 0.999 - 0.2 * O.newton_schulz(g + 0.9 * b))
+    t, _ = O.muon_step(grads, theta, buf, 0.1, 0.9, 0.0, 2.0, nesterov=False)
+    assert np.allclose(t, theta - 0.2 * O.newton_schulz(b))
