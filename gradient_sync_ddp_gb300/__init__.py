@@ -774,3 +774,66 @@ def layernorm_backward(dy, h, mean, rstd, gamma, dx, dgamma=None, dbeta=None, wo
 
 
 __all__ += ["layernorm_forward", "layernorm_backward_workspace_bytes", "layernorm_backward"]
+
+
+LOGPROB_MAX_TOP = 128
+_lib.token_logprobs_forward.argtypes = [_P, _i64, _i32, _P, _i32, _i64, _i32, _f32, _P, _P, _P, _i32, _P, _i64, _i32, _P,
+                                        _i64, _P]
+_lib.token_logprobs_forward.restype = _c.c_int
+_lib.token_logprobs_backward.argtypes = [_P, _i64, _i32, _P, _i32, _i64, _i32, _f32, _P, _P, _P, _P, _P, _i64, _P]
+_lib.token_logprobs_backward.restype = _c.c_int
+
+
+def _ints(t, name: str, n: int):
+    """(address, bits) of a contiguous int32 or int64 vector of n elements; None -> (NULL, 64)."""
+    if t is None:
+        return None, 64
+    if t.dtype != _Torch.i64 and t.dtype != _Torch.i32:
+        raise TypeError(f"{name}: dtype {t.dtype}, need torch.int32 or torch.int64")
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name}: need {n} contiguous elements")
+    return t.data_ptr(), 8 * t.element_size()
+
+
+def token_logprobs_forward(logits, target, logprob, entropy=None, lse=None, top_index=None, top_logprob=None,
+                           temperature: float = 1.0, stream=None) -> None:
+    """Of every token's softmax(logits / temperature), logits [T, V]: the log probability of target (int32 or int64 [T];
+    one outside the vocabulary counts as 0), the entropy, the log-sum-exp (float32 [T] each; any may be None) and the k
+    most probable entries, the lower index first among equals: top_index (int32 or int64 [T, k]) with top_logprob
+    (float32 [T, k])."""
+    code, (T, V) = _code(logits), logits.shape
+    pz, ldz = _mat(logits, "logits")
+    py, bits = _ints(target, "target", T)
+    if logprob is not None and target is None:
+        raise ValueError("target: needed for logprob")
+    shape = top_index.shape if top_index is not None else top_logprob.shape if top_logprob is not None else (T, 0)
+    if len(shape) != 2 or shape[0] != T:
+        raise ValueError(f"top: shape {tuple(shape)}, need [{T}, k]")
+    if top_index is not None and top_index.dtype != _Torch.i64 and top_index.dtype != _Torch.i32:
+        raise TypeError(f"top_index: dtype {top_index.dtype}, need torch.int32 or torch.int64")
+    pi, ldi = _mat(top_index, "top_index", shape)
+    pl, ldl = _mat(top_logprob, "top_logprob", shape, _Torch.f32)
+    _check(_lib.token_logprobs_forward(pz, ldz, code, py, bits, T, _n32(V), temperature, _vec(logprob, "logprob", T),
+                                       _vec(entropy, "entropy", T), _vec(lse, "lse", T), _n32(shape[1]), pi, ldi,
+                                       64 if top_index is None else 8 * top_index.element_size(), pl, ldl,
+                                       _launch_stream(stream)),
+           "token_logprobs_forward")
+
+
+def token_logprobs_backward(logits, target, lse, dlogprob, dlogits, entropy=None, dentropy=None,
+                            temperature: float = 1.0, stream=None) -> None:
+    """Gradient of token_logprobs_forward's logprob and entropy into dlogits (may be logits): dlogprob and dentropy are
+    float32 [T] or None (no gradient comes that way), lse and entropy what the forward pass wrote."""
+    code, (T, V) = _code(logits), logits.shape
+    pz, ldz = _mat(logits, "logits")
+    py, bits = _ints(target, "target", T)
+    if dlogprob is not None and target is None:
+        raise ValueError("target: needed for dlogprob")
+    pd, ldd = _mat(dlogits, "dlogits", logits.shape, logits.dtype)
+    _check(_lib.token_logprobs_backward(pz, ldz, code, py, bits, T, _n32(V), temperature, _vec(lse, "lse", T),
+                                        _vec(entropy, "entropy", T), _vec(dlogprob, "dlogprob", T),
+                                        _vec(dentropy, "dentropy", T), pd, ldd, _launch_stream(stream)),
+           "token_logprobs_backward")
+
+
+__all__ += ["token_logprobs_forward", "token_logprobs_backward", "LOGPROB_MAX_TOP"]

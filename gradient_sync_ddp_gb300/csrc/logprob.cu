@@ -1,0 +1,661 @@
+// Log probabilities of given tokens, with the entropy and the most probable
+// entries, and their gradient.
+//
+// For a token with logits z[0..V), a target y and the temperature τ:
+//   p = softmax(z / τ), lse = ln Σ exp(z / τ), log p_v = z_v / τ − lse
+//   logprob = log p_y (0 where y lies outside the vocabulary)
+//   entropy = −Σ p_v log p_v
+//   top: the k largest z in descending order, the lower index first among equals
+//   dz_v = (dlogprob·([v = y] − p_v) − dentropy·p_v·(log p_v + entropy)) / τ
+// A logit of −infinity has probability 0; a token with nothing else has lse
+// −infinity, log probabilities −infinity, entropy 0 and gradient 0.
+//
+// Forward: one launch, one pass over z from HBM.  A CTA takes a token (a cluster
+// of CTAs, each a slice of the vocabulary, when tokens are too few to fill the
+// GPU).  With x = (z − reference)·log2(e)/τ a thread sums 2^x and x·2^x about a
+// reference of its own that stays within 8 of its largest x, so that neither
+// sum loses what the entropy, log2(Σ2^x) − Σx2^x / Σ2^x, is the difference of.
+// Top entries: the first vectors that the threads load are spread over the row.
+// Each thread's largest logit of them is sorted within its warp; the smallest,
+// over the 8 warps, of the warps' ceil(k/8)-th largest is a bound that at least
+// k entries of the row reach.  During the rest of the pass a thread only notes
+// the vectors whose maximum reaches it.  The same bound over whole rows is
+// tighter; of the noted vectors that reach it the entries are collected (about
+// 1.5·k of them), and each one's rank among them is counted.  Where the lists
+// run over (long ties, a row whose large entries lie where few threads saw
+// them), or a short row leaves warps without entries, the k-th largest is found
+// by digits of (value, index), as whole numbers of 64 bits.
+#include <cstdint>
+
+#include "vocab.cuh"
+
+namespace ddp {
+namespace {
+
+constexpr int kThr = kVocabThreads, kWarps = kThr / 32;
+constexpr int kMaxTop = DDP_LOGPROB_MAX_TOP;
+constexpr int kVectors = 6;          // in flight per thread
+constexpr int kHits = 2048;          // vectors noted during the pass
+constexpr int kCands = 1024;         // entries collected
+constexpr int kCount = 256;          // up to this many entries ranks are counted at once
+constexpr float kRaise = 8.0f;       // how far a thread's x may lie above its reference
+constexpr float kFarRef = 4096.0f;   // of the reference times log2(e)/τ: beyond, its spacing is felt: differences first
+static_assert(kMaxCluster * kMaxTop <= kCands, "a cluster's lists are joined in one");
+
+struct ForwardParams {
+    const void* z;
+    const void* target;
+    float* logprob;
+    float* entropy;
+    float* lse;
+    void* top_index;
+    float* top_logprob;
+    int64_t ldz, ldti, ldtl, T;
+    int32_t V, k;
+    float tau, c;                    // c = log2(e) / τ
+    int32_t target_64, index_64, cluster;
+};
+
+__device__ __forceinline__ int64_t load_target(const void* t, int32_t is64, int64_t row) {
+    return is64 ? static_cast<const int64_t*>(t)[row] : static_cast<int64_t>(static_cast<const int32_t*>(t)[row]);
+}
+
+// Whole numbers in the order of the values: 0 and −0 alike, NaN above all.
+__device__ __forceinline__ uint32_t order_of(float z) {
+    const uint32_t u = __float_as_uint(z + 0.0f);
+    return z != z ? 0xffffffffu : (u & 0x80000000u) ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float value_of(uint32_t o) {
+    return __uint_as_float((o & 0x80000000u) ? o & 0x7fffffffu : ~o);
+}
+__device__ __forceinline__ uint64_t entry(float z, int v) {     // the larger value first, then the lower index
+    return static_cast<uint64_t>(order_of(z)) << 32 | static_cast<uint32_t>(~v);
+}
+
+// NaN if one is among them.
+template <bool BF16>
+__device__ __forceinline__ float vec_max(const uint4& v) {
+    if constexpr (BF16) {
+        uint32_t a, b;
+        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(v.x), "r"(v.y));
+        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(v.z), "r"(v.w));
+        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(a), "r"(b));
+        return max_nan(bf16_lo(a), bf16_hi(a));
+    } else {
+        return max_nan(max_nan(__uint_as_float(v.x), __uint_as_float(v.y)), max_nan(__uint_as_float(v.z), __uint_as_float(v.w)));
+    }
+}
+
+// A thread's sums about its reference m: x = z·c − mc, s0 = Σ 2^x, s1 = Σ x·2^x.
+struct Sums {
+    float m = -INFINITY, mc = 0.0f;
+    uint64_t s0 = 0, s1 = 0;          // pairs, added at the end
+    bool bad = false;                 // +infinity or NaN
+    __device__ __forceinline__ void raise(float to, float c) {
+        if (!(to < INFINITY)) {
+            bad = true;
+            return;
+        }
+        const float n = fminf(fmaxf(to * c, -kHuge), kHuge), d = m == -INFINITY ? -kHuge : mc - n, f = pow2(d);
+        // sums of 0 stay 0 however far the reference moves, and what is 0 beside the new one goes
+        if (f == 0.0f) {
+            s0 = s1 = 0;
+        } else {
+            s1 = mul2(fma2(pair(d, d), s0, s1), pair(f, f));
+            s0 = mul2(s0, pair(f, f));
+        }
+        m = to;
+        mc = n;
+    }
+    template <bool BF16>
+    __device__ __forceinline__ void add(const uint4& v, float c) {
+        const uint64_t c2 = pair(c, c), n2 = pair(-mc, -mc);
+#pragma unroll
+        for (int e = 0; e < (BF16 ? 4 : 2); ++e) {
+            const uint64_t x = fma2(vec_pair<BF16>(v, e), c2, n2), p = pow2_pair(x);
+            s0 = add2(s0, p);
+            float lo, hi;
+            unpair(x, lo, hi);
+            s1 = fma2(pair(fmaxf(lo, -200.0f), fmaxf(hi, -200.0f)), p, s1);   // −infinity·0 would be NaN
+        }
+    }
+    __device__ __forceinline__ void add_one(float z, float c) {
+        const float x = fmaf(z, c, -mc), p = pow2(x);
+        s0 = add2(s0, pair(p, 0.0f));
+        s1 = fma2(pair(fmaxf(x, -200.0f), 0.0f), pair(p, 0.0f), s1);
+    }
+};
+
+// A warp's values in descending order over its lanes.
+__device__ __forceinline__ uint32_t warp_sort(uint32_t v) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int size = 2; size <= 32; size *= 2) {
+#pragma unroll
+        for (int step = size / 2; step > 0; step /= 2) {
+            const uint32_t o = __shfl_xor_sync(0xffffffffu, v, step);
+            const bool up = ((lane & size) == 0) == ((lane & step) == 0);    // this lane keeps the larger one
+            v = up ? max(v, o) : min(v, o);
+        }
+    }
+    return v;
+}
+
+struct TopShared {
+    uint64_t cand[kCands];
+    uint64_t top[kMaxTop];
+    int2 hit[kHits];                 // vector, its maximum
+    int hist[256];
+    uint32_t bound[2][kWarps];
+    int hits, cands, digit, above;
+};
+
+// What at least k entries of the CTA's slice reach, given each thread's largest; all threads call it.
+__device__ __forceinline__ float top_bound(float mine, int k, uint32_t* sh) {
+    const uint32_t s = warp_sort(order_of(mine));
+    if ((threadIdx.x & 31) == (k + kWarps - 1) / kWarps - 1) sh[threadIdx.x >> 5] = s;
+    __syncthreads();
+    uint32_t b = sh[0];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) b = min(b, sh[w]);
+    return value_of(b);
+}
+
+// Leaves in t.cand the k largest of the entries that each(body) passes to body, and in t.cands their number.  Entries
+// are distinct; each() may read t.cand: it is written only after the last pass over it.  All threads call it, with more
+// than k entries.
+template <class Each>
+__device__ void select_by_digits(TopShared& t, int k, Each each) {
+    uint64_t prefix = 0;
+    int need = k;
+    for (int shift = 56; shift >= 0; shift -= 8) {
+        t.hist[threadIdx.x] = 0;
+        __syncthreads();
+        each([&](uint64_t e) {
+            if (shift == 56 || (e >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&t.hist[(e >> shift) & 255], 1);
+        });
+        __syncthreads();
+        if (threadIdx.x < 32) {                          // lane l: digits 255 − 8l down to 248 − 8l
+            const int hi = 255 - 8 * static_cast<int>(threadIdx.x);
+            int n = 0;
+            for (int i = 0; i < 8; ++i) n += t.hist[hi - i];
+            int before = n;
+#pragma unroll
+            for (int o = 1; o < 32; o *= 2) {
+                const int x = __shfl_up_sync(0xffffffffu, before, o);
+                if (static_cast<int>(threadIdx.x) >= o) before += x;
+            }
+            before -= n;                                 // entries of larger digits
+            if (before < need && before + n >= need) {
+                for (int i = 0; i < 8; ++i) {
+                    const int h = t.hist[hi - i];
+                    if (before + h >= need) {
+                        t.digit = hi - i;
+                        t.above = before;
+                        break;
+                    }
+                    before += h;
+                }
+            }
+        }
+        __syncthreads();
+        prefix |= static_cast<uint64_t>(t.digit) << shift;
+        need -= t.above;
+        if (t.hist[t.digit] == need) break;              // all of this digit belong to the k largest
+        __syncthreads();
+    }
+    // the survivors, held by their threads until the last read of the source
+    if (threadIdx.x == 0) t.cands = 0;
+    uint64_t keep[kCands / kThr];
+    int n = 0;
+    bool more = false;
+    each([&](uint64_t e) {
+        if (e < prefix) return;
+        if (n < kCands / kThr) {
+#pragma unroll
+            for (int i = 0; i < kCands / kThr; ++i)
+                if (i == n) keep[i] = e;
+            ++n;
+        } else {
+            more = true;
+        }
+    });
+    // a thread with more of them than it holds: only of a source that is not t.cand (there it has kCands / kThr at most)
+    if (__syncthreads_or(more)) {
+        each([&](uint64_t e) {
+            if (e >= prefix) t.cand[atomicAdd(&t.cands, 1)] = e;
+        });
+    } else {
+#pragma unroll
+        for (int i = 0; i < kCands / kThr; ++i)
+            if (i < n) t.cand[atomicAdd(&t.cands, 1)] = keep[i];
+    }
+    __syncthreads();
+}
+
+// The k largest of t.cand[0..n) (all of them if fewer), in order, in t.top; n is at most kCands.
+__device__ __forceinline__ int sort_top(TopShared& t, int n, int k) {
+    if (n > kCount && n > k) {
+        select_by_digits(t, k, [&](auto body) {
+            for (int i = threadIdx.x; i < n; i += kThr) body(t.cand[i]);
+        });
+        n = k;
+    }
+    const int m = min(n, k);
+    if (static_cast<int>(threadIdx.x) < n) {
+        const uint64_t mine = t.cand[threadIdx.x];
+        int rank = 0;
+        for (int i = 0; i < n; ++i) rank += t.cand[i] > mine;
+        if (rank < m) t.top[rank] = mine;
+    }
+    __syncthreads();
+    return m;
+}
+
+__device__ __forceinline__ uint64_t cluster_read64(const uint64_t* p, uint32_t rank) {
+    uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(p)), r;
+    uint64_t v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(r) : "memory");
+    return v;
+}
+
+template <bool BF16, bool TOP>
+__global__ void __launch_bounds__(kThr, 4) logprob_kernel(const __grid_constant__ ForwardParams a) {
+    constexpr int VEC = BF16 ? 8 : 4, ES = BF16 ? 2 : 4, U = kVectors;
+    __shared__ alignas(16) unsigned char raw[TOP ? sizeof(TopShared) : 16];
+    __shared__ float2 sh[2][kWarps];
+    __shared__ float s_part[3];                          // this CTA's (reference, Σ2^x, Σx2^x), read by its cluster
+    __shared__ int s_tops;
+    TopShared& t = *reinterpret_cast<TopShared*>(raw);
+    pdl_enter();
+    const int tid = threadIdx.x;
+    const int64_t row = blockIdx.x / a.cluster;
+    const int rank = blockIdx.x % a.cluster;
+    const char* z = row_ptr<BF16>(a.z, row, a.ldz);
+    // slices of whole 256-byte lines of the row's own grid
+    const int per = ((a.V + a.cluster - 1) / a.cluster + 127) / 128 * 128;
+    const int v0 = min(a.V, rank * per), v1 = min(a.V, v0 + per);
+    const Slice s = make_slice<BF16>(z, v0, v1);
+    const char* zv = s.base + static_cast<int64_t>(s.v0 + s.lead) * ES;
+    const float c = a.c;
+    const int64_t target = tid == 0 && rank == 0 && a.logprob ? load_target(a.target, a.target_64, row) : -1;
+    const bool inside = target >= 0 && target < a.V;
+    const float zt = inside ? load_elem<BF16>(z, target) : 0.0f;
+    const bool has_edge = tid < s.lead + s.tail;
+    const int ve = has_edge ? edge<BF16>(s, tid) : 0;
+    const float xe = has_edge ? load_elem<BF16>(z, ve) : -INFINITY;
+    if constexpr (TOP) {
+        if (tid == 0) t.hits = t.cands = 0;
+    }
+
+    // ---- the pass: group j + u·J of 256 vectors in the j-th round, so that the first round is spread over the slice
+    Sums w;
+    float most = xe, bound = INFINITY;                   // the thread's largest logit; what the k largest reach
+    const int groups = (s.nvec + kThr - 1) / kThr, J = (groups + U - 1) / U;
+    auto note = [&](int i, float vm) {
+        if constexpr (TOP) {
+            if (vm < bound) return;
+            const int at = atomicAdd(&t.hits, 1);
+            if (at < kHits) t.hit[at] = make_int2(i, __float_as_int(vm));
+        }
+    };
+    for (int j = 0; j < J; ++j) {
+        uint4 v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = (j + u * J) * kThr + tid;
+            if (i < s.nvec) v[u] = TOP ? ld16_keep(zv + static_cast<int64_t>(i) * 16) : ld16<true>(zv + static_cast<int64_t>(i) * 16);
+        }
+        if (j == 0) {
+            float vm[U], top = has_edge ? xe : -INFINITY;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                vm[u] = u * J * kThr + tid < s.nvec ? vec_max<BF16>(v[u]) : -INFINITY;
+                top = max_nan(top, vm[u]);
+            }
+            if (!(top == -INFINITY)) w.raise(top, c);
+            most = top;
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (u * J * kThr + tid < s.nvec) w.add<BF16>(v[u], c);
+            if constexpr (TOP) {
+                bound = top_bound(top, a.k, t.bound[0]);
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (u * J * kThr + tid < s.nvec) note(u * J * kThr + tid, vm[u]);
+            }
+        } else {
+            const float room = kRaise / c;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int i = (j + u * J) * kThr + tid;
+                if (i >= s.nvec) continue;
+                const float vm = vec_max<BF16>(v[u]);
+                most = max_nan(most, vm);
+                if (!(vm < fminf(w.m + room, bound))) {
+                    if (!(vm < w.m + room)) {
+                        if (vm > -INFINITY || vm != vm) w.raise(vm, c);
+                    }
+                    note(i, vm);
+                }
+                w.add<BF16>(v[u], c);
+            }
+        }
+    }
+    if (J == 0) {                                        // a slice of its ends alone
+        if (!(xe == -INFINITY)) w.raise(xe, c);
+        if constexpr (TOP) __syncthreads();              // t.hits
+    }
+    if (has_edge) w.add_one(xe, c);
+
+    // ---- the CTA's sums about one reference
+    float s0, s1, lo, hi, m = w.m, mc = w.m == -INFINITY ? -INFINITY : w.mc;
+    unpair(w.s0, lo, hi);
+    s0 = lo + hi;
+    unpair(w.s1, lo, hi);
+    s1 = lo + hi;
+    if constexpr (TOP) bound = top_bound(most, a.k, t.bound[1]);
+    float M = m, MC = mc;
+    once_all2<MaxOp, MaxOp>(M, MC, sh[0]);
+    const bool bad = __syncthreads_or(w.bad);
+    if (MC > -INFINITY && fabsf(MC) > kFarRef) {         // far from 0: again, of differences about the largest
+        w = Sums{};
+        float top = most != most ? -INFINITY : most;
+        top = warp_all<MaxOp>(top);
+        if ((tid & 31) == 0) sh[0][tid >> 5].x = top;
+        __syncthreads();
+        M = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) M = fmaxf(M, sh[0][i].x);
+        s0 = s1 = 0.0f;
+        auto one = [&](float x) {
+            x = (x - M) * c;
+            const float p = pow2(x);
+            s0 += p;
+            s1 = fmaf(fmaxf(x, -200.0f), p, s1);
+        };
+        each_vector<BF16, true>(s, [&](int, const uint4& v) {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) one(vec_elem<BF16>(v, e));
+        });
+        if (has_edge) one(xe);
+    } else {
+        // x is of z·c − mc: about MC, then about M·c itself, of which MC is the rounded value
+        const float d = mc - MC, f = mc > -INFINITY ? pow2(d) : 0.0f;
+        const float r = MC > -INFINITY ? fmaf(M, c, -MC) : 0.0f, g = pow2(-r);
+        s1 = f == 0.0f ? 0.0f : fmaf(d, s0, s1) * f;
+        s0 = f == 0.0f ? 0.0f : s0 * f;
+        s1 = (s1 - r * s0) * g;
+        s0 *= g;
+    }
+    once_all2<SumOp, SumOp>(s0, s1, sh[1]);
+    if (bad) s0 = s1 = __int_as_float(0x7fffffff);
+
+    // ---- the CTA's k largest, in order
+    int tops = 0;
+    if constexpr (TOP) {
+        // t.hits is final: the barrier of the sums lies between
+        const int hits = t.hits;
+        auto collect = [&](float x, int v) {
+            if (x < bound) return;
+            const int at = atomicAdd(&t.cands, 1);
+            if (at < kCands) t.cand[at] = entry(x, v);
+        };
+        const int first = s.v0 + s.lead;
+        if (has_edge) collect(xe, ve);
+        if (hits <= kHits) {
+            for (int h = tid; h < hits; h += kThr) {
+                const int2 q = t.hit[h];
+                if (__int_as_float(q.y) < bound) continue;
+                const uint4 v = ld16_keep(zv + static_cast<int64_t>(q.x) * 16);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) collect(vec_elem<BF16>(v, e), first + q.x * VEC + e);
+            }
+        } else {
+            each_vector<BF16, true>(s, [&](int i, const uint4& v) {
+                if (vec_max<BF16>(v) < bound) return;
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) collect(vec_elem<BF16>(v, e), first + i * VEC + e);
+            });
+        }
+        __syncthreads();
+        int n = t.cands;
+        if (n > kCands) {                                // more than kCands >= k entries: by digits of the whole slice
+            __syncthreads();
+            select_by_digits(t, a.k, [&](auto body) {
+                each_vector<BF16, true>(s, [&](int i, const uint4& v) {
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) body(entry(vec_elem<BF16>(v, e), first + i * VEC + e));
+                });
+                if (has_edge) body(entry(xe, ve));
+            });
+            n = a.k;
+        }
+        tops = sort_top(t, n, a.k);
+    }
+
+    // ---- the cluster's
+    if (a.cluster > 1) {
+        if (tid == 0) {
+            s_part[0] = M;
+            s_part[1] = s0;
+            s_part[2] = s1;
+            s_tops = tops;
+        }
+        cluster_sync();
+        if (rank == 0) {
+            float pm[kMaxCluster], p0[kMaxCluster], p1[kMaxCluster];
+            M = -INFINITY;
+#pragma unroll
+            for (int r = 0; r < kMaxCluster; ++r) {
+                pm[r] = r < a.cluster ? cluster_read(&s_part[0], r) : -INFINITY;
+                p0[r] = r < a.cluster ? cluster_read(&s_part[1], r) : 0.0f;
+                p1[r] = r < a.cluster ? cluster_read(&s_part[2], r) : 0.0f;
+                M = fmaxf(M, pm[r]);
+            }
+            s0 = s1 = 0.0f;
+#pragma unroll
+            for (int r = 0; r < kMaxCluster; ++r) {
+                const float d = (pm[r] - M) * c, f = pm[r] > -INFINITY ? pow2(d) : 0.0f;
+                if (f == 0.0f && p0[r] == p0[r]) continue;   // NaN is not dropped
+                s0 = fmaf(p0[r], f, s0);
+                s1 = fmaf(fmaf(d, p0[r], p1[r]), f, s1);
+            }
+            if constexpr (TOP) {
+                int n = 0;
+                for (int r = 0; r < a.cluster; ++r) {
+                    const int m = __float_as_int(cluster_read(reinterpret_cast<const float*>(&s_tops), r));
+                    if (tid < m) t.cand[n + tid] = cluster_read64(&t.top[tid], r);
+                    n += m;
+                }
+                __syncthreads();
+                tops = sort_top(t, n, a.k);
+            }
+        }
+        cluster_sync();                                  // no CTA ends while another reads its part
+        if (rank != 0) return;
+    }
+    // log p of a logit: (z − M) / τ − ln Σ2^x (differences that fp32 holds stay finite)
+    const float l0 = log2f(s0);
+    auto logp = [&](float x) { return M > -INFINITY || bad ? (x - M) / a.tau - l0 * kLn2 : l0; };
+    if (tid == 0) {
+        if (a.logprob) a.logprob[row] = inside ? logp(zt) : 0.0f;
+        if (a.lse) a.lse[row] = M > -INFINITY ? M / a.tau + l0 * kLn2 : l0;
+        if (a.entropy) {
+            const float h = (l0 - s1 / s0) * kLn2;
+            a.entropy[row] = s0 == 0.0f || h < 0.0f ? 0.0f : h;
+        }
+    }
+    if constexpr (TOP) {
+        for (int j = tid; j < a.k; j += kThr) {
+            const uint64_t e = j < tops ? t.top[j] : 0;
+            const int64_t v = j < tops ? static_cast<int64_t>(static_cast<uint32_t>(~e)) : -1;
+            if (a.top_index) {
+                if (a.index_64) static_cast<int64_t*>(a.top_index)[row * a.ldti + j] = v;
+                else static_cast<int32_t*>(a.top_index)[row * a.ldti + j] = static_cast<int32_t>(v);
+            }
+            if (a.top_logprob) a.top_logprob[row * a.ldtl + j] = j < tops ? logp(value_of(static_cast<uint32_t>(e >> 32))) : -INFINITY;
+        }
+    }
+}
+
+struct BackwardParams {
+    const void* z;
+    const void* target;
+    const float* lse;
+    const float* entropy;
+    const float* dlogprob;
+    const float* dentropy;
+    void* dz;
+    int64_t ldz, lddz, T;
+    int32_t V;
+    float tau, c;
+    int32_t target_64, slices;
+};
+
+// A CTA per slice of a token's row: with the log-sum-exp at hand slices do not
+// depend on one another.  dz_v = p_v·(A + B·log2 p_v), and dlogprob / τ more at the target.
+template <bool BF16>
+__global__ void __launch_bounds__(kThr, 4) logprob_grad_kernel(const __grid_constant__ BackwardParams a) {
+    constexpr int VEC = BF16 ? 8 : 4, ES = BF16 ? 2 : 4;
+    pdl_enter();
+    const int tid = threadIdx.x;
+    const int64_t row = blockIdx.x / a.slices;
+    const int part = blockIdx.x % a.slices;
+    const char* z = row_ptr<BF16>(a.z, row, a.ldz);
+    char* dz = row_ptr<BF16>(a.dz, row, a.lddz);
+    const int per = ((a.V + a.slices - 1) / a.slices + 127) / 128 * 128;
+    const int v0 = min(a.V, part * per), v1 = min(a.V, v0 + per);
+    if (v0 == v1) return;
+    const Slice s = make_slice<BF16>(z, v0, v1);
+    const int64_t target = a.dlogprob ? load_target(a.target, a.target_64, row) : -1;
+    const bool inside = target >= 0 && target < a.V, here = target >= v0 && target < v1;
+    const float lse = a.lse[row], up = inside ? a.dlogprob[row] : 0.0f, ue = a.dentropy ? a.dentropy[row] : 0.0f;
+    const float h = ue != 0.0f ? a.entropy[row] : 0.0f;
+    const float zt = here ? load_elem<BF16>(z, target) : 0.0f;
+    if (here) __syncthreads();                           // read before dz, which may be z, is written
+    const bool has_edge = tid < s.lead + s.tail;
+    const int ve = has_edge ? edge<BF16>(s, tid) : 0;
+    const float xe = has_edge ? load_elem<BF16>(z, ve) : 0.0f;
+    if ((up == 0.0f && ue == 0.0f) || lse == -INFINITY) {
+        write_zero<BF16>(s, dz);
+        return;
+    }
+    const float A = -(up + ue * h) / a.tau, B = -ue * kLn2 / a.tau;
+    // log2 p = z·c − L − ls, L the rounded lse·log2(e) and ls what that left; of logits far from 0 (z − m)·c − ls
+    const float L = lse * kLog2e, m = fminf(fmaxf(lse * a.tau, -kHuge), kHuge);
+    const bool far = !(fabsf(L) <= kFarRef);
+    const float ls = far ? fmaf(lse, a.tau, -m) * a.c : fmaf(lse, kLog2e, -L) + lse * kLog2eLow;
+    // log2 p is at most 0 (a kept lse of far logits is rounded by more than ln V), and −infinity·0 would be NaN
+    auto grad = [&](float x) {
+        float l = far ? (x - m) * a.c - ls : fmaf(x, a.c, -L) - ls;
+        l = l > 0.0f ? 0.0f : l;
+        return pow2(l) * fmaf(B, l < -200.0f ? -200.0f : l, A);
+    };
+    char* dv = dz + static_cast<int64_t>(s.v0 + s.lead) * ES;
+    const bool whole = (reinterpret_cast<uintptr_t>(dv) & 15) == 0;
+    each_vector<BF16, false>(s, [&](int i, const uint4& v) {
+        float o[VEC];
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) o[e] = grad(vec_elem<BF16>(v, e));
+        uint4 w;
+        if constexpr (BF16) w = make_uint4(pack2(o[0], o[1]), pack2(o[2], o[3]), pack2(o[4], o[5]), pack2(o[6], o[7]));
+        else w = f4_bits(o[0], o[1], o[2], o[3]);
+        if (whole) st16(dv + static_cast<int64_t>(i) * 16, w);
+        else store_vec_anywhere<BF16>(dv + static_cast<int64_t>(i) * 16, w);
+    });
+    if (has_edge) store_elem<BF16>(dz, ve, grad(xe));
+    if (here && up != 0.0f) {                            // in every thread alike
+        __syncthreads();                                 // before the target's entry is written again
+        if (tid == 0) store_elem<BF16>(dz, target, grad(zt) + up / a.tau);
+    }
+}
+
+// log2(e)/τ, or 0 where the temperature is not one.
+float scale_of(float tau) {
+    if (!(tau > 0.0f) || !(tau < 3.0e38f)) return 0.0f;
+    const float c = static_cast<float>(1.4426950408889634 / static_cast<double>(tau));
+    return c > 1.2e-38f && c < 3.0e38f ? c : 0.0f;
+}
+
+}  // namespace
+}  // namespace ddp
+
+using namespace ddp;
+
+extern "C" int token_logprobs_forward(const void* logits, int64_t ldz, int32_t dtype, const void* target,
+                                      int32_t target_bits, int64_t T, int32_t V, float temperature, float* logprob,
+                                      float* entropy, float* lse, int32_t k, void* top_index, int64_t ldti,
+                                      int32_t index_bits, float* top_logprob, int64_t ldtl, void* stream) {
+    const float c = scale_of(temperature);
+    if (!dtype_ok(dtype) || (target_bits != 32 && target_bits != 64) || (index_bits != 32 && index_bits != 64) || T < 0 ||
+        V < 1 || k < 0 || c == 0.0f)
+        return DDP_ERR_INVALID_ARG;
+    if (k > kMaxTop || V > kMaxWidth) return DDP_ERR_UNSUPPORTED;
+    const int es = dsize(dtype);
+    const Mat mz{logits, T, V, ldz, es}, mt{target, 1, T, T, target_bits / 8}, ml{logprob, 1, T, T, 4},
+        me{entropy, 1, T, T, 4}, ms{lse, 1, T, T, 4}, mi{top_index, T, k, ldti, index_bits / 8},
+        mp{top_logprob, T, k, ldtl, 4};
+    if (!mat_valid(mz) || !mat_valid(mt) || (top_index && !mat_valid(mi)) || (top_logprob && !mat_valid(mp)))
+        return DDP_ERR_INVALID_ARG;
+    if (T > 0 && (logits == nullptr || (logprob != nullptr && target == nullptr))) return DDP_ERR_INVALID_ARG;
+    const Mat* outs[5] = {&ml, &me, &ms, &mi, &mp};
+    for (const Mat* m : {&mz, &mt})
+        if (!mat_aligned(*m)) return DDP_ERR_ALIGNMENT;
+    for (const Mat* m : outs)
+        if (!mat_aligned(*m)) return DDP_ERR_ALIGNMENT;
+    for (int i = 0; i < 5; ++i) {
+        if (mats_overlap(*outs[i], mz) || mats_overlap(*outs[i], mt)) return DDP_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j)
+            if (mats_overlap(*outs[i], *outs[j])) return DDP_ERR_INVALID_ARG;
+    }
+    if (T == 0) return DDP_OK;
+    DeviceInfo d;
+    const int st = current_device_info(&d);
+    if (st != DDP_OK) return st;
+    // one CTA per token fills the GPU from about two CTAs per SM; fewer tokens are split into slices of at least
+    // 2048 logits each
+    int cluster = 1;
+    while (cluster < kMaxCluster && V / (2 * cluster) >= 2048 && T * cluster < 2ll * d.sm_count) cluster *= 2;
+    if (T * cluster > INT32_MAX) return DDP_ERR_UNSUPPORTED;
+    const bool top = k > 0 && (top_index != nullptr || top_logprob != nullptr);
+    const ForwardParams p{logits, target, logprob, entropy, lse, top_index, top_logprob, ldz, ldti, ldtl, T, V, k,
+                          temperature, c, target_bits == 64, index_bits == 64, cluster};
+    void (*kernel)(ForwardParams) = dtype == DDP_BF16 ? (top ? logprob_kernel<true, true> : logprob_kernel<true, false>)
+                                                      : (top ? logprob_kernel<false, true> : logprob_kernel<false, false>);
+    return launch_smem(kernel, static_cast<unsigned>(T * cluster), kThr, 0, static_cast<cudaStream_t>(stream), p,
+                       static_cast<unsigned>(cluster));
+}
+
+extern "C" int token_logprobs_backward(const void* logits, int64_t ldz, int32_t dtype, const void* target,
+                                       int32_t target_bits, int64_t T, int32_t V, float temperature, const float* lse,
+                                       const float* entropy, const float* dlogprob, const float* dentropy,
+                                       void* dlogits, int64_t lddz, void* stream) {
+    const float c = scale_of(temperature);
+    if (!dtype_ok(dtype) || (target_bits != 32 && target_bits != 64) || T < 0 || V < 1 || c == 0.0f) return DDP_ERR_INVALID_ARG;
+    if (V > kMaxWidth) return DDP_ERR_UNSUPPORTED;
+    const int es = dsize(dtype);
+    const Mat mz{logits, T, V, ldz, es}, mt{target, 1, T, T, target_bits / 8}, ms{lse, 1, T, T, 4},
+        me{entropy, 1, T, T, 4}, mu{dlogprob, 1, T, T, 4}, mh{dentropy, 1, T, T, 4}, md{dlogits, T, V, lddz, es};
+    if (!mat_valid(mz) || !mat_valid(mt) || !mat_valid(md)) return DDP_ERR_INVALID_ARG;
+    if (T > 0 && (logits == nullptr || lse == nullptr || dlogits == nullptr || (dlogprob != nullptr && target == nullptr) ||
+                  (dentropy != nullptr && entropy == nullptr)))
+        return DDP_ERR_INVALID_ARG;
+    for (const Mat* m : {&mz, &mt, &ms, &me, &mu, &mh, &md})
+        if (!mat_aligned(*m)) return DDP_ERR_ALIGNMENT;
+    if (!mats_same(md, mz) && mats_overlap(md, mz)) return DDP_ERR_INVALID_ARG;
+    for (const Mat* i : {&mt, &ms, &me, &mu, &mh})
+        if (mats_overlap(md, *i)) return DDP_ERR_INVALID_ARG;
+    if (T == 0) return DDP_OK;
+    DeviceInfo d;
+    const int st = current_device_info(&d);
+    if (st != DDP_OK) return st;
+    int slices = 1;                                      // as the forward pass, without a cluster's limit
+    while (slices < 64 && V / (2 * slices) >= 2048 && T * slices < 4ll * d.sm_count) slices *= 2;
+    if (T * slices > INT32_MAX) return DDP_ERR_UNSUPPORTED;
+    const BackwardParams p{logits, target, lse, entropy, dlogprob, dentropy, dlogits, ldz, lddz, T, V, temperature, c,
+                           target_bits == 64, slices};
+    return launch_pdl(dtype == DDP_BF16 ? logprob_grad_kernel<true> : logprob_grad_kernel<false>,
+                      dim3(static_cast<unsigned>(T * slices)), kThr, static_cast<cudaStream_t>(stream), p);
+}

@@ -803,6 +803,56 @@ int layernorm_backward(const void* dy, int64_t lddy, int32_t dy_dtype, const voi
                        int64_t rows, int32_t D, void* dx, int64_t lddx, float* dgamma, float* dbeta, void* workspace,
                        size_t workspace_bytes, void* stream);
 
+#define DDP_LOGPROB_MAX_TOP 128
+
+/*
+ * token_logprobs_forward — log probabilities of given tokens.  Per token, with
+ * logits z[0..V) and a target y, at temperature t, p = softmax(z/t):
+ *     lse = ln(sum exp(z/t)),  logprob = z_y/t - lse,  entropy = -sum p ln p,
+ *     the k most probable entries in descending order with their log
+ *     probabilities (equal logits by ascending index)
+ *   logits        device [T, V], dtype
+ *   target        device [T], int32 or int64 (target_bits 32 or 64); NULL
+ *                 where logprob is; a target outside [0, V) (padding) has
+ *                 logprob 0
+ *   logprob, entropy, lse   device float[T] each, or NULL (not wanted)
+ *   k             0 .. DDP_LOGPROB_MAX_TOP, V <= 2^31 - 65536
+ *                 (DDP_ERR_UNSUPPORTED beyond)
+ *   top_index     device [T, k], int32 or int64 (index_bits 32 or 64), or NULL
+ *   top_logprob   device float[T, k] or NULL.  Entries past the vocabulary
+ *                 (k > V) have index -1 and log probability -infinity: what
+ *                 distill_topk_forward takes for no entry
+ *   temperature   > 0
+ * Logits of -infinity have probability 0 (they are listed last, with their
+ * index and log probability -infinity); a token with no others has lse
+ * -infinity, entropy 0 and log probabilities -infinity.  A token with a logit
+ * of NaN or +infinity has logprob, entropy, lse and top_logprob NaN; its
+ * largest entries are listed all the same, NaN before +infinity.
+ * Results depend on the logits' differences: a token whose logits are all far
+ * from 0 keeps its distribution (its lse is rounded as fp32 numbers are).
+ */
+int token_logprobs_forward(const void* logits, int64_t ldz, int32_t dtype, const void* target, int32_t target_bits,
+                           int64_t T, int32_t V, float temperature, float* logprob, float* entropy, float* lse,
+                           int32_t k, void* top_index, int64_t ldti, int32_t index_bits, float* top_logprob,
+                           int64_t ldtl, void* stream);
+
+/*
+ * token_logprobs_backward — the gradient of logprob and entropy:
+ *     dlogits[v] = (dlogprob*([v = y] - p_v) - dentropy*p_v*(ln p_v + entropy))/t
+ *   lse, entropy         what the forward pass wrote (entropy may be NULL
+ *                        without dentropy).  An fp32 lse is off by up to
+ *                        |lse|*2^-24, and p by that factor
+ *   dlogprob, dentropy   device float[T] each, or NULL (no gradient comes that
+ *                        way); target may be NULL without dlogprob, and a
+ *                        target outside [0, V) takes no dlogprob
+ *   dlogits              device [T, V], dtype; may be logits itself
+ * A token that takes neither (0 in both) has gradient 0, whatever its logits
+ * hold, and so has one whose lse is -infinity.
+ */
+int token_logprobs_backward(const void* logits, int64_t ldz, int32_t dtype, const void* target, int32_t target_bits,
+                            int64_t T, int32_t V, float temperature, const float* lse, const float* entropy,
+                            const float* dlogprob, const float* dentropy, void* dlogits, int64_t lddz, void* stream);
+
 /* Human-readable name of a ddp_status value (static string). */
 const char* ddp_status_string(int status);
 

@@ -51,8 +51,9 @@ def token_logprobs(logits, target, temperature, k=0):
             lse[t] = -np.inf
             lp = np.full(V, -np.inf)
         else:
-            lse[t] = m + np.log(np.sum(np.exp(z - m)))
-            lp = z - lse[t]
+            rest = np.log(np.sum(np.exp(z - m)))
+            lse[t] = m + rest
+            lp = (z - m) - rest          # z − lse, without what lse is rounded by where m is far from 0
             p = np.exp(lp)
             entropy[t] = -np.sum(p[p > 0] * lp[p > 0])
         y = int(target[t])
