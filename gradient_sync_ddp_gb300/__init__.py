@@ -837,3 +837,70 @@ def token_logprobs_backward(logits, target, lse, dlogprob, dlogits, entropy=None
 
 
 __all__ += ["token_logprobs_forward", "token_logprobs_backward", "LOGPROB_MAX_TOP"]
+
+
+_lib.newton_schulz_workspace_bytes.argtypes = [_i32] * 3
+_lib.newton_schulz_workspace_bytes.restype = _c.c_size_t
+_lib.newton_schulz.argtypes = [_P, _i64, _i32, _P, _i64, _i32, _i32, _i32, _i32, _i32, _f32, _P, _c.c_size_t, _P]
+_lib.newton_schulz.restype = _c.c_int
+_lib.ddp_bucket_allreduce_muon.argtypes = [_P, _i32, _i32, _P, _i32, _i32, _i32, _P, _P, _f32, _f32, _f32, _f32, _i32, _i32,
+                                           _f32, _P, _P, _c.c_size_t, _P]
+_lib.ddp_bucket_allreduce_muon.restype = _c.c_int
+
+
+def newton_schulz_workspace_bytes(count: int, rows: int, cols: int) -> int:
+    return int(_lib.newton_schulz_workspace_bytes(_n32(count), _n32(rows), _n32(cols)))
+
+
+def _mats(ts, name: str, shape=None):
+    """(addresses, leading dimension, dtype code) of 2-D tensors that share shape, dtype and row stride."""
+    code, ld = _code(ts[0]), _mat(ts[0], name, shape)[1]
+    arr = (ctypes.c_void_p * len(ts))()
+    for i, t in enumerate(ts):
+        arr[i], ldi = _mat(t, name, ts[0].shape, ts[0].dtype)
+        if ldi != ld:
+            raise ValueError(f"{name}: row strides {ld} and {ldi}")
+    return arr, ld, code
+
+
+def newton_schulz(xs, outs, workspace, steps: int = 5, eps: float = 1e-7, stream=None) -> None:
+    """Orthogonalise the matrices xs (a list of fp32 or bf16 tensors [rows, cols] of one shape) into outs: divided by
+    their norm, then `steps` Newton-Schulz steps.  outs[i] may be xs[i]; the workspace has
+    newton_schulz_workspace_bytes(len(xs), rows, cols) bytes."""
+    if len(xs) != len(outs):
+        raise ValueError("need one output per matrix")
+    if not xs:
+        return
+    rows, cols = xs[0].shape
+    px, ldx, cx = _mats(xs, "xs")
+    po, ldo, co = _mats(outs, "outs", xs[0].shape)
+    _check(_lib.newton_schulz(px, ldx, cx, po, ldo, co, len(xs), _n32(rows), _n32(cols), steps, eps, _ptr(workspace),
+                              _bytes(workspace), _launch_stream(stream)), "newton_schulz")
+
+
+def ddp_bucket_allreduce_muon(replicas, offsets, rows: int, cols: int, param, momentum_buf, workspace, lr: float,
+                              momentum: float, weight_decay: float, update_scale: float = 1.0, nesterov: bool = True,
+                              steps: int = 5, eps: float = 1e-7, param_bf16=None, stream=None) -> None:
+    """Average the replicas' flat gradient buffers at the [rows, cols] matrices that begin at `offsets` (elements), and
+    take the optimizer step on param and momentum_buf (flat float32, in place): momentum, orthogonalised update, weight
+    decay.  The workspace has newton_schulz_workspace_bytes(len(offsets), rows, cols) bytes."""
+    if not 1 <= len(replicas) <= MAX_REPLICAS:
+        raise ValueError("need 1..16 replicas")
+    code, end = _code(replicas[0]), (max(offsets) + rows * cols if len(offsets) else 0)
+    for name, t, dtype in [("replicas", r, replicas[0].dtype) for r in replicas] + [
+            ("param", param, _Torch.f32), ("momentum_buf", momentum_buf, _Torch.f32), ("param_bf16", param_bf16, _Torch.bf16)]:
+        if t is None and name == "param_bf16":
+            continue
+        if t.dtype != dtype:
+            raise TypeError(f"{name}: dtype {t.dtype}, need {dtype}")
+        if not t.is_contiguous() or t.numel() < end:
+            raise ValueError(f"{name}: need at least {end} contiguous elements")
+    arr = (ctypes.c_int64 * max(1, len(offsets)))(*offsets)
+    _check(_lib.ddp_bucket_allreduce_muon(_ptr_array(replicas), len(replicas), code, arr, len(offsets), _n32(rows),
+                                          _n32(cols), param.data_ptr(), momentum_buf.data_ptr(), lr, momentum,
+                                          weight_decay, update_scale, int(bool(nesterov)), steps, eps, _ptr(param_bf16),
+                                          _ptr(workspace), _bytes(workspace), _launch_stream(stream)),
+           "ddp_bucket_allreduce_muon")
+
+
+__all__ += ["newton_schulz_workspace_bytes", "newton_schulz", "ddp_bucket_allreduce_muon"]

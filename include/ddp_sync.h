@@ -853,6 +853,63 @@ int token_logprobs_backward(const void* logits, int64_t ldz, int32_t dtype, cons
                             int64_t T, int32_t V, float temperature, const float* lse, const float* entropy,
                             const float* dlogprob, const float* dentropy, void* dlogits, int64_t lddz, void* stream);
 
+#define DDP_NS_GROUP 64
+
+/*
+ * newton_schulz — orthogonalises matrices of one shape by Newton-Schulz steps.
+ * Per matrix U [rows, cols] (a tall one by its transpose, so that m <= n):
+ *     X = U/(|U| + eps), |U| the Frobenius norm; `steps` times, with
+ *     (a, b, c) = (3.4445, -4.7750, 2.0315):  A = X*X^T,  X = a*X + (b*A + c*A*A)*X
+ * After 5 steps the singular values that were above about 1e-3 of the norm lie
+ * around 1 (between 0.7 and 1.2); smaller ones are grown by up to a^steps.
+ *   x, out       host arrays of `count` device pointers to row-major matrices
+ *                (ldx, ldo elements between rows), x_dtype and out_dtype;
+ *                out[i] may be x[i] itself (same dtype and ld), no other overlap
+ *   count        any; DDP_NS_GROUP matrices at a time run together
+ *   rows, cols   <= 65536 (DDP_ERR_UNSUPPORTED beyond)
+ *   steps        1 .. 16;  eps >= 0
+ *   workspace    device buffer of newton_schulz_workspace_bytes(count, rows,
+ *                cols), 16-byte aligned, contents ignored on entry; overlapping
+ *                calls need different ones
+ * The norm is the root of an fp32 sum of squares (exact enough between about
+ * 1e-19 and 1.8e19); a matrix of zeros gives zeros, one whose squares overflow
+ * or that holds a NaN or an infinity gives NaN, and leaves the others alone.
+ * Products have fp16 operands and fp32 sums: X is off by about 1e-3 of its
+ * 2-norm after 5 steps.  The tiles' waits on their own copies and products are
+ * bounded (about a second of GPU clocks): a tile whose wait ran out is written
+ * as NaN, and the call, which has returned by then, reports nothing.
+ */
+size_t newton_schulz_workspace_bytes(int32_t count, int32_t rows, int32_t cols);
+int newton_schulz(const void* const* x, int64_t ldx, int32_t x_dtype, void* const* out, int64_t ldo,
+                  int32_t out_dtype, int32_t count, int32_t rows, int32_t cols, int32_t steps, float eps,
+                  void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * ddp_bucket_allreduce_muon — the replicas' average and the optimizer step of
+ * a model's matrices, of one shape per call, in flat buffers:
+ *     g = (sum over the replicas, in rank order) / N,  buf = momentum*buf + g,
+ *     U = g + momentum*buf (nesterov) or buf,
+ *     param = param*(1 - lr*weight_decay) - lr*update_scale*newton_schulz(U)
+ *   replicas       host array of n_replicas (1 .. 16) device pointers, dtype
+ *   offsets        host int64[count]: first element of each [rows, cols]
+ *                  matrix (row-major, no gaps) in every buffer, as
+ *                  ddp_plan_buckets lays tensors out; matrices do not overlap
+ *   param, momentum_buf   device float, updated in place.  A new momentum_buf
+ *                  holds zeros
+ *   param_bf16     device bf16 or NULL: the updated parameters, rounded
+ *   update_scale   what the update's size is to depend on beside lr, e.g.
+ *                  sqrt(max(1, rows/cols)) or 0.2*sqrt(max(rows, cols))
+ *   steps, eps, workspace   as newton_schulz
+ * Base pointers are 16-byte aligned; matrices whose offsets are multiples of 4
+ * run fastest.  Elements between the matrices are left alone.
+ * The buffers' ranges that hold the matrices must not overlap one another.
+ */
+int ddp_bucket_allreduce_muon(const void* const* replicas, int32_t n_replicas, int32_t dtype,
+                              const int64_t* offsets, int32_t count, int32_t rows, int32_t cols, float* param,
+                              float* momentum_buf, float lr, float momentum, float weight_decay, float update_scale,
+                              int32_t nesterov, int32_t steps, float eps, void* param_bf16, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
 /* Human-readable name of a ddp_status value (static string). */
 const char* ddp_status_string(int status);
 

@@ -129,3 +129,67 @@ def test_sizes_past_32_bits_are_refused(g):
         with pytest.raises(g.DdpError) as e:
             call()
         assert e.value.status == g.DDP_ERR_UNSUPPORTED
+
+
+def test_newton_schulz(g):
+    import ctypes
+    need = g.newton_schulz_workspace_bytes(2, 64, 100)
+    f = g.newton_schulz_workspace_bytes
+    assert need > 0 and f(-1, 4, 4) == f(1, -1, 4) == f(1, 4, -1) == f(1, 65537, 4) == f(1, 4, 65537) == 0
+    assert f(0, 4, 4) == 16 and f(64, 8, 8) == f(1000, 8, 8)
+
+    def ptrs(*a):
+        return (ctypes.c_void_p * len(a))(*a)
+    call = caller(g.lib_handle().newton_schulz, x=ptrs(at(0), at(1)), ldx=100, xdt=0, out=ptrs(at(2), at(3)), ldo=100, odt=1,
+                  count=2, rows=64, cols=100, steps=5, eps=1e-7, ws=at(5), wsb=need)
+    assert call(count=0) == g.DDP_OK and call(rows=0) == g.DDP_OK and call(cols=0, x=None, out=None, ws=None) == g.DDP_OK
+    for bad in (dict(x=None), dict(out=None), dict(ws=None), dict(xdt=2), dict(odt=-1), dict(count=-1), dict(rows=-1),
+                dict(cols=-1), dict(steps=0), dict(steps=17), dict(eps=-1.0), dict(eps=float("nan")), dict(eps=float("inf")),
+                dict(ldx=99), dict(ldo=99), dict(x=ptrs(at(0), None)), dict(out=ptrs(None, at(3))),
+                dict(out=ptrs(at(2), at(2) + 16)), dict(out=ptrs(at(0), at(3))), dict(out=ptrs(at(1), at(3)), odt=0),
+                dict(ws=at(0)), dict(ws=at(3))):
+        assert call(**bad) == g.DDP_ERR_INVALID_ARG, bad
+    assert call(x=ptrs(at(0) + 2, at(1))) == g.DDP_ERR_ALIGNMENT and call(ws=at(5) + 8) == g.DDP_ERR_ALIGNMENT
+    assert call(wsb=need - 1) == g.DDP_ERR_CAPACITY and call(rows=65537) == g.DDP_ERR_UNSUPPORTED
+
+
+def test_muon(g):
+    import ctypes
+    need = g.newton_schulz_workspace_bytes(2, 8, 16)
+    reps = (ctypes.c_void_p * 2)(at(0), at(1))
+
+    def offs(*a):
+        return (ctypes.c_int64 * len(a))(*a)
+    call = caller(g.lib_handle().ddp_bucket_allreduce_muon, r=reps, n=2, dt=1, off=offs(0, 128), count=2, rows=8, cols=16,
+                  p=at(2), b=at(3), lr=0.1, mu=0.9, wd=0.0, scale=1.0, nest=1, steps=5, eps=1e-7, half=at(4), ws=at(5), wsb=need)
+    assert call(count=0) == g.DDP_OK and call(rows=0, r=None, off=None, p=None, b=None, ws=None) == g.DDP_OK
+    for bad in (dict(r=None), dict(off=None), dict(p=None), dict(b=None), dict(ws=None), dict(n=0), dict(n=17), dict(dt=3),
+                dict(count=-1), dict(rows=-1), dict(steps=0), dict(steps=99), dict(eps=float("nan")), dict(off=offs(0, 127)),
+                dict(off=offs(-1, 128)), dict(off=offs(0, 1 << 62)), dict(p=at(0)), dict(b=at(2)), dict(half=at(3)),
+                dict(ws=at(1)), dict(p=at(5)), dict(r=(ctypes.c_void_p * 2)(at(0), None))):
+        assert call(**bad) == g.DDP_ERR_INVALID_ARG, bad
+    for bad in (dict(p=at(2) + 4), dict(b=at(3) + 8), dict(half=at(4) + 2), dict(ws=at(5) + 8),
+                dict(r=(ctypes.c_void_p * 2)(at(0), at(1) + 2))):
+        assert call(**bad) == g.DDP_ERR_ALIGNMENT, bad
+    assert call(wsb=need - 1) == g.DDP_ERR_CAPACITY and call(rows=8, cols=65537) == g.DDP_ERR_UNSUPPORTED
+
+
+def test_muon_binding(g):
+    x, ws = torch.zeros(4, 8), torch.zeros(16)
+    flat = torch.zeros(64)
+    for error, call in (
+            (ValueError, lambda: g.newton_schulz([x], [], ws, stream=0)),
+            (ValueError, lambda: g.newton_schulz([x, torch.zeros(4, 9)[:, :8]], [x, x], ws, stream=0)),
+            (ValueError, lambda: g.newton_schulz([x], [torch.zeros(8, 4)], ws, stream=0)),
+            (TypeError, lambda: g.newton_schulz([x, x.bfloat16()], [x, x], ws, stream=0)),
+            (TypeError, lambda: g.newton_schulz([x.double()], [x], ws, stream=0)),
+            (ValueError, lambda: g.ddp_bucket_allreduce_muon([], [0], 4, 8, flat, flat, ws, 0.1, 0.9, 0.0, stream=0)),
+            (ValueError, lambda: g.ddp_bucket_allreduce_muon([flat], [33], 4, 8, flat, flat, ws, 0.1, 0.9, 0.0, stream=0)),
+            (ValueError, lambda: g.ddp_bucket_allreduce_muon([flat], [0], 4, 8, flat[:31], flat, ws, 0.1, 0.9, 0.0, stream=0)),
+            (TypeError, lambda: g.ddp_bucket_allreduce_muon([flat], [0], 4, 8, flat.bfloat16(), flat, ws, 0.1, 0.9, 0.0, stream=0)),
+            (TypeError, lambda: g.ddp_bucket_allreduce_muon([flat, flat.bfloat16()], [0], 4, 8, flat, flat, ws, 0.1, 0.9, 0.0,
+                                                            stream=0)),
+            (g.DdpError, lambda: g.newton_schulz([x], [x], ws, steps=0, stream=0))):
+        with pytest.raises(error):
+            call()
+    assert g.newton_schulz_workspace_bytes(1, 2 ** 32 + 4, 4) == 0
