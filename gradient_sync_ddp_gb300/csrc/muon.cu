@@ -19,20 +19,26 @@
 // without the second number 1.2e-3, 3.4e-3 and 2e-2.
 //
 // Matrices of one shape run together, so that a step of many small ones fills
-// the GPU.  A and B are symmetric: tiles on and above the diagonal are
-// computed and stored twice, the second time transposed, 3mn·m + m³ operations
-// per step instead of 4mn·m + 2m³.
+// the GPU.  A and B are symmetric: only tiles on and above the diagonal are
+// computed, 3mn·m + m³ operations per step instead of 4mn·m + 2m³.
 //   update_kernel / square_kernel   average, momentum, U; parts of ‖U‖²
 //   split_kernel   ‖U‖ from its parts, U to fp16 (and the rest), transposed where tall
-//   step_kernel    persistent tcgen05 tiles, 3 launches per step (Gram matrix,
-//                  polynomial, product with X; the last one writes the result): a pair of
-//                  CTAs per tile of 256 x 256, or a CTA per tile of 128 x 128 where pairs would leave
-//                  SMs without work.  Roles by warp: a TMA producer (64 of K a stage, 128-byte
-//                  swizzle, six stages), an issuer of tcgen05.mma, eight
-//                  epilogue warps; two accumulators in TMEM, so that a tile's
-//                  epilogue runs under the next one's products.
+//   step_kernel    all products of all steps, persistent: a pair of CTAs per tile of
+//                  256 x 256, or a CTA per tile of 128 x 128 where pairs would leave
+//                  SMs without work.  Roles by warp: a producer that takes the next tile's number,
+//                  waits until the rows it needs of the product before are whole, and loads by TMA (64
+//                  of K a stage, 128-byte swizzle, five stages); an issuer of tcgen05.mma; sixteen
+//                  epilogue warps.  Two accumulators in TMEM, so that a tile's epilogue
+//                  runs under the next one's products.  A symmetric matrix's tiles are
+//                  stored a second time, transposed in shared memory, below the diagonal: read by
+//                  columns instead (the MMA's other operand order) a block of 64 of K took 880
+//                  clocks in place of 520.  X is read so in the last product (610), for a
+//                  transposed copy of it would not fit L2 beside the rest.
+// Tiles are taken in the order of their products by CTAs that already run, so that
+// what a tile waits for is always under way, however few CTAs the GPU has room for.
 // Every wait on a barrier is bounded; a tile whose wait ran out is written as NaN.
 #include <algorithm>
+#include <cmath>
 #include <cstdint>
 
 #include <cuda_fp16.h>
@@ -48,7 +54,7 @@ constexpr int kMaxSide = 65536;
 constexpr int kMaxSteps = 16;
 constexpr int kPad = 64;               // sides are padded to blocks of K
 constexpr int kParts = 1024;           // of a matrix's ‖U‖², at most
-constexpr int kPartElems = 8192;       // a part has at least so many elements
+constexpr int kPartElems = 2048;       // a part has at least so many elements
 constexpr int kMaxReplicas = 16;
 
 // ---- average, momentum, sums of squares ------------------------------------
@@ -138,6 +144,8 @@ struct SplitParams {
     int64_t ldx, pitch;
     const float* part;
     float* alpha;            // [count]: 1 / ((‖U‖ + eps)·scale)
+    int* sync;               // step_kernel's, set to 0
+    int32_t sync_ints;
     __half* hi;              // [count][mp][np]
     __half* lo;              // or NULL
     int64_t size;
@@ -203,7 +211,10 @@ __global__ void __launch_bounds__(kThreads) split_kernel(const __grid_constant__
         scale = want < 0x1p126f ? exp2f(floorf(log2f(fmaxf(want, 0x1p-126f)))) : norm > 0.0f ? 0x1p126f : 1.0f;
         alpha = norm > 0.0f ? 1.0f / (norm + p.eps) / scale : 0.0f;
     }
-    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) p.alpha[b] = alpha;
+    if (blockIdx.x == 0 && blockIdx.y == 0) {
+        if (threadIdx.x == 0) p.alpha[b] = alpha;
+        for (int i = b * kThreads + threadIdx.x; i < p.sync_ints; i += gridDim.z * kThreads) p.sync[i] = 0;
+    }
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
         const float s = v[k] * scale;
@@ -234,34 +245,41 @@ __global__ void __launch_bounds__(kThreads) split_kernel(const __grid_constant__
 
 constexpr int kBlockK = 64;            // a row of 128 bytes
 constexpr int kRows = 128;             // rows of either operand that a CTA holds
-constexpr int kOperandBytes = kRows * 128, kStageBytes = 2 * kOperandBytes, kStages = 6;
-constexpr int kStepThreads = 384;      // 4 warps of single roles, 8 of the epilogue
-constexpr size_t kStepSmem = kStages * kStageBytes + 1024;   // more than half of an SM's: a CTA takes all of its TMEM
+constexpr int kOperandBytes = kRows * 128, kStageBytes = 2 * kOperandBytes, kStages = 5;
+constexpr int kEpilogueWarps = 16;     // four for each quarter of the rows
+constexpr int kStepThreads = 128 + 32 * kEpilogueWarps;   // and four of single roles
+constexpr int kWarpBytes = 2 * 32 * 64;   // twice 64 bytes of a warp's 32 rows in shared memory at a time
+// more than half of an SM's shared memory: a CTA takes all of its SM's TMEM
+constexpr size_t kStepSmem = kStages * kStageBytes + kEpilogueWarps * kWarpBytes + 1024;
+constexpr int kItems = 4;              // tiles on their way from the producer to the other roles
 
-enum { kGram = 0, kPoly = 1, kApply = 2, kLast = 3 };
+enum { kGram = 0, kPoly = 1, kApply = 2 };
 enum { kOutF32 = 0, kOutBf16 = 1, kOutParam = 2 };
 
 struct StepParams {
-    CUtensorMap ta, tb;
-    const float* alpha;       // of the first step, or NULL: 1
-    const __half* e_hi;       // kPoly: A; kApply and kLast: X
-    const __half* e_lo;       // or NULL
-    __half* o_hi;             // kGram: A; kPoly: B; kApply: X
-    __half* o_lo;             // or NULL
-    void* out[kGroup];        // kLast: results, or parameters
+    CUtensorMap xk[2], xn[2], ak, bk;   // X by rows (K-major boxes) and by columns, A and B by rows
+    const float* alpha;
+    __half* x[2];
+    __half* lo;
+    __half* a;
+    __half* b;
+    int* sync;                // the next tile's number, then the tiles done of each product, matrix and tile row
+    void* out[kGroup];        // results, or parameters
     void* out2[kGroup];       // parameters in bf16
     int64_t ldo;
     float decay, step;        // kOutParam
-    float shift, ca, cb;      // of this step: A − shift·I, (a, b) of the polynomial of it
     int32_t kind, tall, vec, has2;
-    int32_t m, n, mp, ld, cols;   // ld, cols: of what is read and written here (mp, or the padded n)
-    int32_t blocks, tm, tn, per, pieces;
+    int32_t m, n, mp, np, count, steps;
+    int32_t tm, tn, sym, full;   // tiles of a matrix: rows, columns, on and above the diagonal, all of X's
 };
 
 struct StepShared {
     uint64_t ready[kStages];   // of the first CTA: both CTAs' operands are in shared memory
     uint64_t done[kStages];    // a stage's MMAs: it may be overwritten
     uint64_t d_full[2], d_empty[2], idle;
+    uint64_t item_full[kItems], item_empty[kItems];   // item_empty: of the first CTA
+    int item[kItems];
+    int warps_done[4];         // of the epilogue's, with a tile
     uint32_t tmem;
     volatile int failed;
 };
@@ -288,22 +306,31 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
     else asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// The same operand by columns: 64 of them, 128 bytes, in each of the block's 64 rows of K (128-byte swizzle), the next
+// An operand by columns: 64 of them, 128 bytes, in each of the block's 64 rows of K (128-byte swizzle), the next
 // 64 columns 8 KB on; groups of 8 rows 1024 bytes apart.
 __device__ __forceinline__ uint64_t smem_desc_columns(uint32_t addr) {
     return static_cast<uint64_t>((addr >> 4) & 0x3fff) | (512ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
 }
 
-// The u-th tile: matrix, tile row and column; on and above the diagonal of a symmetric result.
-struct Tile {
-    int b, i, j;
+// The u-th tile of all steps: step, product, matrix, tile row and column.  Tiles go by product, then by matrix; the Gram
+// matrix's by columns and the others by rows, so that a product's first tiles need the first rows of the one before.
+struct Item {
+    int step, mode, b, i, j;
 };
-template <int MODE>
-__device__ __forceinline__ Tile tile_of(const StepParams& p, int u) {
-    Tile t;
-    t.b = u / p.per;
-    int r = u - t.b * p.per;
-    if constexpr (MODE == kGram || MODE == kPoly) {
+__device__ __forceinline__ Item item_of(const StepParams& p, int u) {
+    Item t;
+    const int sym = p.sym * p.count, all = 2 * sym + p.full * p.count;
+    t.step = u / all;
+    int r = u - t.step * all;
+    t.mode = r < sym ? kGram : r < 2 * sym ? kPoly : kApply;
+    r -= t.mode * sym;
+    const int per = t.mode == kApply ? p.full : p.sym;
+    t.b = r / per;
+    r -= t.b * per;
+    if (t.mode == kApply) {
+        t.i = r / p.tn;
+        t.j = r - t.i * p.tn;
+    } else if (t.mode == kPoly) {
         t.i = 0;
         for (int w = p.tm; r >= w; --w) {
             r -= w;
@@ -311,77 +338,197 @@ __device__ __forceinline__ Tile tile_of(const StepParams& p, int u) {
         }
         t.j = t.i + r;
     } else {
-        t.i = r % p.tm;
-        t.j = r / p.tm;
+        t.j = 0;
+        for (int w = 1; r >= w; ++w) {
+            r -= w;
+            ++t.j;
+        }
+        t.i = r;
     }
     return t;
 }
+// Once A is near I: of A' = A − I, aI + B = (a + b + c)I + (b + 2c)A' + cA'², and X ← (aI + B)·X.
+__device__ __forceinline__ bool near_one(const StepParams& p, int step) { return step >= max(p.steps - 2, 2); }
+// X's second half goes into the steps but the last two.
+__device__ __forceinline__ bool has_rest(const StepParams& p, int step) { return step < p.steps - 2; }
 
-__device__ __forceinline__ float2 half_pair(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2*>(&v)); }
+// CTAs done with tiles of row i of a product.  A tile of a symmetric one counts for its row and for its column.
+__device__ __forceinline__ int* done_of(const StepParams& p, int step, int mode, int b, int i) {
+    return p.sync + 1 + ((step * 3 + mode) * p.count + b) * p.tm + i;
+}
+__device__ __forceinline__ bool wait_count(const int* c, int want, StepShared& s) {
+    const long long t0 = clock64();
+    for (;;) {
+        int v;
+        asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(c) : "memory");
+        if (v >= want) return true;
+        if (s.failed) return false;
+        if (clock64() - t0 > kWaitClocks) {
+            s.failed = 1;
+            return false;
+        }
+    }
+}
+// Waits until the rows that the tile reads of the product before are whole: X's rows i and j for the Gram matrix, A's
+// for the polynomial, B's row i for the product with X (and then all of X: B's row i took all of A, which took
+// all of X).  The same waits keep a tile from overwriting what an earlier product still reads: whoever read the
+// old A (i, j), B (i, j) or X was part of what is waited for.  Tiles are taken in order by CTAs that run, so what is
+// waited for is under way, whatever else holds the GPU.
+template <int ARRIVALS>
+__device__ __forceinline__ bool wait_before(const StepParams& p, const Item& t, StepShared& s) {
+    if (t.step == 0 && t.mode == kGram) return true;
+    const int step = t.mode == kGram ? t.step - 1 : t.step, mode = t.mode == kGram ? kApply : t.mode - 1;
+    const int want = (t.mode == kGram ? p.tn : p.tm) * ARRIVALS;
+    if (!wait_count(done_of(p, step, mode, t.b, t.i), want, s)) return false;
+    return t.mode == kApply || t.i == t.j || wait_count(done_of(p, step, mode, t.b, t.j), want, s);
+}
+// The next tile's number, for as long as tiles come, whether or not a wait has run out before.
+template <bool PAIR>
+__device__ __forceinline__ int next_item(StepShared& s, const Ring& r) {
+    const long long t0 = clock64();
+    while (!bar_poll_pair(&s.item_full[r.i], r.ph)) {
+        if (clock64() - t0 > 2 * kWaitClocks) {
+            s.failed = 1;
+            return -1;
+        }
+    }
+    return *static_cast<volatile int*>(&s.item[r.i]);
+}
+template <bool PAIR>
+__device__ __forceinline__ void item_taken(StepShared& s, const Ring& r) {
+    if constexpr (PAIR)
+        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(first_of_pair(&s.item_empty[r.i])) : "memory");
+    else bar_arrive(&s.item_empty[r.i]);
+}
+template <bool PAIR>
+__device__ __forceinline__ void publish_item(StepShared& s, const Ring& r, int u) {
+    s.item[r.i] = u;
+    if constexpr (PAIR) {
+        uint32_t v, b;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, 1;" : "=r"(v) : "r"(smem_u32(&s.item[r.i])));
+        asm volatile("mapa.shared::cluster.u32 %0, %1, 1;" : "=r"(b) : "r"(smem_u32(&s.item_full[r.i])));
+        asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(v), "r"(u) : "memory");
+        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(b) : "memory");
+    }
+    bar_arrive(&s.item_full[r.i]);
+}
+
+// Two fp16 values of a word as a pair of fp32 ones, and back (rounded).
+__device__ __forceinline__ uint64_t half_pair2(uint32_t v) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v));
+    return pair(f.x, f.y);
+}
+__device__ __forceinline__ uint32_t half_bits2(uint64_t v) {
+    float a, b;
+    unpair(v, a, b);
+    const __half2 x = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&x);
+}
 __device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
-// Sixteen columns of a result's row (of a column, where tall) to where the caller keeps them.
-__device__ __forceinline__ void write_out(const StepParams& p, int b, int row, int col, const float (&v)[16]) {
-    if (row >= p.m) return;
-    const int cols = min(16, p.n - col);
-    const int64_t at = p.tall ? static_cast<int64_t>(col) * p.ldo + row : static_cast<int64_t>(row) * p.ldo + col, by = p.tall ? p.ldo : 1;
-    if (p.kind == kOutBf16) {
-        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out[b]) + at;
-        if (!p.tall && p.vec && cols == 16) {
-            reinterpret_cast<uint4*>(o)[0] = make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
-            reinterpret_cast<uint4*>(o)[1] = make_uint4(pack2(v[8], v[9]), pack2(v[10], v[11]), pack2(v[12], v[13]), pack2(v[14], v[15]));
-            return;
+// A warp's 32 rows of 64 bytes in shared memory, the 16-byte pieces of a row exchanged by its number, so that neither a
+// lane per row nor rows across lanes collide.
+__device__ __forceinline__ uint32_t piece(uint32_t w, int row, int c) { return w + row * 64 + ((c ^ ((row >> 1) & 3)) << 4); }
+__device__ __forceinline__ void copy16(uint32_t to, const void* p) {   // by L2: what other SMs have written since this one last read it
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(p) : "memory");
+}
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+__device__ __forceinline__ void sts2(uint32_t a, uint32_t v) { asm volatile("st.shared.u16 [%0], %1;" ::"r"(a), "h"(static_cast<unsigned short>(v)) : "memory"); }
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts16(uint32_t a, const uint4& v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// The warp's 32 x 16 results (in `w`, in 32 bits) from row row0 and column col0 on to where the caller keeps them.
+__device__ __forceinline__ void write_rows(const StepParams& p, uint32_t w, int b, int row0, int col0) {
+    const int lane = threadIdx.x & 31;
+    float* o = static_cast<float*>(p.out[b]);
+    __nv_bfloat16* h = static_cast<__nv_bfloat16*>(p.kind == kOutBf16 ? p.out[b] : p.out2[b]);
+    const bool bf = p.kind == kOutBf16 || p.has2;
+    if (p.vec) {
+        const int c = lane & 3, col = col0 + 4 * c;
+        float4 t[4];
+        if (p.kind == kOutParam) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int row = row0 + 8 * k + (lane >> 2);
+                if (row < p.m && col < p.n) t[k] = *reinterpret_cast<const float4*>(o + row * p.ldo + col);
+            }
         }
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-            if (e < cols) o[e * by] = __float2bfloat16_rn(v[e]);
+        for (int k = 0; k < 4; ++k) {
+            const int r = 8 * k + (lane >> 2), row = row0 + r;
+            if (row >= p.m || col >= p.n) continue;
+            const uint4 x = lds16(piece(w, r, c));
+            float4 v = make_float4(__uint_as_float(x.x), __uint_as_float(x.y), __uint_as_float(x.z), __uint_as_float(x.w));
+            if (p.kind == kOutParam) {
+                v.x = fmaf(-p.step, v.x, t[k].x * p.decay);
+                v.y = fmaf(-p.step, v.y, t[k].y * p.decay);
+                v.z = fmaf(-p.step, v.z, t[k].z * p.decay);
+                v.w = fmaf(-p.step, v.w, t[k].w * p.decay);
+            }
+            const int64_t at = row * p.ldo + col;
+            if (p.kind != kOutBf16) *reinterpret_cast<float4*>(o + at) = v;
+            if (bf) *reinterpret_cast<uint2*>(h + at) = make_uint2(pack2(v.x, v.y), pack2(v.z, v.w));
+        }
         return;
     }
-    float* o = static_cast<float*>(p.out[b]) + at;
-    float w[16];
-    const bool whole = !p.tall && p.vec && cols == 16;
-    if (p.kind == kOutParam) {
-        if (whole) {
+    const int e = lane & 15, col = col0 + e;
+#pragma unroll 1
+    for (int r0 = 0; r0 < 32; r0 += 16) {
+        float t[8];
+        if (p.kind == kOutParam) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const float4 t = reinterpret_cast<const float4*>(o)[q];
-                w[4 * q] = t.x;
-                w[4 * q + 1] = t.y;
-                w[4 * q + 2] = t.z;
-                w[4 * q + 3] = t.w;
+            for (int k = 0; k < 8; ++k) {
+                const int row = row0 + r0 + 2 * k + (lane >> 4);
+                if (row < p.m && col < p.n) t[k] = o[row * p.ldo + col];
             }
-        } else {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) w[e] = e < cols ? o[e * by] : 0.0f;
         }
 #pragma unroll
-        for (int e = 0; e < 16; ++e) w[e] = fmaf(-p.step, v[e], w[e] * p.decay);
-    } else {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) w[e] = v[e];
+        for (int k = 0; k < 8; ++k) {
+            const int r = r0 + 2 * k + (lane >> 4), row = row0 + r;
+            if (row >= p.m || col >= p.n) continue;
+            float v;
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(piece(w, r, e >> 2) + 4 * (e & 3)) : "memory");
+            if (p.kind == kOutParam) v = fmaf(-p.step, v, t[k] * p.decay);
+            const int64_t at = row * p.ldo + col;
+            if (p.kind != kOutBf16) o[at] = v;
+            if (bf) h[at] = __float2bfloat16_rn(v);
+        }
     }
-    if (whole) {
+}
+// Eight columns of a lane's row where the result is the transpose: a column's rows lie side by side.
+__device__ __forceinline__ void write_columns(const StepParams& p, int b, int row, int col0, const float* v) {
+    if (row >= p.m) return;
+    float* o = static_cast<float*>(p.out[b]);
+    __nv_bfloat16* h = static_cast<__nv_bfloat16*>(p.kind == kOutBf16 ? p.out[b] : p.out2[b]);
+    const bool bf = p.kind == kOutBf16 || p.has2;
+    float t[8];
+    if (p.kind == kOutParam) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) reinterpret_cast<float4*>(o)[q] = make_float4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
-    } else {
-#pragma unroll
-        for (int e = 0; e < 16; ++e)
-            if (e < cols) o[e * by] = w[e];
+        for (int e = 0; e < 8; ++e)
+            if (col0 + e < p.n) t[e] = o[(col0 + e) * p.ldo + row];
     }
-    if (p.has2) {
-        __nv_bfloat16* c = static_cast<__nv_bfloat16*>(p.out2[b]) + at;
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-            if (e < cols) c[e * by] = __float2bfloat16_rn(w[e]);
+    for (int e = 0; e < 8; ++e) {
+        if (col0 + e >= p.n) break;
+        const float x = p.kind == kOutParam ? fmaf(-p.step, v[e], t[e] * p.decay) : v[e];
+        const int64_t at = (col0 + e) * p.ldo + row;
+        if (p.kind != kOutBf16) o[at] = x;
+        if (bf) h[at] = __float2bfloat16_rn(x);
     }
 }
 
-template <int MODE, bool PAIR>
+template <bool PAIR>
 __global__ void __launch_bounds__(kStepThreads, 1) step_kernel(const __grid_constant__ StepParams p) {
     extern __shared__ unsigned char raw[];
     __shared__ StepShared s;
     constexpr int SIDE = PAIR ? 256 : 128;               // of a tile
-    constexpr int ARRIVALS = PAIR ? 16 : 8;
+    constexpr int ARRIVALS = PAIR ? 2 * kEpilogueWarps : kEpilogueWarps;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = PAIR ? blockIdx.x & 1 : 0;
     const uint32_t pad = (1024u - (smem_u32(raw) & 1023u)) & 1023u;
@@ -395,7 +542,12 @@ __global__ void __launch_bounds__(kStepThreads, 1) step_kernel(const __grid_cons
             bar_init(&s.d_full[i], 1);
             bar_init(&s.d_empty[i], ARRIVALS);
         }
+        for (int i = 0; i < kItems; ++i) {
+            bar_init(&s.item_full[i], 1);
+            bar_init(&s.item_empty[i], PAIR ? 2 * kEpilogueWarps + 2 : kEpilogueWarps + 1);   // the issuer, the other producer
+        }
         bar_init(&s.idle, 1);
+        for (int i = 0; i < 4; ++i) s.warps_done[i] = 0;
         s.failed = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -417,17 +569,34 @@ __global__ void __launch_bounds__(kStepThreads, 1) step_kernel(const __grid_cons
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // every thread waits itself: what the launches before wrote is visible to a thread that has waited, and to no other
     pdl_wait();
-    const int first = PAIR ? blockIdx.x >> 1 : blockIdx.x, step = PAIR ? gridDim.x >> 1 : gridDim.x;
+    const int total = p.steps * p.count * (2 * p.sym + p.full);
 
     if (warp == 0 && lane == 0) {                        // producer
-        Ring r;
+        Ring r, q;
         int issued = 0;
         bool ok = true;
-        for (int u = first; u < p.pieces && ok; u += step) {
-            const Tile t = tile_of<MODE>(p, u);
-            const int ya = t.b * p.mp + t.i * SIDE + rank * kRows;
-            const int jb = t.j * SIDE + rank * kRows;
-            for (int k = 0; k < p.blocks; ++k) {
+        for (;;) {
+            int u;
+            if (rank == 0) {
+                u = atomicAdd(p.sync, 1);
+                if (u >= total) u = -1;
+                // one thread per tile looks at the counters (with the epilogue's looking too, counting took longer than
+                // launches), and tells the others that all is there by telling them the tile
+                if (u >= 0 && ok) ok = wait_before<PAIR ? 2 : 1>(p, item_of(p, u), s);
+                bar_drain(&s.item_empty[q.i], q.ph ^ 1, s);
+                publish_item<PAIR>(s, q, u);
+            } else {
+                u = next_item<PAIR>(s, q);
+                item_taken<PAIR>(s, q);
+            }
+            q.next(kItems);
+            if (u < 0) break;
+            const Item t = item_of(p, u);
+            if (!ok) continue;                           // tiles go on, as NaN
+            asm volatile("fence.proxy.async.global;" ::: "memory");        // written through the generic proxy
+            const int row0 = t.b * p.mp, ra = t.i * SIDE + rank * kRows, rb = t.j * SIDE + rank * kRows, from = t.step & 1;
+            const int blocks = (t.mode == kGram ? p.np : p.mp) / kBlockK;
+            for (int k = 0; k < blocks; ++k) {
                 if (!(ok = bar_wait(&s.done[r.i], r.ph ^ 1, s))) break;
                 unsigned char* d = ring + r.i * kStageBytes;
                 if (rank == 0) bar_expect(&s.ready[r.i], (PAIR ? 2 : 1) * kStageBytes);
@@ -435,13 +604,14 @@ __global__ void __launch_bounds__(kStepThreads, 1) step_kernel(const __grid_cons
                     if constexpr (PAIR) tma_load_pair(to, map, x, y, first_of_pair(&s.ready[r.i]));
                     else tma_load(to, map, x, y, &s.ready[r.i]);
                 };
-                load(d, &p.ta, k * kBlockK, ya);
-                if constexpr (MODE == kGram || MODE == kPoly) {
-                    load(d + kOperandBytes, &p.tb, k * kBlockK, t.b * p.mp + jb);
-                } else {
-                    load(d + kOperandBytes, &p.tb, jb, t.b * p.mp + k * kBlockK);
-                    load(d + kOperandBytes + kOperandBytes / 2, &p.tb, jb + 64, t.b * p.mp + k * kBlockK);
-                }
+                auto by_rows = [&](unsigned char* to, const CUtensorMap* map, int row) { load(to, map, k * kBlockK, row0 + row); };
+                auto by_columns = [&](unsigned char* to, const CUtensorMap* map, int col) {
+                    load(to, map, col, row0 + k * kBlockK);
+                    load(to + kOperandBytes / 2, map, col + 64, row0 + k * kBlockK);
+                };
+                by_rows(d, t.mode == kGram ? &p.xk[from] : t.mode == kPoly ? &p.ak : &p.bk, ra);
+                if (t.mode == kApply) by_columns(d + kOperandBytes, &p.xn[from], rb);
+                else by_rows(d + kOperandBytes, t.mode == kGram ? &p.xk[from] : &p.ak, rb);
                 r.next(kStages);
                 ++issued;
             }
@@ -452,25 +622,33 @@ __global__ void __launch_bounds__(kStepThreads, 1) step_kernel(const __grid_cons
             bar_drain(&s.done[r.i], r.ph, s);
         }
     } else if (warp == 1 && rank == 0) {                 // issuer: the whole warp, so that descriptors stay in uniform registers
-        Ring x, d;
-        constexpr uint32_t idesc = (1u << 4) | (MODE == kGram || MODE == kPoly ? 0u : 1u << 16) |
-                                   (static_cast<uint32_t>(SIDE / 8) << 17) | (static_cast<uint32_t>(SIDE / 16) << 24);
+        Ring x, d, q;
+        constexpr uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(SIDE / 8) << 17) | (static_cast<uint32_t>(SIDE / 16) << 24);
         const bool one = elect();
         bool ok = true, there = false;
-        for (int u = first; u < p.pieces && ok; u += step) {
-            if (!(ok = __all_sync(0xffffffffu, bar_wait(&s.d_empty[d.i], d.ph ^ 1, s)))) break;
+        for (;;) {
+            const int u = __shfl_sync(0xffffffffu, next_item<PAIR>(s, q), 0);
+            __syncwarp();
+            if (lane == 0) item_taken<PAIR>(s, q);
+            q.next(kItems);
+            if (__any_sync(0xffffffffu, u < 0)) break;
+            if (!ok || !(ok = __all_sync(0xffffffffu, bar_wait(&s.d_empty[d.i], d.ph ^ 1, s)))) continue;
             fence_after();
+            // votes, so that what follows from the tile's number is known to be the warp's: registers that the MMA takes as
+            // they are (376 clocks to issue four of them without)
+            const int mode = item_of(p, u).mode;
+            const bool gram = __any_sync(0xffffffffu, mode == kGram), by_columns = __any_sync(0xffffffffu, mode == kApply);
             const uint32_t acc = d.i * SIDE;
-            for (int k = 0; k < p.blocks; ++k) {
+            const int blocks = (gram ? p.np : p.mp) / kBlockK;
+            for (int k = 0; k < blocks; ++k) {
                 if (!there && !(ok = __all_sync(0xffffffffu, bar_wait_pair(&s.ready[x.i], x.ph, s)))) break;
                 fence_after();
                 const uint32_t at = ring_addr + x.i * kStageBytes;
-                const uint64_t a = smem_desc(at);
-                const uint64_t b = MODE == kGram || MODE == kPoly ? smem_desc(at + kOperandBytes) : smem_desc_columns(at + kOperandBytes);
-                constexpr int bstep = MODE == kGram || MODE == kPoly ? 2 : 128;   // 16 of K, in 16 bytes
+                const uint64_t a = smem_desc(at), b = by_columns ? smem_desc_columns(at + kOperandBytes) : smem_desc(at + kOperandBytes);
+                const uint32_t how = by_columns ? idesc | 1u << 16 : idesc, bstep = by_columns ? 128 : 2;   // 16 of K, in 16 bytes
                 if (one) {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) mma_ss<PAIR>(acc, a + 2 * q, b + bstep * q, idesc, k > 0 || q > 0);
+                    for (int i = 0; i < 4; ++i) mma_ss<PAIR>(acc, a + 2 * i, b + bstep * i, how, k > 0 || i > 0);
                 }
                 // a look at the next stage while these run
                 Ring y = x;
@@ -487,43 +665,64 @@ __global__ void __launch_bounds__(kStepThreads, 1) step_kernel(const __grid_cons
             commit<PAIR, false>(&s.idle);
             bar_drain(&s.idle, 0, s);
         }
-    } else if (warp >= 4) {                              // epilogue: 32 rows, half of the columns
-        Ring d;
-        constexpr int COLS = SIDE / 2;
-        const int q = warp & 3, half = (warp - 4) >> 2;
-        for (int u = first; u < p.pieces; u += step) {
-            const Tile t = tile_of<MODE>(p, u);
-            const int row = t.i * SIDE + rank * kRows + q * 32 + lane;
-            const bool in = row < p.mp;
-            const float alpha = p.alpha ? p.alpha[t.b] : 1.0f;
-            const int64_t base = (static_cast<int64_t>(t.b) * p.mp + row) * p.ld;
-            const uint32_t acc = d.i * SIDE + (static_cast<uint32_t>(q * 32) << 16);
-            bool ok = true;
-            for (int c0 = 0; c0 < COLS; c0 += 64) {
-                const int col0 = t.j * SIDE + half * COLS + c0;
-                const bool cols = col0 < p.cols;         // padded to 64: all or none
-                uint4 hi[8], lo[8];
-                if constexpr (MODE != kGram) {           // fetched while the tile is still being summed
-                    if (in && cols) {
+    } else if (warp >= 4) {                              // epilogue: 32 rows, every fourth 32 columns
+        Ring d, q;
+        int tile = 0;
+        constexpr int UNITS = SIDE / 32, EVERY = kEpilogueWarps / 4;
+        const int w = warp - 4, rows = (warp & 3) * 32, lr = lane >> 2, lc = lane & 3;   // the rows that a warp reaches in TMEM
+        const uint32_t st = ring_addr + kStages * kStageBytes + w * kWarpBytes, st2 = st + kWarpBytes / 2;
+        for (;;) {
+            const int u = __shfl_sync(0xffffffffu, next_item<PAIR>(s, q), 0);
+            __syncwarp();
+            if (lane == 0) item_taken<PAIR>(s, q);
+            q.next(kItems);
+            if (u < 0) break;
+            const Item t = item_of(p, u);
+            const int row0 = t.i * SIDE + rank * kRows + rows, from = t.step & 1;
+            const bool last = t.mode == kApply && t.step == p.steps - 1;
+            const bool in = row0 < p.mp;                 // padded to 64: all 32 rows or none
+            const int ld = t.mode == kApply ? p.np : p.mp;
+            const bool e_lo = t.mode == kApply && has_rest(p, t.step), o_lo = t.mode == kApply && has_rest(p, t.step + 1);
+            const float alpha = t.step == 0 && t.mode != kPoly ? p.alpha[t.b] : 1.0f;
+            const bool near = near_one(p, t.step), below = t.mode != kApply && t.i != t.j;
+            // near I, B's diagonal has room for a: X need not be added to the product
+            const bool adds = t.mode == kPoly || (t.mode == kApply && !near);
+            const float scale = t.mode == kGram ? alpha * alpha : t.mode == kPoly ? kC : alpha;
+            const float coef = t.mode == kPoly ? (near ? kB + 2.0f * kC : kB) : alpha * kA;
+            const float shift = t.mode == kGram ? -1.0f : kA + kB + kC;   // of the diagonal, near I
+            // the lane's pieces of the warp's rows: 8k + lane / 4
+            const int64_t base = (static_cast<int64_t>(t.b) * p.mp + row0 + lr) * ld + 8 * lc;
+            const __half* e_hi = (t.mode == kPoly ? p.a : p.x[from]) + base;
+            __half* o_hi = (t.mode == kGram ? p.a : t.mode == kPoly ? p.b : p.x[from ^ 1]) + base;
+            const int64_t rows8 = 8ll * ld;
+            const uint32_t acc = d.i * SIDE + (static_cast<uint32_t>(rows) << 16);
+            // Rows across lanes in global memory, a row per lane in TMEM: through shared memory from one to the other, X and
+            // A by `st`, the rest (or the tile below the diagonal) by `st2`.
+            auto fetch = [&](int unit) {
+                const int col0 = t.j * SIDE + 32 * unit;
+                if (!adds || !in || col0 >= ld) return;
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) hi[i] = ld16_keep(p.e_hi + base + col0 + 8 * i);
-                        if (MODE != kPoly && p.e_lo) {
+                for (int k = 0; k < 4; ++k) copy16(piece(st, 8 * k + lr, lc), e_hi + k * rows8 + col0);
+                if (e_lo) {
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) lo[i] = ld16_keep(p.e_lo + base + col0 + 8 * i);
-                        }
-                    }
+                    for (int k = 0; k < 4; ++k) copy16(piece(st2, 8 * k + lr, lc), p.lo + base + k * rows8 + col0);
                 }
-                if (c0 == 0) {
-                    ok = bar_wait(&s.d_full[d.i], d.ph, s) && !s.failed;
-                    fence_after();
-                }
+            };
+            fetch(w >> 2);                               // while the tile is still being summed
+            const bool ok = bar_wait(&s.d_full[d.i], d.ph, s) && !s.failed;
+            fence_after();
+#pragma unroll 1
+            for (int unit = w >> 2; unit < UNITS; unit += EVERY) {
+                const int col0 = t.j * SIDE + 32 * unit;
+                const bool here = in && col0 < ld;       // padded to 64: all or none
+                copies_done();
                 __syncwarp();
 #pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    float v[16];
+                for (int g = 0; g < 2; ++g) {
+                    float a[16];
                     __syncwarp();
-                    tmem_ld16(acc + half * COLS + c0 + 16 * h, v);
-                    if (c0 + 64 >= COLS && h == 3) {     // the accumulator is free before its last columns are stored
+                    tmem_ld16(acc + 32 * unit + 16 * g, a);
+                    if (g == 1 && unit + EVERY >= UNITS) {   // the accumulator is free before its last columns are stored
                         fence_before();
                         __syncwarp();
                         if (lane == 0) {
@@ -531,67 +730,101 @@ __global__ void __launch_bounds__(kStepThreads, 1) step_kernel(const __grid_cons
                             else bar_arrive(&s.d_empty[d.i]);
                         }
                     }
-                    if (!in || !cols) continue;
-                    const int col = col0 + 16 * h;
+                    if (!here) continue;
                     if (!ok) {
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) v[e] = __int_as_float(0x7fffffff);
+                        for (int e = 0; e < 16; ++e) a[e] = __int_as_float(0x7fffffff);
                     }
+                    uint64_t v[8];
 #pragma unroll
-                    for (int e = 0; e < 16; e += 2) {
-                        if constexpr (MODE == kGram) {
-                            v[e] = fmaf(v[e], alpha * alpha, row == col + e ? -p.shift : 0.0f);
-                            v[e + 1] = fmaf(v[e + 1], alpha * alpha, row == col + e + 1 ? -p.shift : 0.0f);
-                        } else {
-                            float2 f = half_pair(word(hi[2 * h + e / 8], e / 2 % 4));
-                            if constexpr (MODE == kPoly) {
-                                v[e] = fmaf(kC, v[e], p.cb * f.x);
-                                v[e + 1] = fmaf(kC, v[e + 1], p.cb * f.y);
-                            } else {
-                                if (p.e_lo) {
-                                    const float2 g = half_pair(word(lo[2 * h + e / 8], e / 2 % 4));
-                                    f.x += g.x;
-                                    f.y += g.y;
-                                }
-                                v[e] = alpha * fmaf(p.ca, f.x, v[e]);
-                                v[e + 1] = alpha * fmaf(p.ca, f.y, v[e + 1]);
+                    for (int e = 0; e < 8; ++e) v[e] = pair(a[2 * e], a[2 * e + 1]);
+                    const uint64_t scale2 = pair(scale, scale), coef2 = pair(coef, coef);
+                    if (!adds) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) v[e] = mul2(v[e], scale2);
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            const uint4 x = lds16(piece(st, lane, 2 * g + c));
+                            uint64_t f[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) f[e] = half_pair2(word(x, e));
+                            if (e_lo) {
+                                const uint4 y = lds16(piece(st2, lane, 2 * g + c));
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) f[e] = add2(f[e], half_pair2(word(y, e)));
                             }
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) v[4 * c + e] = fma2(scale2, v[4 * c + e], mul2(coef2, f[e]));
                         }
                     }
-                    if constexpr (MODE == kLast) {
-                        if (col < p.n) write_out(p, t.b, row, col, v);
-                    } else {
-                        uint32_t w[8];
+                    if (near && t.mode != kApply && t.i == t.j) {
+                        const int diag = row0 + lane - col0 - 16 * g;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) v[e] = add2(v[e], pair(2 * e == diag ? shift : 0.0f, 2 * e + 1 == diag ? shift : 0.0f));
+                    }
+                    if (last) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) unpair(v[e], a[2 * e], a[2 * e + 1]);
+                        if (p.tall) {
+                            write_columns(p, t.b, row0 + lane, col0 + 16 * g, a);
+                            write_columns(p, t.b, row0 + lane, col0 + 16 * g + 8, a + 8);
+                            continue;
+                        }
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) sts16(piece(st2, lane, c), f4_bits(a[4 * c], a[4 * c + 1], a[4 * c + 2], a[4 * c + 3]));
+                        __syncwarp();
+                        write_rows(p, st2, t.b, row0, col0 + 16 * g);
+                        continue;
+                    }
+                    uint32_t x[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] = half_bits2(v[e]);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) sts16(piece(st, lane, 2 * g + c), make_uint4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]));
+                    if (o_lo) {
+                        const uint64_t minus = pair(-1.0f, -1.0f);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) x[e] = half_bits2(fma2(half_pair2(x[e]), minus, v[e]));
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) sts16(piece(st2, lane, 2 * g + c), make_uint4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]));
+                    } else if (below) {                  // transposed: the lane's row is a column of it
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
-                            const __half2 x = __floats2half2_rn(v[2 * e], v[2 * e + 1]);
-                            w[e] = *reinterpret_cast<const uint32_t*>(&x);
-                        }
-                        uint4* o = reinterpret_cast<uint4*>(p.o_hi + base + col);
-                        o[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                        o[1] = make_uint4(w[4], w[5], w[6], w[7]);
-                        if constexpr (MODE == kApply) {
-                            if (p.o_lo) {
-                                uint32_t z[8];
-#pragma unroll
-                                for (int e = 0; e < 8; ++e) {
-                                    const float2 f = half_pair(w[e]);
-                                    const __half2 x = __floats2half2_rn(v[2 * e] - f.x, v[2 * e + 1] - f.y);
-                                    z[e] = *reinterpret_cast<const uint32_t*>(&x);
-                                }
-                                uint4* ol = reinterpret_cast<uint4*>(p.o_lo + base + col);
-                                ol[0] = make_uint4(z[0], z[1], z[2], z[3]);
-                                ol[1] = make_uint4(z[4], z[5], z[6], z[7]);
-                            }
-                        } else if (t.i != t.j) {         // the tile below the diagonal
-                            unsigned short* m = reinterpret_cast<unsigned short*>(p.o_hi) + (static_cast<int64_t>(t.b) * p.mp + col) * p.ld + row;
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) m[static_cast<int64_t>(e) * p.ld] = static_cast<unsigned short>(w[e / 2] >> (16 * (e & 1)));
+                            sts2(piece(st2, 16 * g + 2 * e, lane >> 3) + 2 * (lane & 7), x[e]);
+                            sts2(piece(st2, 16 * g + 2 * e + 1, lane >> 3) + 2 * (lane & 7), x[e] >> 16);
                         }
                     }
                 }
+                __syncwarp();
+                if (here && !last) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4*>(o_hi + k * rows8 + col0) = lds16(piece(st, 8 * k + lr, lc));
+                    if (o_lo || below) {
+                        __half* o2 = o_lo ? p.lo + base + col0
+                                          : (t.mode == kGram ? p.a : p.b) + (static_cast<int64_t>(t.b) * p.mp + col0 + lr) * ld + row0 + 8 * lc;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4*>(o2 + k * rows8) = lds16(piece(st2, 8 * k + lr, lc));
+                    }
+                }
+                __syncwarp();
+                if (unit + EVERY < UNITS) fetch(unit + EVERY);
             }
             d.next(2);
+            if (!last) {                                 // told to those that wait for the tile's rows
+                asm volatile("fence.proxy.async.global;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) {
+                    __threadfence();
+                    if (atomicAdd(&s.warps_done[tile & 3], 1) == kEpilogueWarps - 1) {   // a warp is two tiles ahead of another at most
+                        s.warps_done[tile & 3] = 0;
+                        __threadfence();
+                        atomicAdd(done_of(p, t.step, t.mode, t.b, t.i), 1);
+                        if (t.mode != kApply && t.i != t.j) atomicAdd(done_of(p, t.step, t.mode, t.b, t.j), 1);
+                    }
+                }
+            }
+            ++tile;
         }
     }
     __syncwarp();
@@ -612,7 +845,7 @@ struct Layout {
     int m, n, mp, np;
     bool tall;
     int64_t size, pitch;      // of U
-    size_t u, part, alpha, x0, x1, lo, a, b, total;
+    size_t u, part, alpha, sync, x0, x1, lo, a, b, total;
 };
 Layout layout_of(int count, int rows, int cols) {
     Layout l{};
@@ -633,6 +866,7 @@ Layout layout_of(int count, int rows, int cols) {
     l.u = take(l.pitch * 4);
     l.part = take(kParts * 4);
     l.alpha = take(4);
+    l.sync = take((3 * kMaxSteps * ((l.mp + kRows - 1) / kRows) + 1) * 4);
     l.x0 = take(x);
     l.x1 = take(x);
     l.lo = take(x);
@@ -642,26 +876,30 @@ Layout layout_of(int count, int rows, int cols) {
     return l;
 }
 
-// Tiles by pairs of CTAs or by single ones: the less time, in K blocks of a 128 x 128 tile.  A pair's 256 x 256 tile
-// takes two such times of the tensor cores, a CTA's 128 x 128 one a little more than one (its operands come at
-// twice the bytes per product).
+// Tiles by pairs of CTAs or by single ones, for all products alike: the less time, in K blocks of a 128 x 128 tile.  A
+// pair's 256 x 256 tile takes two such times of the tensor cores, a CTA's 128 x 128 one a little more than one (its
+// operands come at twice the bytes per product).  Several matrices fill each other's last waves.
 struct Tiling {
     bool pair;
-    int tm, tn, per, ctas;
+    int tm, tn, sym, full, ctas;
 };
-Tiling tiling(int count, int rows, int cols, bool symmetric, int sms) {
-    auto tiles = [&](int side) {
-        const int64_t tm = (rows + side - 1) / side, tn = (cols + side - 1) / side;
-        return symmetric ? tm * (tm + 1) / 2 : tm * tn;
-    };
-    auto waves = [](int64_t n, int at) { return (n + at - 1) / at; };
-    const int64_t two = tiles(256) * count, one = tiles(128) * count;
-    const bool pair = waves(two, sms / 2) * 20 <= waves(one, sms) * 13;
-    const int side = pair ? 256 : 128;
-    Tiling t{pair, (rows + side - 1) / side, (cols + side - 1) / side, static_cast<int>(tiles(side)), 0};
-    const int64_t n = pair ? two : one, most = pair ? sms / 2 : sms;
-    t.ctas = static_cast<int>(std::min(n, most)) * (pair ? 2 : 1);
-    return t;
+Tiling tiling(int count, const Layout& l, int sms) {
+    Tiling best{};
+    double least = 0.0;
+    for (const bool pair : {true, false}) {
+        const int side = pair ? 256 : 128, at = pair ? sms / 2 : sms;
+        const int tm = (l.mp + side - 1) / side, tn = (l.np + side - 1) / side, sym = tm * (tm + 1) / 2, full = tm * tn;
+        auto waves = [&](int tiles) {
+            const double w = static_cast<double>(tiles) * count / at;
+            return count == 1 ? std::ceil(w) : std::max(w, 1.0);
+        };
+        const double cost = (pair ? 2.0 : 1.3) * (waves(sym) * (l.np + l.mp) + waves(full) * l.mp);
+        if (pair || cost < least) {
+            least = cost;
+            best = Tiling{pair, tm, tn, sym, full, std::min(std::max(sym, full) * count, at) * (pair ? 2 : 1)};
+        }
+    }
+    return best;
 }
 
 struct Call {
@@ -681,97 +919,61 @@ struct Results {
     void* const* out2;
 };
 
-template <int MODE>
-int launch_step(const StepParams& p, const Tiling& t, cudaStream_t s) {
-    return launch_smem(t.pair ? step_kernel<MODE, true> : step_kernel<MODE, false>, static_cast<unsigned>(t.ctas), kStepThreads,
-                       kStepSmem, s, p, t.pair ? 2 : 1);
-}
-
 // The steps on a group of matrices that split_kernel has laid out.
 int run_steps(const Call& c, const Layout& l, const Results& r) {
     DeviceInfo d;
     int st = current_device_info(&d);
     if (st != DDP_OK) return st;
-    __half* x[2] = {reinterpret_cast<__half*>(c.ws + l.x0), reinterpret_cast<__half*>(c.ws + l.x1)};
-    __half* lo = reinterpret_cast<__half*>(c.ws + l.lo);
-    __half* a = reinterpret_cast<__half*>(c.ws + l.a);
-    __half* b = reinterpret_cast<__half*>(c.ws + l.b);
+    StepParams p{};
+    p.alpha = reinterpret_cast<const float*>(c.ws + l.alpha);
+    p.x[0] = reinterpret_cast<__half*>(c.ws + l.x0);
+    p.x[1] = reinterpret_cast<__half*>(c.ws + l.x1);
+    p.lo = reinterpret_cast<__half*>(c.ws + l.lo);
+    p.a = reinterpret_cast<__half*>(c.ws + l.a);
+    p.b = reinterpret_cast<__half*>(c.ws + l.b);
+    p.sync = reinterpret_cast<int*>(c.ws + l.sync);
     const int64_t all = static_cast<int64_t>(c.count) * l.mp;
     auto map = [&](CUtensorMap* t, const __half* base, int cols, int box_rows) {
         return encode(t, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, base, cols, all, static_cast<int64_t>(cols) * 2, kBlockK, box_rows,
                       CU_TENSOR_MAP_SWIZZLE_128B);
     };
-    CUtensorMap xk[2], xn[2], ak, bk;
     for (int i = 0; i < 2; ++i) {
-        if ((st = map(&xk[i], x[i], l.np, kRows)) != DDP_OK) return st;
-        if ((st = map(&xn[i], x[i], l.np, kBlockK)) != DDP_OK) return st;
+        if ((st = map(&p.xk[i], p.x[i], l.np, kRows)) != DDP_OK) return st;
+        if ((st = map(&p.xn[i], p.x[i], l.np, kBlockK)) != DDP_OK) return st;
     }
-    if ((st = map(&ak, a, l.mp, kRows)) != DDP_OK) return st;
-    if ((st = map(&bk, b, l.mp, kRows)) != DDP_OK) return st;
-    const Tiling sym = tiling(c.count, l.mp, l.mp, true, d.sm_count), full = tiling(c.count, l.mp, l.np, false, d.sm_count);
-    StepParams p{};
+    if ((st = map(&p.ak, p.a, l.mp, kRows)) != DDP_OK || (st = map(&p.bk, p.b, l.mp, kRows)) != DDP_OK) return st;
+    const Tiling t = tiling(c.count, l, d.sm_count);
+    if (static_cast<int64_t>(c.steps) * c.count * (2 * t.sym + t.full) > INT32_MAX / 2) return DDP_ERR_UNSUPPORTED;
     p.m = l.m;
     p.n = l.n;
     p.mp = l.mp;
-    auto shape = [&](const Tiling& t, int cols, int blocks) {
-        p.ld = p.cols = cols;
-        p.blocks = blocks;
-        p.tm = t.tm;
-        p.tn = t.tn;
-        p.per = t.per;
-        p.pieces = t.per * c.count;
-    };
-    for (int i = 0; i < c.steps; ++i) {
-        const int from = i & 1;
-        // once A is near I: of A' = A − I, B = (b + c)I + (b + 2c)A' + cA'²
-        const bool near = i >= std::max(c.steps - 2, 2);
-        p.shift = near ? 1.0f : 0.0f;
-        p.ca = near ? kA + kB + kC : kA;
-        p.cb = near ? kB + 2.0f * kC : kB;
-        p.alpha = i == 0 ? reinterpret_cast<const float*>(c.ws + l.alpha) : nullptr;
-        shape(sym, l.mp, l.np / kBlockK);
-        p.ta = xk[from];
-        p.tb = xk[from];
-        p.o_hi = a;
-        if ((st = launch_step<kGram>(p, sym, c.s)) != DDP_OK) return st;
-        p.alpha = nullptr;
-        shape(sym, l.mp, l.mp / kBlockK);
-        p.ta = ak;
-        p.tb = ak;
-        p.e_hi = a;
-        p.o_hi = b;
-        if ((st = launch_step<kPoly>(p, sym, c.s)) != DDP_OK) return st;
-        p.alpha = i == 0 ? reinterpret_cast<const float*>(c.ws + l.alpha) : nullptr;
-        shape(full, l.np, l.mp / kBlockK);
-        p.ta = bk;
-        p.tb = xn[from];
-        p.e_hi = x[from];
-        p.e_lo = i < c.steps - 2 ? lo : nullptr;
-        if (i + 1 < c.steps) {
-            p.o_hi = x[from ^ 1];
-            p.o_lo = i + 1 < c.steps - 2 ? lo : nullptr;
-            if ((st = launch_step<kApply>(p, full, c.s)) != DDP_OK) return st;
-        } else {
-            p.kind = r.kind;
-            p.tall = l.tall;
-            p.vec = r.vec;
-            p.has2 = r.out2 != nullptr;
-            p.ldo = r.ld;
-            p.decay = r.decay;
-            p.step = r.step;
-            for (int k = 0; k < c.count; ++k) {
-                p.out[k] = r.out[k];
-                p.out2[k] = r.out2 ? r.out2[k] : nullptr;
-            }
-            if ((st = launch_step<kLast>(p, full, c.s)) != DDP_OK) return st;
-        }
+    p.np = l.np;
+    p.count = c.count;
+    p.steps = c.steps;
+    p.tm = t.tm;
+    p.tn = t.tn;
+    p.sym = t.sym;
+    p.full = t.full;
+    p.kind = r.kind;
+    p.tall = l.tall;
+    p.vec = r.vec;
+    p.has2 = r.out2 != nullptr;
+    p.ldo = r.ld;
+    p.decay = r.decay;
+    p.step = r.step;
+    for (int k = 0; k < c.count; ++k) {
+        p.out[k] = r.out[k];
+        p.out2[k] = r.out2 ? r.out2[k] : nullptr;
     }
-    return DDP_OK;
+    return launch_smem(t.pair ? step_kernel<true> : step_kernel<false>, static_cast<unsigned>(t.ctas), kStepThreads, kStepSmem, c.s, p,
+                       t.pair ? 2 : 1);
 }
 
 int split(const Call& c, const Layout& l, SplitParams& p, bool bf16) {
     p.part = reinterpret_cast<const float*>(c.ws + l.part);
     p.alpha = reinterpret_cast<float*>(c.ws + l.alpha);
+    p.sync = reinterpret_cast<int*>(c.ws + l.sync);
+    p.sync_ints = 1 + 3 * c.steps * c.count * ((l.mp + kRows - 1) / kRows);   // at most: larger tiles have fewer rows
     p.hi = reinterpret_cast<__half*>(c.ws + l.x0);
     p.lo = c.steps > 2 ? reinterpret_cast<__half*>(c.ws + l.lo) : nullptr;
     p.size = l.size;
@@ -832,7 +1034,7 @@ extern "C" int newton_schulz(const void* const* x, int64_t ldx, int32_t x_dtype,
     const size_t need = newton_schulz_workspace_bytes(count, rows, cols);
     const Mat ws{workspace, 1, static_cast<int64_t>(need), static_cast<int64_t>(need), 1};
     const bool bf16 = x_dtype == DDP_BF16;
-    bool in_vec = cols % (bf16 ? 8 : 4) == 0, out_vec = true;
+    bool in_vec = cols % (bf16 ? 8 : 4) == 0, out_vec = cols % 4 == 0;
     for (int i = 0; i < count; ++i) {
         const Mat mx{x[i], rows, cols, ldx, dsize(x_dtype)}, mo{out[i], rows, cols, ldo, dsize(out_dtype)};
         if (!mat_valid(mx) || !mat_valid(mo) || x[i] == nullptr || out[i] == nullptr) return DDP_ERR_INVALID_ARG;

@@ -58,8 +58,8 @@ def emulate(x, steps=5, eps=1e-7):
         lo = r(full - hi) if i < steps - 2 else 0
         s = 1.0 if i >= max(steps - 2, 2) else 0.0       # of A − I
         gram = r(alpha * alpha * (hi @ hi.t()) - s * torch.eye(len(hi), dtype=torch.float64, device=hi.device))
-        poly = r((b + 2 * c * s) * gram + c * (gram @ gram))
-        full = alpha * ((a + (b + c) * s) * (hi + lo) + poly @ hi)
+        poly = r((b + 2 * c * s) * gram + c * (gram @ gram) + s * (a + b + c) * torch.eye(len(hi), dtype=torch.float64, device=hi.device))
+        full = alpha * ((1 - s) * a * (hi + lo) + poly @ hi)
         alpha = 1.0
     return full.t() if tall else full
 
