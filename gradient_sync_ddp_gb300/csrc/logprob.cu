@@ -15,15 +15,14 @@
 // GPU).  With x = (z − reference)·log2(e)/τ a thread sums 2^x and x·2^x about a
 // reference of its own that stays within 8 of its largest x, so that neither
 // sum loses what the entropy, log2(Σ2^x) − Σx2^x / Σ2^x, is the difference of.
-// Top entries: the first vectors that the threads load are spread over the row.
-// Each thread's largest logit of them is sorted within its warp; the smallest,
-// over the 8 warps, of the warps' ceil(k/8)-th largest is a bound that at least
-// k entries of the row reach.  During the rest of the pass a thread only notes
-// the vectors whose maximum reaches it.  The same bound over whole rows is
-// tighter; of the noted vectors that reach it the entries are collected (about
-// 1.5·k of them), and each one's rank among them is counted.  Where the lists
-// run over (long ties, a row whose large entries lie where few threads saw
-// them), or a short row leaves warps without entries, the k-th largest is found
+// Top entries: a thread keeps the largest maximum of its vectors, that vector, and
+// the second largest maximum, without a branch.  The threads' largest are sorted
+// within their warps; the smallest, over the warps, of the warps' ceil(k/warps)-th
+// largest is a bound that at least k entries reach (about 1.5·k do).  Vectors that
+// reach it are read again, from L2: a thread's largest by itself, all of a
+// thread's vectors by a warp where the second largest reaches it too; the entries
+// that reach it are collected and each one's rank among them is counted.  Where the list
+// runs over (long ties, a short row), and in rows with NaN, the k-th largest is found
 // by digits of (value, index), as whole numbers of 64 bits.
 #include <cstdint>
 
@@ -34,8 +33,6 @@ namespace {
 
 constexpr int kThr = kVocabThreads, kWarps = kThr / 32;
 constexpr int kMaxTop = DDP_LOGPROB_MAX_TOP;
-constexpr int kVectors = 6;          // in flight per thread
-constexpr int kHits = 2048;          // vectors noted during the pass
 constexpr int kCands = 1024;         // entries collected
 constexpr int kCount = 256;          // up to this many entries ranks are counted at once
 constexpr float kRaise = 8.0f;       // how far a thread's x may lie above its reference
@@ -89,6 +86,7 @@ __device__ __forceinline__ float vec_max(const uint4& v) {
 // A thread's sums about its reference m: x = z·c − mc, s0 = Σ 2^x, s1 = Σ x·2^x.
 struct Sums {
     float m = -INFINITY, mc = 0.0f;
+    float low = -INFINITY;            // m − 200/c: what lies below counts as this much, 2^-200 (−infinity·0 would be NaN)
     uint64_t s0 = 0, s1 = 0;          // pairs, added at the end
     bool bad = false;                 // +infinity or NaN
     __device__ __forceinline__ void raise(float to, float c) {
@@ -106,23 +104,31 @@ struct Sums {
         }
         m = to;
         mc = n;
+        low = to - 200.0f / c;
     }
     template <bool BF16>
-    __device__ __forceinline__ void add(const uint4& v, float c) {
+    __device__ __forceinline__ void add(uint4 v, float c) {
         const uint64_t c2 = pair(c, c), n2 = pair(-mc, -mc);
+        if constexpr (BF16) {
+            const uint32_t l = pack2(low, low);
+            asm("max.bf16x2 %0, %0, %1;" : "+r"(v.x) : "r"(l));
+            asm("max.bf16x2 %0, %0, %1;" : "+r"(v.y) : "r"(l));
+            asm("max.bf16x2 %0, %0, %1;" : "+r"(v.z) : "r"(l));
+            asm("max.bf16x2 %0, %0, %1;" : "+r"(v.w) : "r"(l));
+        } else {
+            v = f4_bits(fmaxf(__uint_as_float(v.x), low), fmaxf(__uint_as_float(v.y), low), fmaxf(__uint_as_float(v.z), low), fmaxf(__uint_as_float(v.w), low));
+        }
 #pragma unroll
         for (int e = 0; e < (BF16 ? 4 : 2); ++e) {
             const uint64_t x = fma2(vec_pair<BF16>(v, e), c2, n2), p = pow2_pair(x);
             s0 = add2(s0, p);
-            float lo, hi;
-            unpair(x, lo, hi);
-            s1 = fma2(pair(fmaxf(lo, -200.0f), fmaxf(hi, -200.0f)), p, s1);   // −infinity·0 would be NaN
+            s1 = fma2(x, p, s1);
         }
     }
     __device__ __forceinline__ void add_one(float z, float c) {
-        const float x = fmaf(z, c, -mc), p = pow2(x);
+        const float x = fmaf(fmaxf(z, low), c, -mc), p = pow2(x);
         s0 = add2(s0, pair(p, 0.0f));
-        s1 = fma2(pair(fmaxf(x, -200.0f), 0.0f), pair(p, 0.0f), s1);
+        s1 = fma2(pair(x, 0.0f), pair(p, 0.0f), s1);
     }
 };
 
@@ -144,20 +150,23 @@ __device__ __forceinline__ uint32_t warp_sort(uint32_t v) {
 struct TopShared {
     uint64_t cand[kCands];
     uint64_t top[kMaxTop];
-    int2 hit[kHits];                 // vector, its maximum
     int hist[256];
-    uint32_t bound[2][kWarps];
-    int hits, cands, digit, above;
+    uint32_t bound[kWarps];
+    int again[kThr];                 // threads whose second largest maximum reaches the bound
+    int agains, cands, digit, above;
 };
 
-// What at least k entries of the CTA's slice reach, given each thread's largest; all threads call it.
-__device__ __forceinline__ float top_bound(float mine, int k, uint32_t* sh) {
+// What at least k entries of the CTA's slice reach, given each thread's largest, of which those of the first `warps`
+// warps are there; −infinity where they are too few.  All threads call it.
+__device__ __forceinline__ float top_bound(float mine, int k, int warps, uint32_t* sh) {
+    const int r = warps > 0 ? (k + warps - 1) / warps : 33;
     const uint32_t s = warp_sort(order_of(mine));
-    if ((threadIdx.x & 31) == (k + kWarps - 1) / kWarps - 1) sh[threadIdx.x >> 5] = s;
+    if (static_cast<int>(threadIdx.x & 31) == r - 1) sh[threadIdx.x >> 5] = s;
     __syncthreads();
-    uint32_t b = sh[0];
+    if (r > 32) return -INFINITY;
+    uint32_t b = 0xffffffffu;
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w) b = min(b, sh[w]);
+    for (int w = 0; w < kWarps; ++w) b = w < warps ? min(b, sh[w]) : b;
     return value_of(b);
 }
 
@@ -262,7 +271,7 @@ __device__ __forceinline__ uint64_t cluster_read64(const uint64_t* p, uint32_t r
 
 template <bool BF16, bool TOP>
 __global__ void __launch_bounds__(kThr, 4) logprob_kernel(const __grid_constant__ ForwardParams a) {
-    constexpr int VEC = BF16 ? 8 : 4, ES = BF16 ? 2 : 4, U = kVectors;
+    constexpr int VEC = BF16 ? 8 : 4, ES = BF16 ? 2 : 4;
     __shared__ alignas(16) unsigned char raw[TOP ? sizeof(TopShared) : 16];
     __shared__ float2 sh[2][kWarps];
     __shared__ float s_part[3];                          // this CTA's (reference, Σ2^x, Σx2^x), read by its cluster
@@ -286,68 +295,32 @@ __global__ void __launch_bounds__(kThr, 4) logprob_kernel(const __grid_constant_
     const int ve = has_edge ? edge<BF16>(s, tid) : 0;
     const float xe = has_edge ? load_elem<BF16>(z, ve) : -INFINITY;
     if constexpr (TOP) {
-        if (tid == 0) t.hits = t.cands = 0;
+        if (tid == 0) t.agains = t.cands = 0;
     }
 
-    // ---- the pass: group j + u·J of 256 vectors in the j-th round, so that the first round is spread over the slice
+    // ---- the pass
     Sums w;
-    float most = xe, bound = INFINITY;                   // the thread's largest logit; what the k largest reach
-    const int groups = (s.nvec + kThr - 1) / kThr, J = (groups + U - 1) / U;
-    auto note = [&](int i, float vm) {
+    const float room = kRaise / c;
+    float limit = -INFINITY;                             // of a maximum that needs no new reference
+    float most = -INFINITY, second = -INFINITY;          // of the thread's vectors
+    int most_at = -1;
+    each_vector<BF16, TOP>(s, [&](int i, const uint4& v) {
+        const float vm = vec_max<BF16>(v);
+        if (!(vm <= limit)) {                            // NaN too
+            w.raise(vm, c);
+            limit = w.m + room;
+        }
         if constexpr (TOP) {
-            if (vm < bound) return;
-            const int at = atomicAdd(&t.hits, 1);
-            if (at < kHits) t.hit[at] = make_int2(i, __float_as_int(vm));
+            most_at = vm > most ? i : most_at;
+            second = fmaxf(second, fminf(most, vm));
+            most = fmaxf(most, vm);
         }
-    };
-    for (int j = 0; j < J; ++j) {
-        uint4 v[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int i = (j + u * J) * kThr + tid;
-            if (i < s.nvec) v[u] = TOP ? ld16_keep(zv + static_cast<int64_t>(i) * 16) : ld16<true>(zv + static_cast<int64_t>(i) * 16);
-        }
-        if (j == 0) {
-            float vm[U], top = has_edge ? xe : -INFINITY;
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                vm[u] = u * J * kThr + tid < s.nvec ? vec_max<BF16>(v[u]) : -INFINITY;
-                top = max_nan(top, vm[u]);
-            }
-            if (!(top == -INFINITY)) w.raise(top, c);
-            most = top;
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (u * J * kThr + tid < s.nvec) w.add<BF16>(v[u], c);
-            if constexpr (TOP) {
-                bound = top_bound(top, a.k, t.bound[0]);
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (u * J * kThr + tid < s.nvec) note(u * J * kThr + tid, vm[u]);
-            }
-        } else {
-            const float room = kRaise / c;
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int i = (j + u * J) * kThr + tid;
-                if (i >= s.nvec) continue;
-                const float vm = vec_max<BF16>(v[u]);
-                most = max_nan(most, vm);
-                if (!(vm < fminf(w.m + room, bound))) {
-                    if (!(vm < w.m + room)) {
-                        if (vm > -INFINITY || vm != vm) w.raise(vm, c);
-                    }
-                    note(i, vm);
-                }
-                w.add<BF16>(v[u], c);
-            }
-        }
+        w.add<BF16>(v, c);
+    });
+    if (has_edge) {
+        if (!(xe <= limit)) w.raise(xe, c);
+        w.add_one(xe, c);
     }
-    if (J == 0) {                                        // a slice of its ends alone
-        if (!(xe == -INFINITY)) w.raise(xe, c);
-        if constexpr (TOP) __syncthreads();              // t.hits
-    }
-    if (has_edge) w.add_one(xe, c);
 
     // ---- the CTA's sums about one reference
     float s0, s1, lo, hi, m = w.m, mc = w.m == -INFINITY ? -INFINITY : w.mc;
@@ -355,13 +328,18 @@ __global__ void __launch_bounds__(kThr, 4) logprob_kernel(const __grid_constant_
     s0 = lo + hi;
     unpair(w.s1, lo, hi);
     s1 = lo + hi;
-    if constexpr (TOP) bound = top_bound(most, a.k, t.bound[1]);
+    float bound = -INFINITY;
+    if constexpr (TOP) bound = top_bound(fmaxf(most, xe), a.k, min(kWarps, s.nvec / 32), t.bound);
     float M = m, MC = mc;
     once_all2<MaxOp, MaxOp>(M, MC, sh[0]);
     const bool bad = __syncthreads_or(w.bad);
     if (MC > -INFINITY && fabsf(MC) > kFarRef) {         // far from 0: again, of differences about the largest
-        w = Sums{};
-        float top = most != most ? -INFINITY : most;
+        float top = -INFINITY;
+        each_vector<BF16, true>(s, [&](int, const uint4& v) {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) top = fmaxf(top, vec_elem<BF16>(v, e));
+        });
+        if (has_edge) top = fmaxf(top, xe);
         top = warp_all<MaxOp>(top);
         if ((tid & 31) == 0) sh[0][tid >> 5].x = top;
         __syncthreads();
@@ -395,42 +373,60 @@ __global__ void __launch_bounds__(kThr, 4) logprob_kernel(const __grid_constant_
     // ---- the CTA's k largest, in order
     int tops = 0;
     if constexpr (TOP) {
-        // t.hits is final: the barrier of the sums lies between
-        const int hits = t.hits;
         auto collect = [&](float x, int v) {
-            if (x < bound) return;
+            if (!(x >= bound)) return;
             const int at = atomicAdd(&t.cands, 1);
             if (at < kCands) t.cand[at] = entry(x, v);
         };
         const int first = s.v0 + s.lead;
-        if (has_edge) collect(xe, ve);
-        if (hits <= kHits) {
-            for (int h = tid; h < hits; h += kThr) {
-                const int2 q = t.hit[h];
-                if (__int_as_float(q.y) < bound) continue;
-                const uint4 v = ld16_keep(zv + static_cast<int64_t>(q.x) * 16);
+        auto collect_vector = [&](int i) {
+            const uint4 v = ld16_keep(zv + static_cast<int64_t>(i) * 16);
+            if (!(vec_max<BF16>(v) >= bound)) return;
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) collect(vec_elem<BF16>(v, e), first + q.x * VEC + e);
+            for (int e = 0; e < VEC; ++e) collect(vec_elem<BF16>(v, e), first + i * VEC + e);
+        };
+        if (!bad) {
+            if (has_edge) collect(xe, ve);
+            if (most_at >= 0 && most >= bound) {
+                if (second >= bound) t.again[atomicAdd(&t.agains, 1)] = tid;
+                else collect_vector(most_at);
+            } else if (most_at < 0 && bound == -INFINITY) {   // vectors of −infinity alone
+                t.again[atomicAdd(&t.agains, 1)] = tid;
             }
-        } else {
-            each_vector<BF16, true>(s, [&](int i, const uint4& v) {
-                if (vec_max<BF16>(v) < bound) return;
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) collect(vec_elem<BF16>(v, e), first + i * VEC + e);
-            });
+            __syncthreads();
+            const int agains = t.agains, groups = (s.nvec + kThr - 1) / kThr;
+            for (int a = tid >> 5; a < agains; a += kWarps) {
+                for (int j = tid & 31; j < groups; j += 32) {
+                    const int i = j * kThr + t.again[a];
+                    if (i < s.nvec) collect_vector(i);
+                }
+            }
         }
         __syncthreads();
         int n = t.cands;
-        if (n > kCands) {                                // more than kCands >= k entries: by digits of the whole slice
+        if (bad || n > kCands) {                         // NaN are not collected; or too many
             __syncthreads();
-            select_by_digits(t, a.k, [&](auto body) {
+            if (v1 - v0 <= kCands) {                         // all of them
+                if (tid == 0) t.cands = 0;
+                __syncthreads();
                 each_vector<BF16, true>(s, [&](int i, const uint4& v) {
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) body(entry(vec_elem<BF16>(v, e), first + i * VEC + e));
+                    for (int e = 0; e < VEC; ++e) t.cand[atomicAdd(&t.cands, 1)] = entry(vec_elem<BF16>(v, e), first + i * VEC + e);
                 });
-                if (has_edge) body(entry(xe, ve));
-            });
-            n = a.k;
+                if (has_edge) t.cand[atomicAdd(&t.cands, 1)] = entry(xe, ve);
+                __syncthreads();
+                n = v1 - v0;
+            } else
+            {
+                select_by_digits(t, a.k, [&](auto body) {
+                    each_vector<BF16, true>(s, [&](int i, const uint4& v) {
+#pragma unroll
+                        for (int e = 0; e < VEC; ++e) body(entry(vec_elem<BF16>(v, e), first + i * VEC + e));
+                    });
+                    if (has_edge) body(entry(xe, ve));
+                });
+                n = a.k;
+            }
         }
         tops = sort_top(t, n, a.k);
     }
@@ -574,9 +570,7 @@ __global__ void __launch_bounds__(kThr, 4) logprob_grad_kernel(const __grid_cons
 
 // log2(e)/τ, or 0 where the temperature is not one.
 float scale_of(float tau) {
-    if (!(tau > 0.0f) || !(tau < 3.0e38f)) return 0.0f;
-    const float c = static_cast<float>(1.4426950408889634 / static_cast<double>(tau));
-    return c > 1.2e-38f && c < 3.0e38f ? c : 0.0f;
+    return tau >= 1.0e-30f && tau <= 1.0e30f ? static_cast<float>(1.4426950408889634 / static_cast<double>(tau)) : 0.0f;
 }
 
 }  // namespace

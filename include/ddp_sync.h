@@ -822,7 +822,7 @@ int layernorm_backward(const void* dy, int64_t lddy, int32_t dy_dtype, const voi
  *   top_logprob   device float[T, k] or NULL.  Entries past the vocabulary
  *                 (k > V) have index -1 and log probability -infinity: what
  *                 distill_topk_forward takes for no entry
- *   temperature   > 0
+ *   temperature   1e-30 .. 1e30
  * Logits of -infinity have probability 0 (they are listed last, with their
  * index and log probability -infinity); a token with no others has lse
  * -infinity, entropy 0 and log probabilities -infinity.  A token with a logit
