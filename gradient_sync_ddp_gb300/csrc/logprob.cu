@@ -33,6 +33,7 @@ namespace {
 
 constexpr int kThr = kVocabThreads, kWarps = kThr / 32;
 constexpr int kMaxTop = DDP_LOGPROB_MAX_TOP;
+constexpr int kHits = 512;           // vectors that hold the largest entries
 constexpr int kCands = 1024;         // entries collected
 constexpr int kCount = 256;          // up to this many entries ranks are counted at once
 constexpr float kRaise = 8.0f;       // how far a thread's x may lie above its reference
@@ -150,20 +151,23 @@ __device__ __forceinline__ uint32_t warp_sort(uint32_t v) {
 struct TopShared {
     uint64_t cand[kCands];
     uint64_t top[kMaxTop];
+    uint4 hit[kHits];                // vectors whose maximum reaches the bound
+    int hit_at[kHits];
     int hist[256];
     uint32_t bound[kWarps];
     int again[kThr];                 // threads whose second largest maximum reaches the bound
-    int agains, cands, digit, above;
+    int agains, hits, cands, digit, above;
 };
 
 // What at least k entries of the CTA's slice reach, given each thread's largest, of which those of the first `warps`
-// warps are there; −infinity where they are too few.  All threads call it.
-__device__ __forceinline__ float top_bound(float mine, int k, int warps, uint32_t* sh) {
-    const int r = warps > 0 ? (k + warps - 1) / warps : 33;
+// warps are there; −infinity where they are too few.  A barrier lies between the two calls.
+__device__ __forceinline__ int bound_rank(int k, int warps) { return warps > 0 ? (k + warps - 1) / warps : 33; }
+__device__ __forceinline__ void bound_begin(float mine, int k, int warps, uint32_t* sh) {
     const uint32_t s = warp_sort(order_of(mine));
-    if (static_cast<int>(threadIdx.x & 31) == r - 1) sh[threadIdx.x >> 5] = s;
-    __syncthreads();
-    if (r > 32) return -INFINITY;
+    if (static_cast<int>(threadIdx.x & 31) == bound_rank(k, warps) - 1) sh[threadIdx.x >> 5] = s;
+}
+__device__ __forceinline__ float bound_end(int k, int warps, const uint32_t* sh) {
+    if (bound_rank(k, warps) > 32) return -INFINITY;
     uint32_t b = 0xffffffffu;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) b = w < warps ? min(b, sh[w]) : b;
@@ -242,7 +246,8 @@ __device__ void select_by_digits(TopShared& t, int k, Each each) {
     __syncthreads();
 }
 
-// The k largest of t.cand[0..n) (all of them if fewer), in order, in t.top; n is at most kCands.
+// The k largest of t.cand[0..n) (all of them if fewer), in order, in t.top; n is at most kCands.  Each warp sorts 32 of
+// up to kCount; an entry's rank is its place there and, by halving, its places in the other warps' lists.
 __device__ __forceinline__ int sort_top(TopShared& t, int n, int k) {
     if (n > kCount && n > k) {
         select_by_digits(t, k, [&](auto body) {
@@ -250,12 +255,33 @@ __device__ __forceinline__ int sort_top(TopShared& t, int n, int k) {
         });
         n = k;
     }
-    const int m = min(n, k);
-    if (static_cast<int>(threadIdx.x) < n) {
-        const uint64_t mine = t.cand[threadIdx.x];
-        int rank = 0;
-        for (int i = 0; i < n; ++i) rank += t.cand[i] > mine;
-        if (rank < m) t.top[rank] = mine;
+    const int m = min(n, k), lists = (n + 31) / 32, lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    uint64_t v = static_cast<int>(threadIdx.x) < n ? t.cand[threadIdx.x] : 0;      // less than any entry
+    if (w < lists) {
+#pragma unroll
+        for (int size = 2; size <= 32; size *= 2) {
+#pragma unroll
+            for (int step = size / 2; step > 0; step /= 2) {
+                const uint64_t o = __shfl_xor_sync(0xffffffffu, v, step);
+                const bool up = ((lane & size) == 0) == ((lane & step) == 0);      // this lane keeps the larger one
+                v = up == (v > o) ? v : o;
+            }
+        }
+        t.cand[threadIdx.x] = v;                         // this warp's own 32
+    }
+    __syncthreads();
+    if (w < lists && v != 0) {
+        int rank = lane;
+        for (int l = 0; l < lists; ++l) {
+            if (l == w) continue;
+            const uint64_t* a = t.cand + 32 * l;
+            int at = 0;
+#pragma unroll
+            for (int step = 16; step > 0; step /= 2)
+                if (a[at + step - 1] > v) at += step;
+            rank += at + (a[at] > v);
+        }
+        if (rank < m) t.top[rank] = v;
     }
     __syncthreads();
     return m;
@@ -295,7 +321,7 @@ __global__ void __launch_bounds__(kThr, 4) logprob_kernel(const __grid_constant_
     const int ve = has_edge ? edge<BF16>(s, tid) : 0;
     const float xe = has_edge ? load_elem<BF16>(z, ve) : -INFINITY;
     if constexpr (TOP) {
-        if (tid == 0) t.agains = t.cands = 0;
+        if (tid == 0) t.agains = t.hits = t.cands = 0;
     }
 
     // ---- the pass
@@ -328,11 +354,18 @@ __global__ void __launch_bounds__(kThr, 4) logprob_kernel(const __grid_constant_
     s0 = lo + hi;
     unpair(w.s1, lo, hi);
     s1 = lo + hi;
-    float bound = -INFINITY;
-    if constexpr (TOP) bound = top_bound(fmaxf(most, xe), a.k, min(kWarps, s.nvec / 32), t.bound);
-    float M = m, MC = mc;
-    once_all2<MaxOp, MaxOp>(M, MC, sh[0]);
+    const int full = min(kWarps, s.nvec / 32);           // warps whose threads all have a vector
+    if constexpr (TOP) bound_begin(fmaxf(most, xe), a.k, full, t.bound);
+    float M = warp_all<MaxOp>(m), MC = warp_all<MaxOp>(mc);
+    if ((tid & 31) == 0) sh[0][tid >> 5] = make_float2(M, MC);
     const bool bad = __syncthreads_or(w.bad);
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+        M = fmaxf(M, sh[0][i].x);
+        MC = fmaxf(MC, sh[0][i].y);
+    }
+    float bound = -INFINITY;
+    if constexpr (TOP) bound = bound_end(a.k, full, t.bound);
     if (MC > -INFINITY && fabsf(MC) > kFarRef) {         // far from 0: again, of differences about the largest
         float top = -INFINITY;
         each_vector<BF16, true>(s, [&](int, const uint4& v) {
@@ -341,6 +374,7 @@ __global__ void __launch_bounds__(kThr, 4) logprob_kernel(const __grid_constant_
         });
         if (has_edge) top = fmaxf(top, xe);
         top = warp_all<MaxOp>(top);
+        __syncthreads();
         if ((tid & 31) == 0) sh[0][tid >> 5].x = top;
         __syncthreads();
         M = -INFINITY;
@@ -367,44 +401,70 @@ __global__ void __launch_bounds__(kThr, 4) logprob_kernel(const __grid_constant_
         s1 = (s1 - r * s0) * g;
         s0 *= g;
     }
+    // ---- the vectors that reach the bound: a thread's own, with the sums under way
+    const int first = s.v0 + s.lead;
+    auto collect = [&](float x, int v) {
+        const int at = atomicAdd(&t.cands, 1);
+        if (at < kCands) t.cand[at] = entry(x, v);
+    };
+    auto note = [&](int i, const uint4& v) {
+        const int at = atomicAdd(&t.hits, 1);
+        if (at >= kHits) return;
+        t.hit[at] = v;
+        t.hit_at[at] = i;
+    };
+    if constexpr (TOP) {
+        if (!bad) {
+            if (has_edge && xe >= bound) collect(xe, ve);
+            if (most_at >= 0 && most >= bound) {
+                if (second >= bound) t.again[atomicAdd(&t.agains, 1)] = tid;
+                else note(most_at, ld16_keep(zv + static_cast<int64_t>(most_at) * 16));
+            } else if (most_at < 0 && bound == -INFINITY) {   // vectors of −infinity alone
+                t.again[atomicAdd(&t.agains, 1)] = tid;
+            }
+        }
+    }
     once_all2<SumOp, SumOp>(s0, s1, sh[1]);
     if (bad) s0 = s1 = __int_as_float(0x7fffffff);
 
     // ---- the CTA's k largest, in order
     int tops = 0;
     if constexpr (TOP) {
-        auto collect = [&](float x, int v) {
-            if (!(x >= bound)) return;
-            const int at = atomicAdd(&t.cands, 1);
-            if (at < kCands) t.cand[at] = entry(x, v);
-        };
-        const int first = s.v0 + s.lead;
-        auto collect_vector = [&](int i) {
-            const uint4 v = ld16_keep(zv + static_cast<int64_t>(i) * 16);
-            if (!(vec_max<BF16>(v) >= bound)) return;
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) collect(vec_elem<BF16>(v, e), first + i * VEC + e);
-        };
         if (!bad) {
-            if (has_edge) collect(xe, ve);
-            if (most_at >= 0 && most >= bound) {
-                if (second >= bound) t.again[atomicAdd(&t.agains, 1)] = tid;
-                else collect_vector(most_at);
-            } else if (most_at < 0 && bound == -INFINITY) {   // vectors of −infinity alone
-                t.again[atomicAdd(&t.agains, 1)] = tid;
-            }
-            __syncthreads();
             const int agains = t.agains, groups = (s.nvec + kThr - 1) / kThr;
-            for (int a = tid >> 5; a < agains; a += kWarps) {
+            constexpr int N = 4;                         // threads at a time: one after another took a latency of L2 each
+            for (int a = tid >> 5; a < agains; a += N * kWarps) {
                 for (int j = tid & 31; j < groups; j += 32) {
-                    const int i = j * kThr + t.again[a];
-                    if (i < s.nvec) collect_vector(i);
+                    int i[N];
+                    uint4 v[N];
+#pragma unroll
+                    for (int q = 0; q < N; ++q) {
+                        i[q] = a + q * kWarps < agains ? j * kThr + t.again[a + q * kWarps] : s.nvec;
+                        if (i[q] < s.nvec) v[q] = ld16_keep(zv + static_cast<int64_t>(i[q]) * 16);
+                    }
+#pragma unroll
+                    for (int q = 0; q < N; ++q)
+                        if (i[q] < s.nvec && vec_max<BF16>(v[q]) >= bound) note(i[q], v[q]);
                 }
             }
         }
         __syncthreads();
+        const int hits = t.hits;
+        for (int q = tid; q < min(hits, kHits); q += kThr) {
+            const uint4 v = t.hit[q];
+            const int at = first + t.hit_at[q] * VEC;
+            uint32_t in = 0;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) in |= vec_elem<BF16>(v, e) >= bound ? 1u << e : 0u;
+            for (; in != 0; in &= in - 1) {
+                const int e = __ffs(in) - 1, l = BF16 ? e >> 1 : e;
+                const uint32_t x = l == 0 ? v.x : l == 1 ? v.y : l == 2 ? v.z : v.w;
+                collect(BF16 ? (e & 1 ? bf16_hi(x) : bf16_lo(x)) : __uint_as_float(x), at + e);
+            }
+        }
+        __syncthreads();
         int n = t.cands;
-        if (bad || n > kCands) {                         // NaN are not collected; or too many
+        if (bad || hits > kHits || n > kCands) {         // NaN are not collected; or too many
             __syncthreads();
             if (v1 - v0 <= kCands) {                         // all of them
                 if (tid == 0) t.cands = 0;
@@ -459,14 +519,24 @@ __global__ void __launch_bounds__(kThr, 4) logprob_kernel(const __grid_constant_
                 s1 = fmaf(fmaf(d, p0[r], p1[r]), f, s1);
             }
             if constexpr (TOP) {
-                int n = 0;
-                for (int r = 0; r < a.cluster; ++r) {
-                    const int m = __float_as_int(cluster_read(reinterpret_cast<const float*>(&s_tops), r));
-                    if (tid < m) t.cand[n + tid] = cluster_read64(&t.top[tid], r);
-                    n += m;
+                // what the ceil(k / cluster) largest of every slice reach, k entries at least reach
+                const int q = (a.k + a.cluster - 1) / a.cluster;
+                int count[kMaxCluster];
+                uint64_t least = ~0ull;
+#pragma unroll
+                for (int r = 0; r < kMaxCluster; ++r) {
+                    count[r] = r < a.cluster ? __float_as_int(cluster_read(reinterpret_cast<const float*>(&s_tops), r)) : 0;
+                    if (r < a.cluster) least = count[r] < q ? 0 : min(least, cluster_read64(&t.top[q - 1], r));
+                }
+                if (tid == 0) t.cands = 0;
+                __syncthreads();
+#pragma unroll
+                for (int r = 0; r < kMaxCluster; ++r) {
+                    const uint64_t e = tid < count[r] ? cluster_read64(&t.top[tid], r) : 0;
+                    if (e != 0 && e >= least) t.cand[atomicAdd(&t.cands, 1)] = e;
                 }
                 __syncthreads();
-                tops = sort_top(t, n, a.k);
+                tops = sort_top(t, t.cands, a.k);
             }
         }
         cluster_sync();                                  // no CTA ends while another reads its part
