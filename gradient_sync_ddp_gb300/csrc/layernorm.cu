@@ -91,9 +91,14 @@ __global__ void __launch_bounds__(kNormThreads) ln_loop_kernel(const __grid_cons
     }
 }
 
+// Threads of a CTA per row, and CTAs of so many per SM.  Rows in flight count: 16384 x 4096 bf16 took 96 us with 42
+// registers a thread (five CTAs of 256 threads per SM), 86 with 32.
+constexpr int max_norm_group(bool bf16, int vpt) { return bf16 && vpt == 2 ? 512 : max_group(bf16, vpt); }
+constexpr int norm_groups(bool bf16, int vpt) { return bf16 && vpt == 2 ? 4 : 1; }
+
 // VPT vectors per thread.  WARP: a warp per row, kWarpRows per CTA; else a CTA per row.
 template <bool BF16, bool YBF16, int VPT, bool EDGE, bool WARP>
-__global__ void __launch_bounds__(WARP ? 32 * kWarpRows : max_group(BF16, VPT))
+__global__ void __launch_bounds__(WARP ? 32 * kWarpRows : max_norm_group(BF16, VPT), WARP || EDGE ? 1 : norm_groups(BF16, VPT))
     ln_kernel(const __grid_constant__ LayerNormParams a) {
     constexpr int ES = BF16 ? 2 : 4, VEC = 16 / ES, YS = YBF16 ? 2 : 4;
     __shared__ float sh[2][32];
@@ -241,6 +246,7 @@ template <bool BF16, bool DYBF16, int VPT, bool WARP, bool AHEAD, bool EDGE>
 __global__ void __launch_bounds__(WARP ? 32 * kGradRows : AHEAD ? 512 : max_grad_group(BF16, VPT))
     ln_grad_kernel(const __grid_constant__ LayerNormGradParams a) {
     constexpr int ES = BF16 ? 2 : 4, VEC = 16 / ES, YS = DYBF16 ? 2 : 4;
+    constexpr bool LATE = WARP && VPT == 4;   // dh after the reduction: 128 registers do not hold it beside the rest
     extern __shared__ float part_sh[];   // WARP and a.partial: [kGradRows][D]
     __shared__ float2 sh[2][32];
     pdl_enter();
@@ -276,6 +282,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kGradRows : AHEAD ? 512 : max_grad
             if (v < s.nvec) {
                 gg[i].load(dy + (s.lead + v * VEC) * YS);
                 hh[i].load(hp + (s.lead + v * VEC) * ES);
+                if (LATE) continue;
                 if (dh) rr[i].load(dh + (s.lead + v * VEC) * ES);
                 else rr[i].zero();
             }
@@ -330,6 +337,10 @@ __global__ void __launch_bounds__(WARP ? 32 * kGradRows : AHEAD ? 512 : max_grad
             const int v = t + i * G;
             if (v >= s.nvec) break;
             float gm[VEC], o[VEC];
+            if constexpr (LATE) {
+                if (a.dh) r[i].load(row_ptr<BF16>(a.dh, row, a.lddh) + (s.lead + v * VEC) * ES);
+                else r[i].zero();
+            }
             load_cols<EDGE, VEC>(a.gamma, 1.0f, a.D, s.lead + v * VEC, gm);
 #pragma unroll
             for (int e = 0; e < VEC; ++e)
@@ -570,7 +581,11 @@ extern "C" int layernorm_forward(const void* x, int64_t ldx, const void* residua
     const Mat* const mats[4] = {&mx, &mr, &mh, &my};
     Lay lay = layout(mats, 4, D, b ? 8 : 4, gamma);
     if (lay == Lay::kAligned && !aligned16(beta)) lay = Lay::kAlike;
-    const Group g = pick_group(rows, D, b, d.sm_count);
+    Group g = pick_group(rows, D, b, d.sm_count);
+    if (!g.warp && g.vpt == 2 && g.threads > max_norm_group(b, 2)) {
+        const int nv = (D + (b ? 8 : 4) - 1) / (b ? 8 : 4);
+        g = Group{4, ((nv + 3) / 4 + 31) / 32 * 32, false};
+    }
     void (*kernel)(LayerNormParams) = b ? (c ? fwd_kernel<true, true>(lay, g) : fwd_kernel<true, false>(lay, g))
                                         : (c ? fwd_kernel<false, true>(lay, g) : fwd_kernel<false, false>(lay, g));
     const bool loop = lay == Lay::kDifferent || g.threads == 0;

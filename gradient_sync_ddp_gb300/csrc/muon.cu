@@ -25,8 +25,8 @@
 //   split_kernel   ‖U‖ from its parts, U to fp16 (and the rest), transposed where tall
 //   step_kernel    all products of all steps, persistent: a pair of CTAs per tile of
 //                  256 x 256, or a CTA per tile of 128 x 128 where pairs would leave
-//                  SMs without work.  Roles by warp: a producer that takes the next tile's number,
-//                  waits until the rows it needs of the product before are whole, and loads by TMA (64
+//                  SMs without work.  Roles by warp: a scheduler that takes the next tile's number and
+//                  waits until the rows it needs of the product before are whole; a producer that loads by TMA (64
 //                  of K a stage, 128-byte swizzle, five stages); an issuer of tcgen05.mma; sixteen
 //                  epilogue warps.  Two accumulators in TMEM, so that a tile's epilogue
 //                  runs under the next one's products.  A symmetric matrix's tiles are
@@ -251,7 +251,8 @@ constexpr int kStepThreads = 128 + 32 * kEpilogueWarps;   // and four of single 
 constexpr int kWarpBytes = 2 * 32 * 64;   // twice 64 bytes of a warp's 32 rows in shared memory at a time
 // more than half of an SM's shared memory: a CTA takes all of its SM's TMEM
 constexpr size_t kStepSmem = kStages * kStageBytes + kEpilogueWarps * kWarpBytes + 1024;
-constexpr int kItems = 4;              // tiles on their way from the producer to the other roles
+constexpr int kMaxGroups = 8;          // of matrices that go through the products one behind another
+constexpr int kItems = 4;              // tiles on their way from the scheduler to the other roles
 
 enum { kGram = 0, kPoly = 1, kApply = 2 };
 enum { kOutF32 = 0, kOutBf16 = 1, kOutParam = 2 };
@@ -269,14 +270,15 @@ struct StepParams {
     int64_t ldo;
     float decay, step;        // kOutParam
     int32_t kind, tall, vec, has2;
-    int32_t m, n, mp, np, count, steps;
+    int32_t m, n, mp, np, count, steps, groups;
+    uint16_t order[kMaxGroups * 3 * kMaxSteps];   // products: 256·group + (3·step + product)
     int32_t tm, tn, sym, full;   // tiles of a matrix: rows, columns, on and above the diagonal, all of X's
 };
 
 struct StepShared {
     uint64_t ready[kStages];   // of the first CTA: both CTAs' operands are in shared memory
     uint64_t done[kStages];    // a stage's MMAs: it may be overwritten
-    uint64_t d_full[2], d_empty[2], idle;
+    uint64_t d_full[2], d_empty[2], idle, taken;
     uint64_t item_full[kItems], item_empty[kItems];   // item_empty: of the first CTA
     int item[kItems];
     int warps_done[4];         // of the epilogue's, with a tile
@@ -312,41 +314,59 @@ __device__ __forceinline__ uint64_t smem_desc_columns(uint32_t addr) {
     return static_cast<uint64_t>((addr >> 4) & 0x3fff) | (512ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
 }
 
-// The u-th tile of all steps: step, product, matrix, tile row and column.  Tiles go by product, then by matrix; the Gram
-// matrix's by columns and the others by rows, so that a product's first tiles need the first rows of the one before.
+// A tile: step, product, matrix, tile row and column.  As one number (48 products, 64 matrices, 512 rows and columns)
+// from the scheduler, which works it out, to the other roles.
 struct Item {
     int step, mode, b, i, j;
 };
-__device__ __forceinline__ Item item_of(const StepParams& p, int u) {
+__device__ __forceinline__ int packed(const Item& t) { return (t.step * 3 + t.mode) << 24 | t.b << 18 | t.i << 9 | t.j; }
+__device__ __forceinline__ Item unpacked(int v) {
     Item t;
-    const int sym = p.sym * p.count, all = 2 * sym + p.full * p.count;
-    t.step = u / all;
-    int r = u - t.step * all;
-    t.mode = r < sym ? kGram : r < 2 * sym ? kPoly : kApply;
-    r -= t.mode * sym;
-    const int per = t.mode == kApply ? p.full : p.sym;
-    t.b = r / per;
-    r -= t.b * per;
-    if (t.mode == kApply) {
-        t.i = r / p.tn;
-        t.j = r - t.i * p.tn;
-    } else if (t.mode == kPoly) {
-        t.i = 0;
-        for (int w = p.tm; r >= w; --w) {
-            r -= w;
-            ++t.i;
-        }
-        t.j = t.i + r;
-    } else {
-        t.j = 0;
-        for (int w = 1; r >= w; ++w) {
-            r -= w;
-            ++t.j;
-        }
-        t.i = r;
-    }
+    t.step = (v >> 24) / 3;
+    t.mode = (v >> 24) - 3 * t.step;
+    t.b = v >> 18 & 63;
+    t.i = v >> 9 & 511;
+    t.j = v & 511;
     return t;
 }
+// The u-th tile, for ever larger u.  Matrices go in groups, and the groups' products in the order that the host has
+// laid out, so that a tile's predecessors have been begun a good while before it.  Within a product the Gram matrix's
+// tiles go by columns and the others by rows, so that a product's first tiles need the first rows of the one before.
+struct Cursor {
+    int at_ = 0, base = 0;
+    __device__ __forceinline__ Item at(const StepParams& p, int u) {
+        for (;; ++at_) {
+            const int entry = p.order[at_], group = entry >> 8, phase = entry & 255, step = phase / 3, mode = phase - 3 * step;
+            const int b0 = group * p.count / p.groups, per = mode == kApply ? p.full : p.sym;
+            const int n = ((group + 1) * p.count / p.groups - b0) * per;
+            if (u >= base + n) {
+                base += n;
+                continue;
+            }
+            int r = u - base;
+            Item t{step, mode, r / per, 0, 0};
+            r -= t.b * per;
+            t.b += b0;
+            if (mode == kApply) {
+                t.i = r / p.tn;
+                t.j = r - t.i * p.tn;
+            } else if (mode == kPoly) {
+                for (int w = p.tm; r >= w; --w) {
+                    r -= w;
+                    ++t.i;
+                }
+                t.j = t.i + r;
+            } else {
+                for (int w = 1; r >= w; ++w) {
+                    r -= w;
+                    ++t.j;
+                }
+                t.i = r;
+            }
+            return t;
+        }
+    }
+};
 // Once A is near I: of A' = A − I, aI + B = (a + b + c)I + (b + 2c)A' + cA'², and X ← (aI + B)·X.
 __device__ __forceinline__ bool near_one(const StepParams& p, int step) { return step >= max(p.steps - 2, 2); }
 // X's second half goes into the steps but the last two.
@@ -382,7 +402,7 @@ __device__ __forceinline__ bool wait_before(const StepParams& p, const Item& t, 
     if (!wait_count(done_of(p, step, mode, t.b, t.i), want, s)) return false;
     return t.mode == kApply || t.i == t.j || wait_count(done_of(p, step, mode, t.b, t.j), want, s);
 }
-// The next tile's number, for as long as tiles come, whether or not a wait has run out before.
+// The next tile, for as long as tiles come, whether or not a wait has run out before.
 template <bool PAIR>
 __device__ __forceinline__ int next_item(StepShared& s, const Ring& r) {
     const long long t0 = clock64();
@@ -544,9 +564,10 @@ __global__ void __launch_bounds__(kStepThreads, 1) step_kernel(const __grid_cons
         }
         for (int i = 0; i < kItems; ++i) {
             bar_init(&s.item_full[i], 1);
-            bar_init(&s.item_empty[i], PAIR ? 2 * kEpilogueWarps + 2 : kEpilogueWarps + 1);   // the issuer, the other producer
+            bar_init(&s.item_empty[i], PAIR ? 2 * kEpilogueWarps + 3 : kEpilogueWarps + 2);   // the issuer, the producers
         }
         bar_init(&s.idle, 1);
+        bar_init(&s.taken, 1);
         for (int i = 0; i < 4; ++i) s.warps_done[i] = 0;
         s.failed = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -571,28 +592,37 @@ __global__ void __launch_bounds__(kStepThreads, 1) step_kernel(const __grid_cons
     pdl_wait();
     const int total = p.steps * p.count * (2 * p.sym + p.full);
 
-    if (warp == 0 && lane == 0) {                        // producer
+    if (warp == 2 && lane == 0 && rank == 0) {           // scheduler: the next tile, under this one's copies
+        Ring q;
+        Cursor cursor;
+        uint32_t taken = 0;
+        bool ok = true;
+        for (;;) {
+            int u = atomicAdd(p.sync, 1);
+            u = u < total ? packed(cursor.at(p, u)) : -1;
+            // one thread per tile looks at the counters (with the epilogue's looking too, counting took longer than
+            // launches), and tells the others that all is there by telling them the tile; what has failed goes on, as NaN
+            if (u >= 0 && ok) ok = wait_before<PAIR ? 2 : 1>(p, unpacked(u), s);
+            bar_drain(&s.item_empty[q.i], q.ph ^ 1, s);
+            publish_item<PAIR>(s, q, u);
+            q.next(kItems);
+            if (u < 0) break;
+            bar_drain(&s.taken, taken, s);               // no more tiles than one ahead: others have none
+            taken ^= 1;
+        }
+    } else if (warp == 0 && lane == 0) {                 // producer
         Ring r, q;
         int issued = 0;
         bool ok = true;
         for (;;) {
-            int u;
-            if (rank == 0) {
-                u = atomicAdd(p.sync, 1);
-                if (u >= total) u = -1;
-                // one thread per tile looks at the counters (with the epilogue's looking too, counting took longer than
-                // launches), and tells the others that all is there by telling them the tile
-                if (u >= 0 && ok) ok = wait_before<PAIR ? 2 : 1>(p, item_of(p, u), s);
-                bar_drain(&s.item_empty[q.i], q.ph ^ 1, s);
-                publish_item<PAIR>(s, q, u);
-            } else {
-                u = next_item<PAIR>(s, q);
-                item_taken<PAIR>(s, q);
-            }
+            const int u = next_item<PAIR>(s, q);
+            item_taken<PAIR>(s, q);
             q.next(kItems);
             if (u < 0) break;
-            const Item t = item_of(p, u);
-            if (!ok) continue;                           // tiles go on, as NaN
+            if (rank == 0) bar_arrive(&s.taken);
+            const Item t = unpacked(u);
+            ok = ok && !s.failed;
+            if (!ok) continue;
             asm volatile("fence.proxy.async.global;" ::: "memory");        // written through the generic proxy
             const int row0 = t.b * p.mp, ra = t.i * SIDE + rank * kRows, rb = t.j * SIDE + rank * kRows, from = t.step & 1;
             const int blocks = (t.mode == kGram ? p.np : p.mp) / kBlockK;
@@ -636,7 +666,7 @@ __global__ void __launch_bounds__(kStepThreads, 1) step_kernel(const __grid_cons
             fence_after();
             // votes, so that what follows from the tile's number is known to be the warp's: registers that the MMA takes as
             // they are (376 clocks to issue four of them without)
-            const int mode = item_of(p, u).mode;
+            const int mode = unpacked(u).mode;
             const bool gram = __any_sync(0xffffffffu, mode == kGram), by_columns = __any_sync(0xffffffffu, mode == kApply);
             const uint32_t acc = d.i * SIDE;
             const int blocks = (gram ? p.np : p.mp) / kBlockK;
@@ -677,7 +707,7 @@ __global__ void __launch_bounds__(kStepThreads, 1) step_kernel(const __grid_cons
             if (lane == 0) item_taken<PAIR>(s, q);
             q.next(kItems);
             if (u < 0) break;
-            const Item t = item_of(p, u);
+            const Item t = unpacked(u);
             const int row0 = t.i * SIDE + rank * kRows + rows, from = t.step & 1;
             const bool last = t.mode == kApply && t.step == p.steps - 1;
             const bool in = row0 < p.mp;                 // padded to 64: all 32 rows or none
@@ -815,7 +845,7 @@ __global__ void __launch_bounds__(kStepThreads, 1) step_kernel(const __grid_cons
                 asm volatile("fence.proxy.async.global;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) {
-                    __threadfence();
+                    __threadfence_block();               // the last warp's fence is for all that it has seen
                     if (atomicAdd(&s.warps_done[tile & 3], 1) == kEpilogueWarps - 1) {   // a warp is two tiles ahead of another at most
                         s.warps_done[tile & 3] = 0;
                         __threadfence();
@@ -876,30 +906,46 @@ Layout layout_of(int count, int rows, int cols) {
     return l;
 }
 
-// Tiles by pairs of CTAs or by single ones, for all products alike: the less time, in K blocks of a 128 x 128 tile.  A
-// pair's 256 x 256 tile takes two such times of the tensor cores, a CTA's 128 x 128 one a little more than one (its
-// operands come at twice the bytes per product).  Several matrices fill each other's last waves.
+// Tiles by pairs of CTAs or by single ones, and the order of the groups' products, with the time that it takes in
+// clocks from what was measured: a block of 64 of K takes a pair's 256 x 256 tile 620, a CTA's 128 x 128 one 660, and 400
+// where few run (its operands come at twice the bytes per product); a tile's epilogue 13000 and 8000; from a tile's last
+// product to the first one of a tile that waits for it 16000 and 11000.  Of the groups' next products the one that
+// can begin first comes next: 12 x 768 x 2304 took 395 us with all matrices in step.
 struct Tiling {
     bool pair;
-    int tm, tn, sym, full, ctas;
+    int tm, tn, sym, full, ctas, groups;
+    uint16_t order[kMaxGroups * 3 * kMaxSteps];
 };
-Tiling tiling(int count, const Layout& l, int sms) {
-    Tiling best{};
-    double least = 0.0;
-    for (const bool pair : {true, false}) {
-        const int side = pair ? 256 : 128, at = pair ? sms / 2 : sms;
-        const int tm = (l.mp + side - 1) / side, tn = (l.np + side - 1) / side, sym = tm * (tm + 1) / 2, full = tm * tn;
-        auto waves = [&](int tiles) {
-            const double w = static_cast<double>(tiles) * count / at;
-            return count == 1 ? std::ceil(w) : std::max(w, 1.0);
-        };
-        const double cost = (pair ? 2.0 : 1.3) * (waves(sym) * (l.np + l.mp) + waves(full) * l.mp);
-        if (pair || cost < least) {
-            least = cost;
-            best = Tiling{pair, tm, tn, sym, full, std::min(std::max(sym, full) * count, at) * (pair ? 2 : 1)};
-        }
+double lay_out(Tiling& t, bool pair, int count, int steps, const Layout& l, int sms) {
+    const int side = pair ? 256 : 128, at = pair ? sms / 2 : sms;
+    t.pair = pair;
+    t.tm = (l.mp + side - 1) / side;
+    t.tn = (l.np + side - 1) / side;
+    t.sym = t.tm * (t.tm + 1) / 2;
+    t.full = t.tm * t.tn;
+    t.ctas = static_cast<int>(std::min<int64_t>(static_cast<int64_t>(std::max(t.sym, t.full)) * count, at)) * (pair ? 2 : 1);
+    t.groups = std::min(count, kMaxGroups);
+    double pool = 0.0, ready[kMaxGroups] = {}, end = 0.0;
+    int phase[kMaxGroups] = {};
+    for (int i = 0; i < t.groups * 3 * steps; ++i) {
+        int g = -1;
+        for (int k = 0; k < t.groups; ++k)
+            if (phase[k] < 3 * steps && (g < 0 || ready[k] < ready[g])) g = k;
+        const int mode = phase[g] % 3;
+        const int64_t tiles = static_cast<int64_t>((g + 1) * count / t.groups - g * count / t.groups) * (mode == kApply ? t.full : t.sym);
+        const double waves = static_cast<double>(tiles) / at;
+        const double product = static_cast<double>((mode == kGram ? l.np : l.mp) / kBlockK) * (pair ? 620 : waves > 0.5 || t.groups > 1 ? 660 : 400);
+        const double each = std::max(product, pair ? 13000.0 : 8000.0), start = std::max(pool, ready[g]);
+        pool = start + each * (t.groups > 1 ? waves : std::ceil(waves) - 1.0);
+        ready[g] = pool + product + (pair ? 16000.0 : 11000.0);
+        end = std::max(end, ready[g]);
+        t.order[i] = static_cast<uint16_t>(g << 8 | phase[g]++);
     }
-    return best;
+    return end;
+}
+Tiling tiling(int count, int steps, const Layout& l, int sms) {
+    Tiling two, one;
+    return lay_out(two, true, count, steps, l, sms) <= lay_out(one, false, count, steps, l, sms) ? two : one;
 }
 
 struct Call {
@@ -942,7 +988,7 @@ int run_steps(const Call& c, const Layout& l, const Results& r) {
         if ((st = map(&p.xn[i], p.x[i], l.np, kBlockK)) != DDP_OK) return st;
     }
     if ((st = map(&p.ak, p.a, l.mp, kRows)) != DDP_OK || (st = map(&p.bk, p.b, l.mp, kRows)) != DDP_OK) return st;
-    const Tiling t = tiling(c.count, l, d.sm_count);
+    const Tiling t = tiling(c.count, c.steps, l, d.sm_count);
     if (static_cast<int64_t>(c.steps) * c.count * (2 * t.sym + t.full) > INT32_MAX / 2) return DDP_ERR_UNSUPPORTED;
     p.m = l.m;
     p.n = l.n;
@@ -950,6 +996,8 @@ int run_steps(const Call& c, const Layout& l, const Results& r) {
     p.np = l.np;
     p.count = c.count;
     p.steps = c.steps;
+    p.groups = t.groups;
+    std::copy(t.order, t.order + t.groups * 3 * c.steps, p.order);
     p.tm = t.tm;
     p.tn = t.tn;
     p.sym = t.sym;
