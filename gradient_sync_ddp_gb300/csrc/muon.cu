@@ -907,10 +907,12 @@ Layout layout_of(int count, int rows, int cols) {
 }
 
 // Tiles by pairs of CTAs or by single ones, and the order of the groups' products, with the time that it takes in
-// clocks from what was measured: a block of 64 of K takes a pair's 256 x 256 tile 620, a CTA's 128 x 128 one 660, and 400
-// where few run (its operands come at twice the bytes per product); a tile's epilogue 13000 and 8000; from a tile's last
-// product to the first one of a tile that waits for it 16000 and 11000.  Of the groups' next products the one that
-// can begin first comes next: 12 x 768 x 2304 took 395 us with all matrices in step.
+// clocks from what was measured: a block of 64 of K takes a pair's 256 x 256 tile 620, a CTA's 128 x 128 one 520, 420 for
+// a matrix alone, 380 where few run (its operands come at twice the bytes per product); a tile's epilogue 13000 and
+// 8000; from a tile's last product to the first one of a tile that waits for it 16000 and 11000.  Of the groups' next
+// products the one that can begin first comes next (12 x 768 x 2304 took 395 us with all matrices in step, 382 so).
+// Pairs and CTAs measured: 4096 x 4096 911 and 1191 us, 48 x 768 x 768 585 and 668, 12 x 768 x 2304 382 and 388; 2560 x 2560
+// 391 and 372, 12 x 768 x 768 230 and 191, 1000 x 2048 231 and 161, 128 x 128 99 and 82.
 struct Tiling {
     bool pair;
     int tm, tn, sym, full, ctas, groups;
@@ -934,7 +936,7 @@ double lay_out(Tiling& t, bool pair, int count, int steps, const Layout& l, int 
         const int mode = phase[g] % 3;
         const int64_t tiles = static_cast<int64_t>((g + 1) * count / t.groups - g * count / t.groups) * (mode == kApply ? t.full : t.sym);
         const double waves = static_cast<double>(tiles) / at;
-        const double product = static_cast<double>((mode == kGram ? l.np : l.mp) / kBlockK) * (pair ? 620 : waves > 0.5 || t.groups > 1 ? 660 : 400);
+        const double product = static_cast<double>((mode == kGram ? l.np : l.mp) / kBlockK) * (pair ? 620 : t.groups > 1 ? 520 : waves > 0.5 ? 420 : 380);
         const double each = std::max(product, pair ? 13000.0 : 8000.0), start = std::max(pool, ready[g]);
         pool = start + each * (t.groups > 1 ? waves : std::ceil(waves) - 1.0);
         ready[g] = pool + product + (pair ? 16000.0 : 11000.0);
