@@ -947,7 +947,8 @@ double lay_out(Tiling& t, bool pair, int count, int steps, const Layout& l, int 
 }
 Tiling tiling(int count, int steps, const Layout& l, int sms) {
     Tiling two, one;
-    return lay_out(two, true, count, steps, l, sms) <= lay_out(one, false, count, steps, l, sms) ? two : one;
+    const double single = lay_out(one, false, count, steps, l, sms);
+    return sms >= 2 && lay_out(two, true, count, steps, l, sms) <= single ? two : one;
 }
 
 struct Call {
