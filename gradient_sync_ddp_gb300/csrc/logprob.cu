@@ -35,6 +35,8 @@ constexpr int kThr = kVocabThreads, kWarps = kThr / 32;
 constexpr int kMaxTop = DDP_LOGPROB_MAX_TOP;
 constexpr int kHits = 512;           // vectors that hold the largest entries
 constexpr int kCands = 1024;         // entries collected
+constexpr int kTaken = 4;            // up to this rank within a warp
+constexpr int kShortRow = 32768;     // bytes
 constexpr int kCount = 256;          // up to this many entries ranks are counted at once
 constexpr float kRaise = 8.0f;       // how far a thread's x may lie above its reference
 constexpr float kFarRef = 4096.0f;   // of the reference times log2(e)/τ: beyond, its spacing is felt: differences first
@@ -163,8 +165,22 @@ struct TopShared {
 // warps are there; −infinity where they are too few.  A barrier lies between the two calls.
 __device__ __forceinline__ int bound_rank(int k, int warps) { return warps > 0 ? (k + warps - 1) / warps : 33; }
 __device__ __forceinline__ void bound_begin(float mine, int k, int warps, uint32_t* sh) {
-    const uint32_t s = warp_sort(order_of(mine));
-    if (static_cast<int>(threadIdx.x & 31) == bound_rank(k, warps) - 1) sh[threadIdx.x >> 5] = s;
+    const int r = bound_rank(k, warps);
+    uint32_t s = order_of(mine);
+    if (r > kTaken) {
+        s = warp_sort(s);
+        if (static_cast<int>(threadIdx.x & 31) == r - 1) sh[threadIdx.x >> 5] = s;
+        return;
+    }
+    // a few are taken one after another, in fewer steps than a sort: a lane's own
+    // is at least 2^23 − 1 (-infinity), so that 0 is below all
+    uint32_t m = 0;
+    for (int i = 0; i < r; ++i) {
+        m = __reduce_max_sync(0xffffffffu, s);
+        const uint32_t who = __ballot_sync(0xffffffffu, s == m);
+        if (static_cast<int>(threadIdx.x & 31) == __ffs(who) - 1) s = 0;
+    }
+    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = m;
 }
 __device__ __forceinline__ float bound_end(int k, int warps, const uint32_t* sh) {
     if (bound_rank(k, warps) > 32) return -INFINITY;
@@ -295,8 +311,13 @@ __device__ __forceinline__ uint64_t cluster_read64(const uint64_t* p, uint32_t r
     return v;
 }
 
-template <bool BF16, bool TOP>
-__global__ void __launch_bounds__(kThr, 4) logprob_kernel(const __grid_constant__ ForwardParams a) {
+// MANY, for short rows of more tokens than four CTAs per SM take at once: six CTAs per SM with three vectors in flight per
+// thread instead of four with six.  What follows the pass over a row is steps that wait for one another, of which
+// more CTAs overlap more, at the price of spills (40 registers).  With 64 entries 16384 x 4000 bf16 185 us against 203, 16384
+// x 8000 fp32 216 against 243; long rows 8192 x 50257 bf16 209 against 211, 4096 x 50257 fp32 203 against 174, 512 x 160000
+// bf16 60 against 49.
+template <bool BF16, bool TOP, bool MANY>
+__global__ void __launch_bounds__(kThr, MANY ? 6 : 4) logprob_kernel(const __grid_constant__ ForwardParams a) {
     constexpr int VEC = BF16 ? 8 : 4, ES = BF16 ? 2 : 4;
     __shared__ alignas(16) unsigned char raw[TOP ? sizeof(TopShared) : 16];
     __shared__ float2 sh[2][kWarps];
@@ -330,7 +351,7 @@ __global__ void __launch_bounds__(kThr, 4) logprob_kernel(const __grid_constant_
     float limit = -INFINITY;                             // of a maximum that needs no new reference
     float most = -INFINITY, second = -INFINITY;          // of the thread's vectors
     int most_at = -1;
-    each_vector<BF16, TOP>(s, [&](int i, const uint4& v) {
+    each_vector<BF16, TOP, MANY ? 3 : 6>(s, [&](int i, const uint4& v) {
         const float vm = vec_max<BF16>(v);
         if (!(vm <= limit)) {                            // NaN too
             w.raise(vm, c);
@@ -686,8 +707,10 @@ extern "C" int token_logprobs_forward(const void* logits, int64_t ldz, int32_t d
     const bool top = k > 0 && (top_index != nullptr || top_logprob != nullptr);
     const ForwardParams p{logits, target, logprob, entropy, lse, top_index, top_logprob, ldz, ldti, ldtl, T, V, k,
                           temperature, c, target_bits == 64, index_bits == 64, cluster};
-    void (*kernel)(ForwardParams) = dtype == DDP_BF16 ? (top ? logprob_kernel<true, true> : logprob_kernel<true, false>)
-                                                      : (top ? logprob_kernel<false, true> : logprob_kernel<false, false>);
+    const bool many = static_cast<int64_t>(V) * es <= kShortRow && T > 4ll * d.sm_count;
+    void (*kernel)(ForwardParams) =
+        dtype == DDP_BF16 ? (!top ? logprob_kernel<true, false, false> : many ? logprob_kernel<true, true, true> : logprob_kernel<true, true, false>)
+                          : (!top ? logprob_kernel<false, false, false> : many ? logprob_kernel<false, true, true> : logprob_kernel<false, true, false>);
     return launch_smem(kernel, static_cast<unsigned>(T * cluster), kThr, 0, static_cast<cudaStream_t>(stream), p,
                        static_cast<unsigned>(cluster));
 }

@@ -68,9 +68,8 @@ __device__ __forceinline__ int edge(const Slice& s, int e) {
 }
 
 // body(vector index, values) for every 16-byte vector of the slice that is this thread's, U loads in flight.
-template <bool BF16, bool KEEP, class F>
+template <bool BF16, bool KEEP, int U = 6, class F>
 __device__ __forceinline__ void each_vector(const Slice& s, F body) {
-    constexpr int U = 6;
     const char* zv = s.base + static_cast<int64_t>(s.v0 + s.lead) * (BF16 ? 2 : 4);
     int i = threadIdx.x;
     for (; i + (U - 1) * kVocabThreads < s.nvec; i += U * kVocabThreads) {
