@@ -24,6 +24,14 @@
 // that reach it are collected and each one's rank among them is counted.  Where the list
 // runs over (long ties, a short row), and in rows with NaN, the k-th largest is found
 // by digits of (value, index), as whole numbers of 64 bits.
+// Bound by HBM without entries: 8192 x 50257 bf16 135 us, 6.1 TB/s (0.90 of a plain
+// copy's rate); with them by steps that wait for one another (a warp's sort, barriers,
+// L2's latency for the vectors read again), during which the SM's other three CTAs
+// stream: 181 us with one entry, 212 with 64, 285 with 128.  A single token of 50257
+// fp32 logits takes 11 us, a launch and the chain of those steps.
+//
+// Backward: one launch, z read and dz written once; 8192 x 50257 bf16 250 us, 6.6 TB/s
+// (0.97), 517 x 32003 fp32 22.7 us, 5.8 TB/s (0.86).
 #include <cstdint>
 
 #include "vocab.cuh"

@@ -847,7 +847,8 @@ int token_logprobs_forward(const void* logits, int64_t ldz, int32_t dtype, const
  *                        target outside [0, V) takes no dlogprob
  *   dlogits              device [T, V], dtype; may be logits itself
  * A token that takes neither (0 in both) has gradient 0, whatever its logits
- * hold, and so has one whose lse is -infinity.
+ * hold, and so has one whose lse is -infinity.  temperature as in the forward
+ * pass, and the same.
  */
 int token_logprobs_backward(const void* logits, int64_t ldz, int32_t dtype, const void* target, int32_t target_bits,
                             int64_t T, int32_t V, float temperature, const float* lse, const float* entropy,

@@ -94,8 +94,8 @@ def test_forward(g, T, V, k, dt, tau):
     check(z, target, tau, plain, 0)
 
 
-@pytest.mark.parametrize("T", [2, 320])
-@pytest.mark.parametrize("V", [700, 9001, 40000])
+@pytest.mark.parametrize("T", [2, 320, 700])
+@pytest.mark.parametrize("V", [700, 8003, 9001, 40000])
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 def test_masks_and_shapes_of_rows(g, T, V, dt):
     """Every row of another kind; what no list holds goes by digits."""
@@ -129,10 +129,10 @@ def test_masks_and_shapes_of_rows(g, T, V, dt):
             check(x[:len(kinds)], target[:len(kinds)], 1.0, tuple(o[:len(kinds)] for o in out), k)
 
 
-@pytest.mark.parametrize("T", [3, 320])
+@pytest.mark.parametrize("T,V", [(3, 9001), (320, 9001), (700, 9001), (700, 8003)])
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
-def test_nan_and_infinity(g, T, dt):
-    V, k = 9001, 6
+def test_nan_and_infinity(g, T, V, dt):
+    k = 6
     z = rand((T, V), 5, 2.0, DT[dt])
     z[0, [17, 8000]] = float("nan")
     z[0, 4] = float("inf")
@@ -235,8 +235,8 @@ def test_backward_against_differences(g, V):
         assert torch.all((num - got).abs() <= tol)
 
 
-@pytest.mark.parametrize("T", [5, 310])
-@pytest.mark.parametrize("V", [515, 8195])
+@pytest.mark.parametrize("T", [5, 310, 700])
+@pytest.mark.parametrize("V", [515, 8003, 8195])
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 def test_strides_and_offsets(g, T, V, dt):
     """Column slices at odd offsets of wider buffers; what lies beside them stays."""
