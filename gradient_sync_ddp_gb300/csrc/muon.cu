@@ -30,7 +30,7 @@
 //                  of K a stage, 128-byte swizzle, five stages); an issuer of tcgen05.mma; sixteen
 //                  epilogue warps.  Two accumulators in TMEM, so that a tile's epilogue
 //                  runs under the next one's products.  A symmetric matrix's tiles are
-//                  stored a second time, transposed in shared memory, below the diagonal: read by
+//                  stored a second time, transposed, below the diagonal: read by
 //                  columns instead (the MMA's other operand order) a block of 64 of K took 880
 //                  clocks in place of 520.  X is read so in the last product (610), for a
 //                  transposed copy of it would not fit L2 beside the rest.
@@ -459,7 +459,6 @@ __device__ __forceinline__ void copy16(uint32_t to, const void* p) {   // by L2:
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(p) : "memory");
 }
 __device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-__device__ __forceinline__ void sts2(uint32_t a, uint32_t v) { asm volatile("st.shared.u16 [%0], %1;" ::"r"(a), "h"(static_cast<unsigned short>(v)) : "memory"); }
 __device__ __forceinline__ uint4 lds16(uint32_t a) {
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
@@ -733,7 +732,7 @@ __global__ void __launch_bounds__(kStepThreads, 1) step_kernel(const __grid_cons
             const int64_t rows8 = 8ll * ld;
             const uint32_t acc = d.i * SIDE + (static_cast<uint32_t>(rows) << 16);
             // Rows across lanes in global memory, a row per lane in TMEM: through shared memory from one to the other, X and
-            // A by `st`, the rest (or the tile below the diagonal) by `st2`.
+            // A by `st`, the rest by `st2`.
             auto fetch = [&](int unit) {
                 const int col0 = t.j * SIDE + 32 * unit;
                 if (!adds || !in || col0 >= ld) return;
@@ -824,11 +823,16 @@ __global__ void __launch_bounds__(kStepThreads, 1) step_kernel(const __grid_cons
                         for (int e = 0; e < 8; ++e) x[e] = half_bits2(fma2(half_pair2(x[e]), minus, v[e]));
 #pragma unroll
                         for (int c = 0; c < 2; ++c) sts16(piece(st2, lane, 2 * g + c), make_uint4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]));
-                    } else if (below) {                  // transposed: the lane's row is a column of it
+                    } else if (below) {
+                        // Transposed: a column's 32 rows lie side by side.  Two rows in a word, an even column's with the
+                        // even lanes: 12 x 768 x 768 178 us; an element a lane 181, rows of 64 bytes turned in shared
+                        // memory, whose accesses it was bound by, 186.
+                        const int odd = lane & 1;
+                        __half* o2 = (t.mode == kGram ? p.a : p.b) + (static_cast<int64_t>(t.b) * p.mp + col0 + 16 * g + odd) * ld + row0 + lane - odd;
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
-                            sts2(piece(st2, 16 * g + 2 * e, lane >> 3) + 2 * (lane & 7), x[e]);
-                            sts2(piece(st2, 16 * g + 2 * e + 1, lane >> 3) + 2 * (lane & 7), x[e] >> 16);
+                            const uint32_t y = __shfl_xor_sync(0xffffffffu, x[e], 1);
+                            *reinterpret_cast<uint32_t*>(o2 + 2 * e * static_cast<int64_t>(ld)) = odd ? __byte_perm(y, x[e], 0x7632) : __byte_perm(x[e], y, 0x5410);
                         }
                     }
                 }
@@ -836,11 +840,9 @@ __global__ void __launch_bounds__(kStepThreads, 1) step_kernel(const __grid_cons
                 if (here && !last) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4*>(o_hi + k * rows8 + col0) = lds16(piece(st, 8 * k + lr, lc));
-                    if (o_lo || below) {
-                        __half* o2 = o_lo ? p.lo + base + col0
-                                          : (t.mode == kGram ? p.a : p.b) + (static_cast<int64_t>(t.b) * p.mp + col0 + lr) * ld + row0 + 8 * lc;
+                    if (o_lo) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4*>(o2 + k * rows8) = lds16(piece(st2, 8 * k + lr, lc));
+                        for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4*>(p.lo + base + k * rows8 + col0) = lds16(piece(st2, 8 * k + lr, lc));
                     }
                 }
                 __syncwarp();
