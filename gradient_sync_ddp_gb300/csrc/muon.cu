@@ -22,7 +22,7 @@
 // the GPU.  A and B are symmetric: only tiles on and above the diagonal are
 // computed, 3mn·m + m³ operations per step instead of 4mn·m + 2m³.
 //   update_kernel / square_kernel   average, momentum, U; parts of ‖U‖²
-//   split_kernel   ‖U‖ from its parts, U to fp16 (and the rest), transposed where tall
+//   split_rows_kernel / split_kernel   ‖U‖ from its parts, U to fp16 (and the rest), transposed where tall
 //   step_kernel    all products of all steps, persistent: a pair of CTAs per tile of
 //                  256 x 256, or a CTA per tile of 128 x 128 where pairs would leave
 //                  SMs without work.  Roles by warp: a scheduler that takes the next tile's number and
@@ -36,10 +36,12 @@
 //                  transposed copy of it would not fit L2 beside the rest.
 // Bound by the tensor cores where tiles are many, by the way from one product to the
 // next where they are few.  Five steps (of 1924 TFLOP/s, what a plain bf16 product is
-// measured at): 4096 x 4096 1.0 ms (0.71; 911 us of it step_kernel), 12 x 768 x 768 188 us
-// (0.30: 15 products, each 11 us from its last block of K to the first one of a tile
-// that waits for it), with the average of 8 bf16 replicas and the momentum 12 x 768 x 2304
-// 484 us (0.50 of operations and bytes), of 8 fp32 ones 1000 x 2048 179 us.
+// measured at): 4096 x 4096 990 us (0.72), 12 x 768 x 768 180 us (0.31: 15 products, each of 12
+// blocks of K, 420 clocks one, then 7000 to 8000 for the epilogue until its last warp has told
+// that the tile is there, and 3000 until the first block of a tile that waits for it), with the
+// average of 8 bf16 replicas and the momentum 12 x 768 x 2304 481 us (0.50 of operations and
+// bytes), of 8 fp32 ones 1000 x 2048 174 us.  The epilogue is bound by the accesses to shared and
+// global memory that its 16 warps issue.
 // Tiles are taken in the order of their products by CTAs that already run, so that
 // what a tile waits for is always under way, however few CTAs the GPU has room for.
 // Every wait on a barrier is bounded; a tile whose wait ran out is written as NaN.
@@ -62,6 +64,7 @@ constexpr int kPad = 64;               // sides are padded to blocks of K
 constexpr int kParts = 1024;           // of a matrix's ‖U‖², at most
 constexpr int kPartElems = 2048;       // a part has at least so many elements
 constexpr int kMaxReplicas = 16;
+constexpr int kSplitVecs = 2;          // of eight columns, per thread
 
 // ---- average, momentum, sums of squares ------------------------------------
 
@@ -156,7 +159,7 @@ struct SplitParams {
     __half* lo;              // or NULL
     int64_t size;
     float eps;
-    int32_t rows, cols, parts, mp, np, tall, vec, listed;
+    int32_t rows, cols, parts, mp, np, tall, vec, listed;   // vec: rows of 16-byte vectors
 };
 
 __device__ __forceinline__ const void* matrix_of(const SplitParams& p, int b, bool bf16) {
@@ -191,7 +194,72 @@ __global__ void __launch_bounds__(kThreads) square_kernel(const __grid_constant_
     block_part(ss, part + blockIdx.y * kParts + blockIdx.x);
 }
 
-// A tile of 64 x 64 of X, read along the rows of the matrix it comes from.
+// The power of two that brings a matrix's entries to about 1, and none of them, at most the norm, past 32768; the first
+// CTA of a matrix leaves step_kernel what it begins with.
+__device__ __forceinline__ float matrix_scale(const SplitParams& p, int b, bool first, float* sh) {
+    float ss = 0.0f;
+    for (int i = threadIdx.x; i < p.parts; i += kThreads) ss += p.part[b * kParts + i];
+    const float norm = sqrtf(block_all<SumOp>(ss, sh));
+    float scale = 1.0f, alpha = __int_as_float(0x7fffffff);
+    if (norm < INFINITY) {
+        const float want = fminf(sqrtf(static_cast<float>(p.size)), 32768.0f) / norm;
+        scale = want < 0x1p126f ? exp2f(floorf(log2f(fmaxf(want, 0x1p-126f)))) : norm > 0.0f ? 0x1p126f : 1.0f;
+        alpha = norm > 0.0f ? 1.0f / (norm + p.eps) / scale : 0.0f;
+    }
+    if (first) {
+        if (threadIdx.x == 0) p.alpha[b] = alpha;
+        for (int i = b * kThreads + threadIdx.x; i < p.sync_ints; i += gridDim.z * kThreads) p.sync[i] = 0;
+    }
+    return scale;
+}
+// Eight values times the scale to fp16, and what that rounded off.
+__device__ __forceinline__ void store_split(const SplitParams& p, int64_t at, const float (&v)[8]) {
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const __half2 h = __floats2half2_rn(v[2 * q], v[2 * q + 1]);
+        const float2 f = __half22float2(h);
+        const __half2 l = __floats2half2_rn(v[2 * q] - f.x, v[2 * q + 1] - f.y);
+        hi[q] = *reinterpret_cast<const uint32_t*>(&h);
+        lo[q] = *reinterpret_cast<const uint32_t*>(&l);
+    }
+    *reinterpret_cast<uint4*>(p.hi + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    if (p.lo) *reinterpret_cast<uint4*>(p.lo + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+}
+
+// X from a matrix that is not tall and lies on 16 bytes: kSplitVecs times eight columns per thread, a wide load each.
+template <bool BF16>
+__global__ void __launch_bounds__(kThreads) split_rows_kernel(const __grid_constant__ SplitParams p) {
+    __shared__ float sh[32];
+    pdl_enter();
+    const int b = blockIdx.z, width = p.np / 8, all = p.mp * width;
+    const char* x = static_cast<const char*>(matrix_of(p, b, BF16));
+    constexpr int HALF = BF16 ? 8 : 4;                   // columns per load, of which a row has a whole number
+    float v[kSplitVecs][8];
+#pragma unroll
+    for (int k = 0; k < kSplitVecs; ++k) {
+        const int e = (blockIdx.x * kSplitVecs + k) * kThreads + threadIdx.x, r = e / width, c = 8 * (e - r * width);
+        const char* row = row_ptr<BF16>(static_cast<const void*>(x), r, p.ldx);
+#pragma unroll
+        for (int h = 0; h < 8; h += HALF) {
+            const bool in = r < p.rows && c + h < p.cols;
+            const uint4 w = in ? ld16<false>(row + static_cast<int64_t>(c + h) * (BF16 ? 2 : 4)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < HALF; ++i) v[k][h + i] = vec_elem<BF16>(w, i);
+        }
+    }
+    const float scale = matrix_scale(p, b, blockIdx.x == 0, sh);
+#pragma unroll
+    for (int k = 0; k < kSplitVecs; ++k) {
+        const int e = (blockIdx.x * kSplitVecs + k) * kThreads + threadIdx.x;
+        if (e >= all) break;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[k][i] *= scale;
+        store_split(p, (static_cast<int64_t>(b) * all + e) * 8, v[k]);
+    }
+}
+
+// Any matrix: a tile of 64 x 64 of X, read along the rows of the matrix it comes from.
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads) split_kernel(const __grid_constant__ SplitParams p) {
     __shared__ float tile[64][65];
@@ -207,20 +275,7 @@ __global__ void __launch_bounds__(kThreads) split_kernel(const __grid_constant__
         const int r = r0 + tr + 4 * k, c = c0 + tc;
         v[k] = r < p.rows && c < p.cols ? load_elem<BF16>(row_ptr<BF16>(static_cast<const void*>(x), r, p.ldx), c) : 0.0f;
     }
-    float ss = 0.0f;
-    for (int i = threadIdx.x; i < p.parts; i += kThreads) ss += p.part[b * kParts + i];
-    const float norm = sqrtf(block_all<SumOp>(ss, sh));
-    // the power of two that brings the entries to about 1, and none of them, at most the norm, past 32768
-    float scale = 1.0f, alpha = __int_as_float(0x7fffffff);
-    if (norm < INFINITY) {
-        const float want = fminf(sqrtf(static_cast<float>(p.size)), 32768.0f) / norm;
-        scale = want < 0x1p126f ? exp2f(floorf(log2f(fmaxf(want, 0x1p-126f)))) : norm > 0.0f ? 0x1p126f : 1.0f;
-        alpha = norm > 0.0f ? 1.0f / (norm + p.eps) / scale : 0.0f;
-    }
-    if (blockIdx.x == 0 && blockIdx.y == 0) {
-        if (threadIdx.x == 0) p.alpha[b] = alpha;
-        for (int i = b * kThreads + threadIdx.x; i < p.sync_ints; i += gridDim.z * kThreads) p.sync[i] = 0;
-    }
+    const float scale = matrix_scale(p, b, blockIdx.x == 0 && blockIdx.y == 0, sh);
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
         const float s = v[k] * scale;
@@ -231,19 +286,10 @@ __global__ void __launch_bounds__(kThreads) split_kernel(const __grid_constant__
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
         const int i = (threadIdx.x >> 3) + 32 * k, j = (threadIdx.x & 7) * 8;
-        uint32_t hi[4], lo[4];
+        float w[8];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const float s0 = tile[i][j + 2 * q], s1 = tile[i][j + 2 * q + 1];
-            const __half2 h = __floats2half2_rn(s0, s1);
-            const float2 f = __half22float2(h);
-            const __half2 l = __floats2half2_rn(s0 - f.x, s1 - f.y);
-            hi[q] = *reinterpret_cast<const uint32_t*>(&h);
-            lo[q] = *reinterpret_cast<const uint32_t*>(&l);
-        }
-        const int64_t at = (static_cast<int64_t>(b) * p.mp + i0 + i) * p.np + j0 + j;
-        *reinterpret_cast<uint4*>(p.hi + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        if (p.lo) *reinterpret_cast<uint4*>(p.lo + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        for (int e = 0; e < 8; ++e) w[e] = tile[i][j + e];
+        store_split(p, (static_cast<int64_t>(b) * p.mp + i0 + i) * p.np + j0 + j, w);
     }
 }
 
@@ -1042,6 +1088,12 @@ int split(const Call& c, const Layout& l, SplitParams& p, bool bf16) {
     p.mp = l.mp;
     p.np = l.np;
     p.tall = l.tall;
+    // 12 x 768 x 2304 fp32 371 us with all steps, 378 by tiles; few or small ones alike
+    if (p.vec && !l.tall) {
+        const int64_t chunks = static_cast<int64_t>(l.mp) * l.np / 8, per = kSplitVecs * kThreads;
+        return launch_pdl(bf16 ? split_rows_kernel<true> : split_rows_kernel<false>,
+                          dim3(static_cast<unsigned>((chunks + per - 1) / per), 1, static_cast<unsigned>(c.count)), kThreads, c.s, p);
+    }
     return launch_pdl(bf16 ? split_kernel<true> : split_kernel<false>,
                       dim3(static_cast<unsigned>(l.np / 64), static_cast<unsigned>(l.mp / 64), static_cast<unsigned>(c.count)), kThreads, c.s, p);
 }
@@ -1209,6 +1261,7 @@ extern "C" int ddp_bucket_allreduce_muon(const void* const* replicas, int32_t n_
         p.x[0] = u.u;
         p.ldx = cols;
         p.pitch = l.pitch;
+        p.vec = cols % 4 == 0;
         p.parts = used;
         if ((st = split(c, l, p, false)) != DDP_OK) return st;
         const Results r{kOutParam, cols, on4 && cols % 4 == 0, 1.0f - lr * weight_decay, lr * update_scale, out, param_bf16 ? out2 : nullptr};
