@@ -112,7 +112,10 @@ def check_backward(dy, h, mean, rstd, gamma, dh, dx, dgamma, dbeta):
         assert np.all(np.abs(f64(dbeta) - dbw) <= (rows + 8) * U * np.sum(np.abs(dyw), axis=0) + 1e-40)
 
 
-@pytest.mark.parametrize("rows,D", SHAPES + [(1300, 96), (2500, 16), (400, 9000)])
+MANY = [(8000, 64), (7500, 130), (7400, 200), (7400, 392), (7400, 515), (7400, 771), (7300, 1000), (7300, 1021)]   # rows after rows per warp
+
+
+@pytest.mark.parametrize("rows,D", SHAPES + [(1300, 96), (2500, 16), (400, 9000)] + MANY)
 @pytest.mark.parametrize("dt,dyt", [("bf16", "bf16"), ("f32", "f32"), ("f32", "bf16"), ("bf16", "f32")])
 def test_backward(g, rows, D, dt, dyt):
     h, dy, dh = rand((rows, D), 7, 2.0, DT[dt], 0.7), rand((rows, D), 8, 0.5, DT[dyt]), rand((rows, D), 9, 0.5, DT[dt])
@@ -135,6 +138,24 @@ def test_backward(g, rows, D, dt, dyt):
         g.layernorm_backward(dy, h, mean, rstd, gm, only, None, one, ws, dh=d)    # one of the two
         sync()
         assert torch.equal(only, dx) and torch.equal(one, dbeta)
+
+
+@pytest.mark.parametrize("D", [64, 255, 512, 768, 1024])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_backward_in_place_of_many_rows(g, D, dt):
+    """dx on dy, h or dh: the rows that are fetched ahead are still what they were."""
+    rows = 7400
+    h, dy, dh = (rand((rows, D), i, 1.0, DT[dt]) for i in (30, 31, 32))
+    mean, rstd, gamma = rand((rows,), 33, 0.1), 1 + rand((rows,), 34, 0.1).abs(), 1 + rand((D,), 35, 0.1)
+    ws = torch.empty(g.layernorm_backward_workspace_bytes(rows, D), dtype=torch.uint8, device="cuda")
+    want, dg, db = torch.empty_like(h), torch.empty(D, device="cuda"), torch.empty(D, device="cuda")
+    g.layernorm_backward(dy, h, mean, rstd, gamma, want, dg, db, ws, dh=dh)
+    for on in range(3):
+        t = [dy.clone(), h.clone(), dh.clone()]
+        dg2, db2 = torch.empty_like(dg), torch.empty_like(db)
+        g.layernorm_backward(t[0], t[1], mean, rstd, gamma, t[on], dg2, db2, ws, dh=t[2])
+        sync()
+        assert torch.equal(t[on], want) and torch.equal(dg2, dg) and torch.equal(db2, db), on
 
 
 @pytest.mark.parametrize("D", [96, 515])
