@@ -161,10 +161,15 @@ template <typename Params>
 int launch_smem(void (*kernel)(Params), unsigned grid, int block, size_t smem, cudaStream_t s, const Params& params,
                 unsigned cluster = 1) {
     cudaError_t e;
-    if (smem > 48 * 1024 - 1024 &&
-        (e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  static_cast<int>(smem))) != cudaSuccess)
-        return cuda_fail(e);
+    if (smem > 48 * 1024 - 1024) {
+        // always the most there is: a smaller call of the same kernel on another thread would take back what this one needs
+        cudaFuncAttributes f;
+        if ((e = cudaFuncGetAttributes(&f, reinterpret_cast<const void*>(kernel))) != cudaSuccess) return cuda_fail(e);
+        if (static_cast<size_t>(f.maxDynamicSharedSizeBytes) < smem &&
+            (e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      227 * 1024 - static_cast<int>(f.sharedSizeBytes))) != cudaSuccess)
+            return cuda_fail(e);
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(static_cast<unsigned>(block));

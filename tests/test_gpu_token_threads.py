@@ -83,3 +83,47 @@ def test_first_calls_of_six_threads():
     load_library()
     r = subprocess.run([sys.executable, "-c", PROGRAM, ROOT], capture_output=True, text=True, timeout=300, cwd=ROOT)
     assert r.returncode == 0 and r.stdout.strip() == "ok", r.stderr[-2000:]
+
+
+WIDTHS = """
+import sys, threading
+sys.path.insert(0, sys.argv[1])
+sys.setswitchinterval(1e-6)
+import torch
+import gradient_sync_ddp_gb300 as g
+torch.cuda.init()
+errors, gate, widths = [], threading.Barrier(6), [800, 1024, 904, 1000, 864, 960]
+f = lambda *s, **k: torch.randn(*s, device="cuda", **k)
+sets = [(f(400, D, dtype=torch.bfloat16), f(400, D, dtype=torch.bfloat16), f(400), f(400).abs(), f(D),
+         torch.empty(400, D, device="cuda", dtype=torch.bfloat16), f(D), f(D),
+         torch.empty(max(g.layernorm_backward_workspace_bytes(400, D), g.rmsnorm_backward_workspace_bytes(400, D)),
+                     device="cuda", dtype=torch.uint8)) for D in widths]
+torch.cuda.synchronize()
+
+def work(i):
+    dy, h, mean, rstd, gamma, dx, dg, db, ws = sets[i]
+    try:
+        with torch.cuda.stream(torch.cuda.Stream()):
+            gate.wait()
+            for _ in range(1500):
+                g.rmsnorm_backward(dy, h, rstd, gamma, dx, dg, ws)
+            g.layernorm_backward(dy, h, mean, rstd, gamma, dx, dg, db, ws)
+    except BaseException as e:
+        errors.append(repr(e))
+
+threads = [threading.Thread(target=work, args=(i,)) for i in range(6)]
+for t in threads:
+    t.start()
+for t in threads:
+    t.join()
+torch.cuda.synchronize()
+assert not errors, errors
+print("ok")
+"""
+
+
+def test_widths_of_one_kernel_at_once():
+    """Calls of one kernel that take different amounts of shared memory, at once: none lowers what another is allowed."""
+    load_library()
+    r = subprocess.run([sys.executable, "-c", WIDTHS, ROOT], capture_output=True, text=True, timeout=300, cwd=ROOT)
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stderr[-2000:]
